@@ -20,6 +20,9 @@ __all__ = [
     "qmm_grouped_gemm_swiglu", "qmm_moe_combine", "qmm_gemv_int8", "qmm_gemm_noalloc", "qmm_set_kernel", "qmm_get_kernel",
     "QMM_KERNEL_AUTO", "QMM_KERNEL_TILE", "QMM_KERNEL_TILE_UNSPLIT", "QMM_KERNEL_FEW_ROW",
     "QMM_KERNEL_GROUPED_MATMUL", "QMM_KERNEL_MULTI_ROW", "EXPORTS",
+    "qmm_fp8_quant", "qmm_fp8_gemm", "qmm_fp8_grouped_gemm", "qmm_fp8_grouped_gemm_swiglu",
+    "qmm_route_topk_workspace_bytes", "qmm_route_topk", "qmm_moe_gather", "qmm_norm_residual",
+    "QMM_BF16", "QMM_F32", "QMM_SCORE_SOFTMAX", "QMM_SCORE_SIGMOID", "QMM_GROUP_MAX", "QMM_GROUP_TOP2",
 ]
 
 QMM_AFFINE4_G64 = 1
@@ -32,6 +35,13 @@ QMM_KERNEL_FEW_ROW = 3
 QMM_KERNEL_GROUPED_MATMUL = 4
 QMM_KERNEL_MULTI_ROW = 5
 
+QMM_BF16 = 1
+QMM_F32 = 2
+QMM_SCORE_SOFTMAX = 0
+QMM_SCORE_SIGMOID = 1
+QMM_GROUP_MAX = 0
+QMM_GROUP_TOP2 = 1
+
 STATUS = {0: "QMM_OK", 1: "QMM_E_ARG", 2: "QMM_E_SHAPE", 3: "QMM_E_ALIGN", 4: "QMM_E_UNSUPPORTED",
           5: "QMM_E_WORKSPACE", 6: "QMM_E_HIP", 7: "QMM_E_LAYOUT", 8: "QMM_E_VALUE"}
 
@@ -39,7 +49,9 @@ EXPORTS = ("qmm_packed_bytes", "qmm_workspace_bytes", "qmm_pack", "qmm_unpack", 
            "qmm_gemm", "qmm_grouped_gemm", "qmm_status_string", "qmm_last_error",
            "qmm_layout_version", "qmm_profile_next", "qmm_stream_read", "qmm_route",
            "qmm_grouped_gemm_swiglu", "qmm_moe_combine", "qmm_gemv_int8", "qmm_gemm_noalloc",
-           "qmm_set_kernel", "qmm_get_kernel")
+           "qmm_set_kernel", "qmm_get_kernel", "qmm_fp8_quant", "qmm_fp8_gemm", "qmm_fp8_grouped_gemm",
+           "qmm_fp8_grouped_gemm_swiglu", "qmm_route_topk_workspace_bytes", "qmm_route_topk",
+           "qmm_moe_gather", "qmm_norm_residual")
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _lib = None
@@ -73,6 +85,7 @@ def load():
                           "`python -m bit_weight_quantized_amd.build` (hipcc, gfx950)")
     lib = ctypes.CDLL(path)
     i64, i32, sz, vp = ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t, ctypes.c_void_p
+    f32 = ctypes.c_float
     sig = {
         "qmm_packed_bytes": (sz, [ctypes.c_int, i64, i64]),
         "qmm_workspace_bytes": (sz, [ctypes.c_int, i64, i64, i64]),
@@ -95,6 +108,17 @@ def load():
         "qmm_gemm_noalloc": (ctypes.c_int, [ctypes.c_int, vp, i64, i64, i64, vp, vp, vp]),
         "qmm_set_kernel": (ctypes.c_int, [ctypes.c_int]),
         "qmm_get_kernel": (ctypes.c_int, []),
+        "qmm_fp8_quant": (ctypes.c_int, [vp, i64, i64, i64, vp, vp, vp]),
+        "qmm_fp8_gemm": (ctypes.c_int, [vp, vp, i64, i64, i64, vp, vp, vp, i64, vp]),
+        "qmm_fp8_grouped_gemm": (ctypes.c_int, [vp, vp, i32, i64, i64, vp, vp, i64, vp, vp, vp, i32, i32, i32, vp, vp]),
+        "qmm_fp8_grouped_gemm_swiglu": (ctypes.c_int, [vp, vp, i32, i64, i64, vp, vp, i64, vp, vp, vp, i32, i32, i32,
+                                                       vp, vp]),
+        "qmm_route_topk_workspace_bytes": (sz, [i64, i32]),
+        "qmm_route_topk": (ctypes.c_int, [vp, ctypes.c_int, i64, i32, i64, ctypes.c_int, vp, i32, i32, ctypes.c_int,
+                                          i32, i32, f32, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+        "qmm_moe_gather": (ctypes.c_int, [vp, i32, i64, i64, i32, vp, vp, vp, vp, vp]),
+        "qmm_norm_residual": (ctypes.c_int, [i64, i64, vp, i64, vp, vp, i64, i64, vp, ctypes.c_int, i64, f32, vp, i64,
+                                             vp, f32, f32, vp, i64, vp, vp, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -236,3 +260,51 @@ def qmm_moe_combine(o, m_total, d, t, k, topk, weights, n_experts, seg_offsets, 
 
 def qmm_gemv_int8(fmt, packed, n, d, x, y, stream=None):
     _check(load().qmm_gemv_int8(fmt, _ptr(packed), n, d, _ptr(x), _ptr(y), _stream(stream)), "qmm_gemv_int8")
+
+
+def qmm_fp8_quant(x, t, d, ldx, q, scales, stream=None):
+    _check(load().qmm_fp8_quant(_ptr(x), t, d, ldx, _ptr(q), _ptr(scales), _stream(stream)), "qmm_fp8_quant")
+
+
+def qmm_fp8_gemm(w, w_scales, t, n, d, x, x_scales, y, ldy, stream=None):
+    _check(load().qmm_fp8_gemm(_ptr(w), _ptr(w_scales), t, n, d, _ptr(x), _ptr(x_scales), _ptr(y), ldy,
+                               _stream(stream)), "qmm_fp8_gemm")
+
+
+def qmm_fp8_grouped_gemm(w_stack, w_scales, n_experts, n, d, x, x_scales, t_x, row_index, seg_expert,
+                         seg_offsets, n_seg, m_total, max_seg_rows, y, stream=None):
+    _check(load().qmm_fp8_grouped_gemm(_ptr(w_stack), _ptr(w_scales), n_experts, n, d, _ptr(x), _ptr(x_scales), t_x,
+                                       _ptr(row_index), _ptr(seg_expert), _ptr(seg_offsets), n_seg, m_total,
+                                       max_seg_rows, _ptr(y), _stream(stream)), "qmm_fp8_grouped_gemm")
+
+
+def qmm_fp8_grouped_gemm_swiglu(w_stack, w_scales, n_experts, n, d, x, x_scales, t_x, row_index, seg_expert,
+                                seg_offsets, n_seg, m_total, max_seg_rows, h, stream=None):
+    _check(load().qmm_fp8_grouped_gemm_swiglu(_ptr(w_stack), _ptr(w_scales), n_experts, n, d, _ptr(x),
+                                              _ptr(x_scales), t_x, _ptr(row_index), _ptr(seg_expert),
+                                              _ptr(seg_offsets), n_seg, m_total, max_seg_rows, _ptr(h),
+                                              _stream(stream)), "qmm_fp8_grouped_gemm_swiglu")
+
+
+def qmm_route_topk_workspace_bytes(t: int, n_experts: int) -> int:
+    return int(load().qmm_route_topk_workspace_bytes(t, n_experts))
+
+
+def qmm_route_topk(logits, dtype, t, n_experts, ld, score, bias, n_groups, keep_groups, group_score, k, renorm, scale,
+                   topk, weights, seg_expert, seg_offsets, row_index, slot_row, ws=None, stream=None):
+    _check(load().qmm_route_topk(_ptr(logits), dtype, t, n_experts, ld, score, _ptr(bias), n_groups, keep_groups,
+                                 group_score, k, int(renorm), scale, _ptr(topk), _ptr(weights), _ptr(seg_expert),
+                                 _ptr(seg_offsets), _ptr(row_index), _ptr(slot_row), _ptr(ws), _nbytes(ws),
+                                 _stream(stream)), "qmm_route_topk")
+
+
+def qmm_moe_gather(o, m_total, d, t, k, slot_row, weights, shared, out, stream=None):
+    _check(load().qmm_moe_gather(_ptr(o), m_total, d, t, k, _ptr(slot_row), _ptr(weights), _ptr(shared), _ptr(out),
+                                 _stream(stream)), "qmm_moe_gather")
+
+
+def qmm_norm_residual(t, d, o, ldo, post_w, gate, ldg, gate_rows, r, r_type, ldr, res_scale, r_out, ldr_out, pre_w,
+                      w_offset, eps, h, ldh, q, q_scales, stream=None):
+    _check(load().qmm_norm_residual(t, d, _ptr(o), ldo, _ptr(post_w), _ptr(gate), ldg, gate_rows, _ptr(r), r_type,
+                                    ldr, res_scale, _ptr(r_out), ldr_out, _ptr(pre_w), w_offset, eps, _ptr(h), ldh,
+                                    _ptr(q), _ptr(q_scales), _stream(stream)), "qmm_norm_residual")

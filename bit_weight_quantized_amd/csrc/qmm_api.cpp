@@ -130,6 +130,9 @@ qmm::ProfileEvents qmm::take_profile_events() {
   return pe;
 }
 
+qmm_status qmm::api_fail(qmm_status s, const char* what) { return fail(s, what); }
+qmm_status qmm::api_hip_fail(int err, const char* where) { return hip_fail(err, where); }
+
 extern "C" {
 
 qmm_status qmm_profile_next(void* start_event, void* stop_event) {

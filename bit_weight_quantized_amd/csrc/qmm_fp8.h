@@ -1,0 +1,114 @@
+// Block-scaled e4m3 path: launch arguments, limits and kernel choice shared by
+// the entry points (qmm_fp8_api.cpp) and the kernels.
+#pragma once
+
+#include <stdint.h>
+
+#include "qmm_internal.h"
+
+namespace qmm {
+
+constexpr int kFp8Block = 128;   // codes that share one scale along the reduction axis
+inline int fp8_blocks(int64_t d) { return int((d + kFp8Block - 1) / kFp8Block); }
+
+struct Fp8QuantArgs {
+  const uint16_t* x;   // [t][ldx] bf16
+  int64_t t, ldx;
+  int d;
+  uint8_t* q;          // [t][d]
+  float* scales;       // [t][blocks]
+};
+int launch_fp8_quant(const Fp8QuantArgs& a, void* stream);
+
+// One product Y = X·Wᵀ, or one for each segment of grouped rows.
+struct Fp8GemmArgs {
+  const uint8_t* w;      // [n][d], or [n_experts][n][d]
+  const float* ws;       // [scale rows][blocks] of each matrix
+  const uint8_t* x;      // [t][d] (grouped: [t_x][d])
+  const float* xs;       // [t][blocks]
+  uint16_t* y;           // [t][ldy] (grouped: [m_total][n], or [m_total][n/2] with the activation)
+  int64_t t, ldy;
+  int n, d;
+  // grouped only (n_seg > 0)
+  int64_t t_x;
+  const int32_t* row_index;
+  const int32_t* seg_expert;
+  const int32_t* seg_offsets;
+  int n_experts, n_seg, m_total, max_seg_rows;
+  bool glu;              // gate rows [0, n/2), up rows [n/2, n): y = silu(gate)·up
+};
+int launch_fp8_rows(const Fp8GemmArgs& a, void* stream);
+
+struct TopkArgs {
+  const void* logits;   // [t][ld], bf16 or fp32
+  bool bf16;
+  int64_t t, ld;
+  int ne;
+  bool sigmoid;
+  const float* bias;    // [ne] or NULL
+  int groups, keep;
+  bool top2;
+  int k;
+  bool renorm;
+  float scale;
+  int32_t* topk;        // [t][k]
+  float* weights;       // [t][k]
+  int32_t* seg_expert;  // [ne]
+  int32_t* seg_offsets; // [ne + 1]
+  int32_t* row_index;   // [t·k]
+  int32_t* slot_row;    // [t][k]
+  int32_t* ws;          // counts [chunks][ne], or NULL for one chunk
+};
+// Tokens of one workgroup: 16 waves, up to 8 tokens each, and no more than 128
+// chunks (the second kernel adds every chunk's counts up itself).
+constexpr int kTopkWaves = 16;
+constexpr int kTopkChunk = 128;
+constexpr int64_t kTopkMaxChunks = 128;
+inline int64_t topk_chunk(int64_t t) {
+  if (t <= kTopkChunk) return kTopkChunk;
+  int64_t c = 2 * kTopkWaves;
+  while (c < kTopkChunk && (t + c - 1) / c > kTopkMaxChunks) c *= 2;
+  if ((t + c - 1) / c > kTopkMaxChunks) c = round_up((t + kTopkMaxChunks - 1) / kTopkMaxChunks, kTopkChunk);
+  return c;
+}
+inline size_t topk_ws_bytes(int64_t t, int ne) {
+  const int64_t c = topk_chunk(t);
+  return t <= c ? 0 : size_t((t + c - 1) / c) * size_t(ne) * 4;
+}
+int launch_topk(const TopkArgs& a, void* stream);
+
+struct GatherArgs {
+  const uint16_t* o;         // [m_total][d]
+  int m_total, d, k;
+  int64_t t;
+  const int32_t* slot_row;   // [t][k]
+  const float* weights;      // [t][k]
+  const uint16_t* shared;    // [t][d] or NULL
+  uint16_t* out;             // [t][d]
+};
+int launch_gather(const GatherArgs& a, void* stream);
+
+struct NormArgs {
+  int64_t t;
+  int d;
+  const uint16_t* o;        // [t][ldo] or NULL
+  int64_t ldo;
+  const uint16_t* post_w;   // [d] or NULL
+  const uint16_t* gate;     // [ceil(t / gate_rows)][ldg] or NULL
+  int64_t ldg, gate_rows;
+  const void* r;            // [t][ldr], bf16 or fp32
+  bool r_f32;
+  int64_t ldr;
+  float res_scale;
+  void* r_out;              // [t][ldr_out], type of r, or NULL
+  int64_t ldr_out;
+  const uint16_t* pre_w;    // [d], or NULL where no h, q are asked for
+  float w_offset, eps;
+  uint16_t* h;              // [t][ldh] or NULL
+  int64_t ldh;
+  uint8_t* q;               // [t][d] or NULL
+  float* q_scales;          // [t][blocks]
+};
+int launch_norm_residual(const NormArgs& a, void* stream);
+
+}  // namespace qmm

@@ -1,0 +1,62 @@
+// bf16 rows -> e4m3 codes with one fp32 scale for each block of 128.
+//
+//   m = max(max_b |x|, 2^-96);  scale = m / 448;  q = e4m3(x·(448 / m))
+//
+// Bound by memory: 2 bytes read and 1 + 4/128 written for each element.  A
+// lane takes 16 elements (two 16-byte loads, one 16-byte store), so a block is
+// 8 lanes and its maximum three DPP steps.
+#include <hip/hip_runtime.h>
+
+#include "qmm_fp8.h"
+#include "qmm_fp8_device.h"
+#include "qmm_launch.h"
+
+namespace qmm {
+namespace {
+
+__global__ __launch_bounds__(256) void fp8_quant_kernel(const uint16_t* __restrict__ x, int64_t ldx, int d,
+                                                        uint32_t nb, int64_t total, uint8_t* __restrict__ q,
+                                                        float* __restrict__ scales) {
+  // block `id` of the [t][nb] blocks, lane `c` of its 8
+  const int64_t id = (int64_t(blockIdx.x) * 256 + threadIdx.x) >> 3;
+  if (id >= total) return;   // whole groups of 8 lanes
+  const int c = threadIdx.x & 7;
+  const int64_t row = id / nb;
+  const int b = int(id - row * nb);
+  const int k = kFp8Block * b + 16 * c;
+  u32x4_t v[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+  if (k < d) {
+    v[0] = load16(x + row * ldx + k);
+    v[1] = load16(x + row * ldx + k + 8);
+  }
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t u = v[i >> 2][i & 3];
+    m = umax(m, umax((u << 16) & 0x7FFFFFFFu, u & 0x7FFF0000u));
+  }
+  const BlockScale s = block_scale(group_umax<8>(m));
+  if (k < d) {
+    u32x4_t o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t u0 = v[i >> 1][2 * (i & 1)], u1 = v[i >> 1][2 * (i & 1) + 1];
+      o[i] = pack_e4m3x4(bf16_lo(u0) * s.factor, bf16_hi(u0) * s.factor, bf16_lo(u1) * s.factor,
+                         bf16_hi(u1) * s.factor);
+    }
+    *reinterpret_cast<u32x4_t*>(q + row * d + k) = o;
+  }
+  if (c == 0) scales[id] = s.scale;
+}
+
+}  // namespace
+
+int launch_fp8_quant(const Fp8QuantArgs& a, void* stream) {
+  const uint32_t nb = uint32_t(fp8_blocks(a.d));
+  const int64_t total = a.t * nb;
+  launch_kernel(fp8_quant_kernel, dim3(unsigned((total + 31) / 32)), dim3(256), static_cast<hipStream_t>(stream),
+                a.x, a.ldx, a.d, nb, total, a.q, a.scales);
+  return int(hipGetLastError());
+}
+
+}  // namespace qmm

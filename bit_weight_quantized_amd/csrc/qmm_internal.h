@@ -151,6 +151,10 @@ struct ProfileEvents {
 };
 ProfileEvents take_profile_events();
 
+// Error text of the calling thread (qmm_last_error); both return the status.
+qmm_status api_fail(qmm_status s, const char* what);
+qmm_status api_hip_fail(int err, const char* where);
+
 struct DevInfo {
   int cus;
 };

@@ -1,0 +1,193 @@
+// Norms before and after a block, with the block's gate and the residual scale,
+// in one pass over the rows:
+//
+//   u = o·rsqrt(mean(o²) + eps)·(w_offset + post_w)     (u = o without post_w)
+//   v = res_scale·r + gate·u                            (the new residual row)
+//   h = v·rsqrt(mean(v²) + eps)·(w_offset + pre_w)      (the next block's input)
+//
+// A workgroup holds one row in registers (8 elements a lane and step), so o and
+// r are read once and v and h are written once: bound by memory for many rows,
+// by the two sums over the row for a few.  Everything between the loads and the
+// stores is fp32; h is made from v before v is rounded for the store, and the
+// e4m3 codes from h before h is rounded.
+#include <hip/hip_runtime.h>
+
+#include "qmm_fp8.h"
+#include "qmm_fp8_device.h"
+#include "qmm_launch.h"
+
+namespace qmm {
+namespace {
+
+struct F8 {
+  float f[8];
+};
+
+__device__ __forceinline__ F8 widen(const u32x4_t v) {
+  F8 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    r.f[2 * i] = bf16_lo(v[i]);
+    r.f[2 * i + 1] = bf16_hi(v[i]);
+  }
+  return r;
+}
+
+__device__ __forceinline__ u32x4_t narrow(const F8& v) {
+  u32x4_t r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    r[i] = uint32_t(f32_to_bf16(v.f[2 * i])) | uint32_t(f32_to_bf16(v.f[2 * i + 1])) << 16;
+  return r;
+}
+
+__device__ __forceinline__ F8 load_f32x8(const float* p) {
+  const f32x4_t a = *reinterpret_cast<const f32x4_t*>(p), b = *reinterpret_cast<const f32x4_t*>(p + 4);
+  F8 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    r.f[i] = a[i];
+    r.f[4 + i] = b[i];
+  }
+  return r;
+}
+
+// Sum over the workgroup, the same in every lane: a tree in each wave, then
+// the waves' sums in wave order.
+template <int WAVES>
+__device__ __forceinline__ float block_sum(float v, float* lds) {
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o);
+  if constexpr (WAVES == 1) return v;
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+  __syncthreads();
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < WAVES; ++i) s += lds[i];
+  return s;
+}
+
+template <int WAVES, int V, bool RF32>
+__global__ __launch_bounds__(64 * WAVES) void norm_kernel(NormArgs a) {
+  __shared__ float sums[2][WAVES];
+  const int64_t row = blockIdx.x;
+  const int n8 = a.d >> 3;
+  const float inv_d = 1.0f / float(a.d);
+  F8 v[V];
+  // the block's output, its norm and its gate
+  if (a.o) {
+    const uint16_t* o = a.o + row * a.ldo;
+    float ss = 0.f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int i = threadIdx.x + 64 * WAVES * j;
+      v[j] = widen(i < n8 ? load16(o + 8 * i) : u32x4_t{0, 0, 0, 0});
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(v[j].f[e], v[j].f[e], ss);
+    }
+    if (a.post_w) {
+      const float k = 1.0f / sqrtf(block_sum<WAVES>(ss, sums[0]) * inv_d + a.eps);
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int i = threadIdx.x + 64 * WAVES * j;
+        const F8 w = widen(i < n8 ? load16(a.post_w + 8 * i) : u32x4_t{0, 0, 0, 0});
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[j].f[e] = v[j].f[e] * k * (a.w_offset + w.f[e]);
+      }
+    }
+    if (a.gate) {
+      const uint16_t* g = a.gate + row / a.gate_rows * a.ldg;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int i = threadIdx.x + 64 * WAVES * j;
+        const F8 w = widen(i < n8 ? load16(g + 8 * i) : u32x4_t{0, 0, 0, 0});
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[j].f[e] *= w.f[e];
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[j].f[e] = 0.f;
+  }
+  // the residual
+  float ss = 0.f;
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int i = threadIdx.x + 64 * WAVES * j;
+    F8 r = widen(u32x4_t{0, 0, 0, 0});
+    if (i < n8) {
+      if constexpr (RF32)
+        r = load_f32x8(static_cast<const float*>(a.r) + row * a.ldr + 8 * i);
+      else
+        r = widen(load16(static_cast<const uint16_t*>(a.r) + row * a.ldr + 8 * i));
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      v[j].f[e] = __builtin_fmaf(a.res_scale, r.f[e], v[j].f[e]);
+      ss = __builtin_fmaf(v[j].f[e], v[j].f[e], ss);
+    }
+    if (a.r_out && i < n8) {
+      if constexpr (RF32) {
+        float* to = static_cast<float*>(a.r_out) + row * a.ldr_out + 8 * i;
+        *reinterpret_cast<f32x4_t*>(to) = f32x4_t{v[j].f[0], v[j].f[1], v[j].f[2], v[j].f[3]};
+        *reinterpret_cast<f32x4_t*>(to + 4) = f32x4_t{v[j].f[4], v[j].f[5], v[j].f[6], v[j].f[7]};
+      } else {
+        *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(a.r_out) + row * a.ldr_out + 8 * i) = narrow(v[j]);
+      }
+    }
+  }
+  if (!a.h && !a.q) return;
+  // the next block's norm
+  const float k = 1.0f / sqrtf(block_sum<WAVES>(ss, sums[1]) * inv_d + a.eps);
+  const int nb = (a.d + kFp8Block - 1) / kFp8Block;
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int i = threadIdx.x + 64 * WAVES * j;
+    const F8 w = widen(i < n8 ? load16(a.pre_w + 8 * i) : u32x4_t{0, 0, 0, 0});
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[j].f[e] = v[j].f[e] * k * (a.w_offset + w.f[e]);
+    if (a.h && i < n8) *reinterpret_cast<u32x4_t*>(a.h + row * a.ldh + 8 * i) = narrow(v[j]);
+    if (a.q) {
+      // a scale block is 16 lanes; lanes past the row hold zeros
+      uint32_t m = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m = umax(m, __float_as_uint(v[j].f[e]) & 0x7FFFFFFFu);
+      m = group_umax<16>(m);
+      const BlockScale s = block_scale(m);
+      if (i < n8) {
+        const float f = s.factor;
+        *reinterpret_cast<u32x2_t*>(a.q + row * a.d + 8 * i) =
+            u32x2_t{pack_e4m3x4(v[j].f[0] * f, v[j].f[1] * f, v[j].f[2] * f, v[j].f[3] * f),
+                    pack_e4m3x4(v[j].f[4] * f, v[j].f[5] * f, v[j].f[6] * f, v[j].f[7] * f)};
+        if ((i & 15) == 0) a.q_scales[row * nb + (i >> 4)] = s.scale;
+      }
+    }
+  }
+}
+
+template <int WAVES, int V>
+int go(const NormArgs& a, hipStream_t s) {
+  if (a.r_f32)
+    launch_kernel(norm_kernel<WAVES, V, true>, dim3(unsigned(a.t)), dim3(64 * WAVES), s, a);
+  else
+    launch_kernel(norm_kernel<WAVES, V, false>, dim3(unsigned(a.t)), dim3(64 * WAVES), s, a);
+  return int(hipGetLastError());
+}
+
+}  // namespace
+
+int launch_norm_residual(const NormArgs& a, void* stream) {
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const int n8 = a.d / 8;
+  if (n8 <= 64) return go<1, 1>(a, s);
+  if (n8 <= 256) return go<4, 1>(a, s);
+  if (n8 <= 512) return go<4, 2>(a, s);
+  if (n8 <= 1024) return go<4, 4>(a, s);
+  if (n8 <= 2048) return go<8, 4>(a, s);
+  if (n8 <= 4096) return go<16, 4>(a, s);
+  return go<16, 8>(a, s);
+}
+
+}  // namespace qmm

@@ -336,6 +336,140 @@ qmm_status qmm_route(const qmm_bf16* x, int64_t t, int64_t d, const qmm_bf16* r,
                      const float* bias, int32_t k, float* scores, int32_t* topk,
                      int32_t* seg_expert, int32_t* seg_offsets, int32_t* row_index, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Block-scaled e4m3 path: 8-bit weights and activations, a router from logits,
+ * and the norms around a block.
+ *
+ * e4m3 is OCP FP8 E4M3 (no infinities, largest value 448), one byte a code.
+ * Codes share one fp32 scale for each block of 128 along the reduction axis,
+ * nb = ceil(d / 128) blocks; the last block may be short:
+ *   activations  x uint8[t][d],  scales fp32[t][nb]
+ *   weights      w uint8[n][d],  scales fp32[ceil(n / 128)][nb] (128 rows share a row)
+ * both row-major, used as they are (no packing).  Limits: d a multiple of 16,
+ * 16 <= d <= 65536; 1 <= n <= 2^28; t <= 2^24; t = 0 is a no-op.  Weights and
+ * activations 16-byte aligned, scales 4-byte, bf16 outputs 2-byte (rows that
+ * are 8-byte aligned are stored faster).
+ * ------------------------------------------------------------------------- */
+typedef enum { QMM_BF16 = 1, QMM_F32 = 2 } qmm_dtype;
+
+/* bf16 rows to e4m3 with their scales, for each block b of 128:
+ *   m = max(max_b |x|, 2^-96);  scales = m / 448;  q = e4m3(x·(448 / m))
+ * divisions and product rounded to fp32, the code to nearest even: a result of
+ * the formula alone, bit for bit.  A block that holds an infinity or a NaN gets
+ * an infinite or NaN scale, and stands for NaN.
+ *   x       bf16[t] rows of d at stride ldx (elements; >= d, a multiple of 8),
+ *           16-byte aligned
+ *   q       uint8[t][d], 16-byte aligned;  scales fp32[t][nb]
+ * t·nb <= 2^28. */
+qmm_status qmm_fp8_quant(const qmm_bf16* x, int64_t t, int64_t d, int64_t ldx, uint8_t* q, float* scales,
+                         void* stream);
+
+/* Y = X·Wᵀ on block-scaled e4m3:
+ *   y[t][n] = Σ_b xs[t][b]·ws[n/128][b]·Σ_{k in b} x[t][k]·w[n][k]
+ * products and block sums in the matrix cores, the sum over the blocks in fp32,
+ * rounded once to bf16.  y: bf16 rows of n at stride ldy (elements, >= n); the
+ * bytes between them are left alone.  No workspace; the order of every sum
+ * depends on the shape alone. */
+qmm_status qmm_fp8_gemm(const uint8_t* w, const float* w_scales, int64_t t, int64_t n, int64_t d, const uint8_t* x,
+                        const float* x_scales, qmm_bf16* y, int64_t ldy, void* stream);
+
+/* qmm_fp8_gemm for the segments of grouped rows, the tables as for
+ * qmm_grouped_gemm (qmm_route, qmm_route_topk):
+ *   w_stack   uint8[n_experts][n][d];  w_scales fp32[n_experts][ceil(n/128)][nb]
+ *   x         uint8[t_x][d], fp32[t_x][nb]; t_x·d < 2^31
+ *   row_index int32[m_total] (grouped row r reads x row row_index[r]) or NULL
+ *   y         bf16[m_total][n]
+ *   max_seg_rows  host upper bound on the rows of a segment: it selects kernels
+ *             and launch shapes, never memory bounds, and t is always a valid one
+ * A segment whose expert is outside [0, n_experts), or a row whose row_index is
+ * outside [0, t_x), gets NaN outputs.  Rows covered by no segment are not
+ * written. */
+qmm_status qmm_fp8_grouped_gemm(const uint8_t* w_stack, const float* w_scales, int32_t n_experts, int64_t n, int64_t d,
+                                const uint8_t* x, const float* x_scales, int64_t t_x, const int32_t* row_index,
+                                const int32_t* seg_expert, const int32_t* seg_offsets, int32_t n_seg, int32_t m_total,
+                                int32_t max_seg_rows, qmm_bf16* y, void* stream);
+
+/* The same for a gate_up stack, with SwiGLU in the epilogue: rows [0, n/2) are
+ * the gate, rows [n/2, n) the up projection, and each half has scale rows of
+ * its own: w_scales fp32[n_experts][2·ceil(n/2 / 128)][nb].
+ *   h   bf16[m_total][n/2] = silu(gate)·up, gate and up the fp32 sums, rounded
+ *       once.  n must be even. */
+qmm_status qmm_fp8_grouped_gemm_swiglu(const uint8_t* w_stack, const float* w_scales, int32_t n_experts, int64_t n,
+                                       int64_t d, const uint8_t* x, const float* x_scales, int64_t t_x,
+                                       const int32_t* row_index, const int32_t* seg_expert, const int32_t* seg_offsets,
+                                       int32_t n_seg, int32_t m_total, int32_t max_seg_rows, qmm_bf16* h,
+                                       void* stream);
+
+typedef enum { QMM_SCORE_SOFTMAX = 0, QMM_SCORE_SIGMOID = 1 } qmm_score;
+typedef enum { QMM_GROUP_MAX = 0, QMM_GROUP_TOP2 = 1 } qmm_group_score;
+
+/* Workspace of qmm_route_topk in bytes (0 up to 128 tokens; never more than
+ * 4·n_experts for every 32 tokens).  Host only. */
+size_t qmm_route_topk_workspace_bytes(int64_t t, int32_t n_experts);
+
+/* Router from logits: scores, a balance bias, groups of experts, top-k,
+ * renormalised weights, and the tokens grouped by expert.
+ *   logits  [t] rows of n_experts at stride ld, bf16 or fp32 (dtype).  A logit of
+ *           -inf masks its expert for that token: never chosen, probability 0.
+ *           NaN logits are never chosen either; under softmax they make the
+ *           token's weights NaN
+ *   p       softmax over the row or 1/(1 + e^-l), fp32
+ *   c       p + bias (fp32[n_experts], or NULL).  Under softmax without a bias,
+ *           unless groups go by their two largest, c is the logit itself: the
+ *           same order, without the rounding of p
+ *   groups  n_groups runs of n_experts/n_groups experts; the keep_groups with
+ *           the largest value (its largest c, or with QMM_GROUP_TOP2 the sum of
+ *           its two largest unmasked c) stay, equal values to the lower group
+ *   topk    int32[t][k]: the k largest c of the kept groups, largest first, equal
+ *           ones to the lower expert; -1 where fewer than k are left
+ *   weights fp32[t][k]: p of the chosen, with renorm != 0 divided by their sum,
+ *           times scale; 0 in slots of -1 and where the sum is 0
+ *   seg_expert int32[n_experts], seg_offsets int32[n_experts + 1], row_index
+ *           int32[t·k]: the tables of qmm_route; segment e is expert e, tokens
+ *           ascending, and row_index is -1 past seg_offsets[n_experts]
+ *   slot_row int32[t][k]: the grouped row of each slot, -1 in slots of -1
+ *   ws      qmm_route_topk_workspace_bytes(t, n_experts) bytes, 4-byte aligned
+ * Limits: t·k < 2^30; n_experts <= 1024; k <= min(64, n_experts); n_groups <= 64,
+ * dividing n_experts.  One launch up to 128 tokens, else two. */
+qmm_status qmm_route_topk(const void* logits, qmm_dtype dtype, int64_t t, int32_t n_experts, int64_t ld,
+                          qmm_score score, const float* bias, int32_t n_groups, int32_t keep_groups,
+                          qmm_group_score group_score, int32_t k, int32_t renorm, float scale, int32_t* topk,
+                          float* weights, int32_t* seg_expert, int32_t* seg_offsets, int32_t* row_index,
+                          int32_t* slot_row, void* ws, size_t ws_bytes, void* stream);
+
+/* Expert outputs back to their tokens by the router's slots:
+ *   out[t] = Σ_j weights[t][j]·o[slot_row[t][j]] (+ shared[t])
+ * in slot order, fp32, rounded once.
+ *   o bf16[m_total][d]; slot_row int32[t][k], weights fp32[t][k] (qmm_route_topk);
+ *   shared bf16[t][d] or NULL; out bf16[t][d] (may be shared).  A slot below 0 adds
+ *   nothing; one at m_total or above makes the token NaN.
+ * Limits: k <= 64, d a multiple of 8 in [8, 65536], t·k < 2^30; o, shared and out
+ * 16-byte aligned. */
+qmm_status qmm_moe_gather(const qmm_bf16* o, int32_t m_total, int64_t d, int64_t t, int32_t k, const int32_t* slot_row,
+                          const float* weights, const qmm_bf16* shared, qmm_bf16* out, void* stream);
+
+/* Norms before and after a block with its gate and the residual scale, one pass:
+ *   u = o·rsqrt(mean(o²) + eps)·(w_offset + post_w)   (u = o without post_w)
+ *   v = res_scale·r + gate·u                          -> r_out, type of r
+ *   h = v·rsqrt(mean(v²) + eps)·(w_offset + pre_w)    -> h (bf16), q + q_scales (e4m3)
+ * all in fp32; each output is rounded once, from the fp32 value (h from the
+ * unrounded v, the codes from the unrounded h, as qmm_fp8_quant rounds them).
+ *   o       bf16[t] rows at stride ldo, or NULL (no block yet: v = res_scale·r)
+ *   post_w  bf16[d] or NULL;  pre_w bf16[d], NULL only without h and q
+ *   gate    bf16 rows at stride ldg: token i takes row i / gate_rows (gate_rows
+ *           >= t or ldg = 0: one row for all); NULL: 1
+ *   r       bf16 or fp32 rows (r_type) at stride ldr; r_out may be r
+ *   r_out, h, (q, q_scales): each may be NULL, not all; q uint8[t][d], q_scales
+ *           fp32[t][nb]
+ *   w_offset  0, or 1 for weights stored as their distance from 1
+ * Limits: d a multiple of 8, 8 <= d <= 65536; t <= 2^24; every row 16-byte
+ * aligned (q 8-byte). */
+qmm_status qmm_norm_residual(int64_t t, int64_t d, const qmm_bf16* o, int64_t ldo, const qmm_bf16* post_w,
+                             const qmm_bf16* gate, int64_t ldg, int64_t gate_rows, const void* r, qmm_dtype r_type,
+                             int64_t ldr, float res_scale, void* r_out, int64_t ldr_out, const qmm_bf16* pre_w,
+                             float w_offset, float eps, qmm_bf16* h, int64_t ldh, uint8_t* q, float* q_scales,
+                             void* stream);
+
 /* Per-kernel GPU timing (per-op GPU timestamps, as in the op profiling of
  * "LLM Decode / Prefill 优化案例（Metal）", Step 1).  Arms two caller-owned
  * hipEvent_t handles for the next qmm_gemv / qmm_gemm / qmm_grouped_gemm /
