@@ -37,7 +37,16 @@ struct Fp8GemmArgs {
   int n_experts, n_seg, m_total, max_seg_rows;
   bool glu;              // gate rows [0, n/2), up rows [n/2, n): y = silu(gate)·up
 };
-int launch_fp8_rows(const Fp8GemmArgs& a, void* stream);
+// Rows one workgroup of the few-row kernel takes in a pass, and the longest
+// segment (dense: row count) that goes to it.
+constexpr int kFp8RowsMax = 64;
+// few rows: every weight read once for up to 64 rows; segments longer than
+// max_rows are left out (0: none)
+int launch_fp8_rows(const Fp8GemmArgs& a, int max_rows, void* stream);
+// many rows: LDS tiles; segments of up to skip_rows rows are left out
+int launch_fp8_tile(const Fp8GemmArgs& a, int skip_rows, void* stream);
+// the choice between them
+int launch_fp8_product(const Fp8GemmArgs& a, void* stream);
 
 struct TopkArgs {
   const void* logits;   // [t][ld], bf16 or fp32

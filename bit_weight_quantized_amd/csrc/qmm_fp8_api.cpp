@@ -64,7 +64,7 @@ qmm_status grouped(const char* name, bool glu, const uint8_t* w_stack, const flo
   a.m_total = m_total;
   a.max_seg_rows = max_seg_rows < m_total ? max_seg_rows : m_total;
   a.glu = glu;
-  const int err = qmm::launch_fp8_rows(a, stream);
+  const int err = qmm::launch_fp8_product(a, stream);
   return err ? api_hip_fail(err, name) : QMM_OK;
 }
 
@@ -111,7 +111,7 @@ qmm_status qmm_fp8_gemm(const uint8_t* w, const float* w_scales, int64_t t, int6
   a.ldy = ldy;
   a.n = int(n);
   a.d = int(d);
-  const int err = qmm::launch_fp8_rows(a, stream);
+  const int err = qmm::launch_fp8_product(a, stream);
   return err ? api_hip_fail(err, "qmm_fp8_gemm") : QMM_OK;
 }
 

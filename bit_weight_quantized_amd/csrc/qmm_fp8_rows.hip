@@ -3,11 +3,13 @@
 //
 //   y[t,n] = Σ_b xs[t,b]·ws[n/128,b] · Σ_{k in b} x[t,k]·w[n,k]
 //
-// One v_mfma_f32_16x16x128_f8f6f4 covers 16 weight rows, 16 activation rows
-// and one whole scale block, so the block's sum comes out of the matrix core
-// exactly once and takes its two scales in one fp32 multiply-add per value:
-// weights are the A operand, activations the B operand, so a lane's four
-// results share one activation row (its xs) and one weight block (ws).
+// Codes are converted to bf16 (exact) and multiplied by four
+// v_mfma_f32_16x16x32_bf16 per scale block: these sum in fp32, where the e4m3
+// instruction aligns the products of 8 neighbouring codes to the largest and
+// cuts what lies 13 binary places below (measured); reading the weights takes
+// several times longer than either.  Weights are the A operand, activations the
+// B operand, so a lane's four results share one activation row (its xs) and one
+// weight block (ws), and a block sum takes its scales in one multiply-add.
 //
 // A workgroup takes 16·R weight rows; its waves split the reduction axis in
 // runs of U blocks (U·128 consecutive bytes of each weight row), each keeps
@@ -19,6 +21,8 @@
 #include "qmm_fp8_device.h"
 #include "qmm_launch.h"
 
+#include <algorithm>
+
 namespace qmm {
 namespace {
 
@@ -28,21 +32,17 @@ struct Fp8Grouped {
   const int32_t* seg_offsets;
   int n_experts, m_total;
   int t_x;
+  int max_rows;   // longer segments are left out (0: none)
 };
 
-__device__ __forceinline__ f32x4_t mfma_fp8_16x16x128(const i32x8_t a, const i32x8_t b) {
-  // formats 0: e4m3; block exponents 0 select the unscaled instruction
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
-}
-
-__device__ __forceinline__ i32x8_t join(const u32x4_t a, const u32x4_t b) {
-  i32x8_t r;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    r[i] = int(a[i]);
-    r[4 + i] = int(b[i]);
-  }
-  return r;
+// eight codes -> eight bf16
+__device__ __forceinline__ bf16x8_t e4m3x8_to_bf16(uint32_t lo, uint32_t hi) {
+  u32x4_t r;
+  r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false));
+  r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true));
+  r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false));
+  r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true));
+  return __builtin_bit_cast(bf16x8_t, r);
 }
 
 // WAVES waves split the reduction axis; R (C) blocks of 16 weight (activation)
@@ -72,7 +72,7 @@ __global__ __launch_bounds__(64 * WAVES) void fp8_rows_kernel(
     const int s = blockIdx.y;
     m_begin = min(max(grp.seg_offsets[s], 0), grp.m_total);
     m_end = min(max(grp.seg_offsets[s + 1], int(m_begin)), grp.m_total);
-    if (m_begin == m_end) return;
+    if (m_begin == m_end || (grp.max_rows && m_end - m_begin > grp.max_rows)) return;
     const int e = grp.seg_expert[s];
     bad_expert = e < 0 || e >= grp.n_experts;
     if (!bad_expert) {
@@ -153,19 +153,27 @@ __global__ __launch_bounds__(64 * WAVES) void fp8_rows_kernel(
         v.s[c] = __uint_as_float(buf_load4(sr, in ? (soff[c] + 4u * uint32_t(b)) | (soff[c] & kOOB8) : kOOB8));
     };
     auto use = [&](const Block& v) {
-      i32x8_t a[R];
+      f32x4_t p[R][C];
 #pragma unroll
-      for (int r = 0; r < R; ++r) a[r] = join(v.a[r][0], v.a[r][1]);
+      for (int h = 0; h < 4; ++h) {   // codes 16·g + 8·(h & 1) .. + 7 of half h >> 1
+        bf16x8_t a[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) a[r] = e4m3x8_to_bf16(v.a[r][h >> 1][2 * (h & 1)], v.a[r][h >> 1][2 * (h & 1) + 1]);
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          const bf16x8_t b = e4m3x8_to_bf16(v.b[c][h >> 1][2 * (h & 1)], v.b[c][h >> 1][2 * (h & 1) + 1]);
+#pragma unroll
+          for (int r = 0; r < R; ++r)
+            p[r][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[r], b, h ? p[r][c] : f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+        }
+      }
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        const i32x8_t b = join(v.b[c][0], v.b[c][1]);
         const float s0 = v.s[c] * v.w0, s1 = GLU ? v.s[c] * v.w1 : 0.f;
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const f32x4_t p = mfma_fp8_16x16x128(a[r], b);
+        for (int r = 0; r < R; ++r)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) acc[r][c][i] = __builtin_fmaf(p[i], r < RO ? s0 : s1, acc[r][c][i]);
-        }
+          for (int i = 0; i < 4; ++i) acc[r][c][i] = __builtin_fmaf(p[r][c][i], r < RO ? s0 : s1, acc[r][c][i]);
       }
     };
 
@@ -235,9 +243,9 @@ __global__ __launch_bounds__(64 * WAVES) void fp8_rows_kernel(
 }
 
 template <int WAVES, int R, int C, int U, bool GROUPED, bool GLU>
-int go(const Fp8GemmArgs& a, hipStream_t s) {
+int go(const Fp8GemmArgs& a, int max_rows, hipStream_t s) {
   const int nout = GLU ? a.n / 2 : a.n, per = 16 * (GLU ? R / 2 : R);
-  const Fp8Grouped grp{a.row_index, a.seg_expert, a.seg_offsets, a.n_experts, a.m_total, int(a.t_x)};
+  const Fp8Grouped grp{a.row_index, a.seg_expert, a.seg_offsets, a.n_experts, a.m_total, int(a.t_x), max_rows};
   const unsigned gy = GROUPED ? unsigned(a.n_seg) : unsigned((a.t + 16 * C - 1) / (16 * C));
   launch_kernel(fp8_rows_kernel<WAVES, R, C, U, GROUPED, GLU>, dim3(unsigned((nout + per - 1) / per), gy),
                 dim3(64 * WAVES), s, a.w, a.ws, a.n, a.d, fp8_blocks(a.d), a.x, a.xs, a.t, a.y, a.ldy, grp);
@@ -246,22 +254,22 @@ int go(const Fp8GemmArgs& a, hipStream_t s) {
 
 }  // namespace
 
-int launch_fp8_rows(const Fp8GemmArgs& a, void* stream) {
+int launch_fp8_rows(const Fp8GemmArgs& a, int max_rows, void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const int64_t rows = a.n_seg > 0 ? a.max_seg_rows : a.t;
+  const int64_t rows = a.n_seg > 0 ? (max_rows ? std::min(max_rows, a.max_seg_rows) : a.max_seg_rows) : a.t;
   if (a.n_seg > 0) {
     if (a.glu) {
-      if (rows <= 16) return go<4, 2, 1, 2, true, true>(a, s);
-      if (rows <= 32) return go<4, 2, 2, 2, true, true>(a, s);
-      return go<4, 4, 4, 1, true, true>(a, s);
+      if (rows <= 16) return go<4, 2, 1, 2, true, true>(a, max_rows, s);
+      if (rows <= 32) return go<4, 2, 2, 2, true, true>(a, max_rows, s);
+      return go<4, 4, 4, 1, true, true>(a, max_rows, s);
     }
-    if (rows <= 16) return go<4, 1, 1, 4, true, false>(a, s);
-    if (rows <= 32) return go<4, 2, 2, 2, true, false>(a, s);
-    return go<4, 4, 4, 1, true, false>(a, s);
+    if (rows <= 16) return go<4, 1, 1, 4, true, false>(a, max_rows, s);
+    if (rows <= 32) return go<4, 2, 2, 2, true, false>(a, max_rows, s);
+    return go<4, 4, 4, 1, true, false>(a, max_rows, s);
   }
-  if (rows <= 16) return go<4, 1, 1, 4, false, false>(a, s);
-  if (rows <= 32) return go<4, 2, 2, 2, false, false>(a, s);
-  return go<4, 4, 4, 1, false, false>(a, s);
+  if (rows <= 16) return go<4, 1, 1, 4, false, false>(a, 0, s);
+  if (rows <= 32) return go<4, 2, 2, 2, false, false>(a, 0, s);
+  return go<4, 4, 4, 1, false, false>(a, 0, s);
 }
 
 }  // namespace qmm
