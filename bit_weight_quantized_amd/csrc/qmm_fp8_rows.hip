@@ -3,28 +3,41 @@
 //
 //   y[t,n] = Σ_b xs[t,b]·ws[n/128,b] · Σ_{k in b} x[t,k]·w[n,k]
 //
-// Codes are converted to bf16 (exact) and multiplied by four
-// v_mfma_f32_16x16x32_bf16 per scale block: these sum in fp32, where the e4m3
-// instruction aligns the products of 8 neighbouring codes to the largest and
-// cuts what lies 13 binary places below (measured); reading the weights takes
-// several times longer than either.  Weights are the A operand, activations the
-// B operand, so a lane's four results share one activation row (its xs) and one
-// weight block (ws), and a block sum takes its scales in one multiply-add.
+// Bound by the weights' bytes, so the kernel is built to keep reads in flight:
+// a workgroup takes 16·R weight rows, its waves split the reduction axis into
+// equal runs of blocks, and every wave streams its blocks through a private LDS
+// ring of D stages (weights, activations and activation scales of one block,
+// global -> LDS, no registers, no barriers): while one block is used, the next
+// D - 1 are on their way.  Each wave keeps fp32 accumulators, and the waves'
+// sums are added in wave order through LDS: nothing depends on timing.
 //
-// A workgroup takes 16·R weight rows; its waves split the reduction axis in
-// runs of U blocks (U·128 consecutive bytes of each weight row), each keeps
-// fp32 accumulators, and the waves' sums are added in wave order through LDS:
-// the result does not depend on timing.
+// Weights are the A operand, activations the B operand: a lane's four results
+// share one activation row (its xs) and one weight block (ws), and a block sum
+// takes its two scales in one multiply-add.  Up to 16 rows convert the codes
+// to bf16 (exact) for four v_mfma_f32_16x16x32_bf16, which sum in fp32; the e4m3
+// instruction, used beyond, aligns the products of 8 neighbouring codes to the
+// largest and cuts what lies 13 binary places below it (measured).  Few rows
+// feed the next layer's rounding directly and have the time; with more rows the
+// conversions would cost more than the reads.
 #include <hip/hip_runtime.h>
 
 #include "qmm_fp8.h"
 #include "qmm_fp8_device.h"
 #include "qmm_launch.h"
+#include "qmm_lds_copy.h"
 
 #include <algorithm>
 
 namespace qmm {
 namespace {
+
+// Waits for the ring, as asm so that no LDS read is moved across them: at most N
+// copies of this wave in flight; every LDS read of this wave done.
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+  asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
+}
+__device__ __forceinline__ void wait_lds_reads() { asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory"); }
 
 struct Fp8Grouped {
   const int32_t* row_index;
@@ -45,17 +58,43 @@ __device__ __forceinline__ bf16x8_t e4m3x8_to_bf16(uint32_t lo, uint32_t hi) {
   return __builtin_bit_cast(bf16x8_t, r);
 }
 
-// WAVES waves split the reduction axis; R (C) blocks of 16 weight (activation)
-// rows; U scale blocks a wave loads at once.  GLU: the upper half of the R
-// blocks are the up rows of the same outputs.
-template <int WAVES, int R, int C, int U, bool GROUPED, bool GLU>
+__device__ __forceinline__ i32x8_t join(const u32x4_t a, const u32x4_t b) {
+  i32x8_t r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    r[i] = int(a[i]);
+    r[4 + i] = int(b[i]);
+  }
+  return r;
+}
+
+// WAVES waves split the reduction axis; R blocks of 16 weight rows, X8 groups of
+// 8 activation rows, D ring stages.  GLU: the upper half of the R blocks are the
+// up rows of the same outputs.
+template <int WAVES, int R, int X8, int D, bool GROUPED, bool GLU>
+struct Fp8Rows {
+  static constexpr int C = (X8 + 1) / 2;                 // blocks of 16 activation rows
+  static constexpr int RO = GLU ? R / 2 : R;             // blocks of output columns
+  static constexpr bool kExact = C == 1;
+  static constexpr int kSc = (X8 * 8 + 63) / 64;         // scale copies of a stage
+  static constexpr int kOps = 2 * R + X8 + kSc;          // copies of a stage
+  static constexpr int kX = 2048 * R, kS = kX + 2048 * C; // stage: weights, activations, scales
+  static constexpr int kStage = kS + 256 * kSc;
+  static constexpr int kRing = WAVES * D * kStage, kPart = WAVES * R * C * 1024;
+  static constexpr int kLds = kRing > kPart ? kRing : kPart;
+  static_assert(!GLU || R % 2 == 0, "gate and up blocks come in pairs");
+  static_assert((D - 1) * kOps <= 63, "the waits count the copies in flight");
+  static_assert(kLds <= 160 * 1024, "LDS");
+};
+
+template <int WAVES, int R, int X8, int D, bool GROUPED, bool GLU>
 __global__ __launch_bounds__(64 * WAVES) void fp8_rows_kernel(
     const uint8_t* __restrict__ w, const float* __restrict__ ws, int n, int d, int nb,
     const uint8_t* __restrict__ x, const float* __restrict__ xs, int64_t t, uint16_t* __restrict__ y, int64_t ldy,
     Fp8Grouped grp) {
-  static_assert(!GLU || R % 2 == 0, "gate and up blocks come in pairs");
-  constexpr int RO = GLU ? R / 2 : R;              // blocks of output columns
-  __shared__ __attribute__((aligned(16))) f32x4_t part[WAVES][R * C][64];
+  using T = Fp8Rows<WAVES, R, X8, D, GROUPED, GLU>;
+  constexpr int C = T::C, RO = T::RO, kRows = 8 * X8;
+  extern __shared__ __attribute__((aligned(1024))) unsigned char lds[];
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -80,48 +119,77 @@ __global__ __launch_bounds__(64 * WAVES) void fp8_rows_kernel(
       wsm += int64_t(e) * (GLU ? 2 * sb : (n + kFp8Block - 1) / kFp8Block) * nb;
     }
   } else {
-    m_begin = int64_t(blockIdx.y) * 16 * C;
-    m_end = min(t, m_begin + 16 * C);
+    m_begin = int64_t(blockIdx.y) * kRows;
+    m_end = min(t, m_begin + kRows);
   }
+  const float* ws0 = wsm + int64_t(n0 / kFp8Block) * nb;
+  const float* ws1 = wsm + int64_t(sb + n0 / kFp8Block) * nb;
 
-  // weight rows: one buffer per half, based at the tile's first row, so the
-  // 32-bit offsets stay small; rows past the matrix read zero
+  // Copies: lane / 8 is the row of a copy's eight, LDS chunk lane % 8 holds the
+  // row's 16-byte chunk (lane % 8) ^ (row % 8), so that the operand reads of
+  // eight neighbouring rows fall into different banks.
+  // Weight rows: one buffer per half, based at the tile's first row, so the
+  // 32-bit offsets stay small; rows past the matrix read zero.
+  const int crow = lane >> 3, cchunk = 16 * ((lane & 7) ^ crow);
   const int live = min(16 * RO, nout - n0);
   const __amdgpu_buffer_rsrc_t wr0 = make_rsrc(wm + int64_t(n0) * d, uint32_t(live) * uint32_t(d));
   const __amdgpu_buffer_rsrc_t wr1 =
       GLU ? make_rsrc(wm + int64_t(nout + n0) * d, uint32_t(live) * uint32_t(d)) : wr0;
-  const float* ws0 = wsm + int64_t(n0 / kFp8Block) * nb;
-  const float* ws1 = wsm + int64_t(sb + n0 / kFp8Block) * nb;
+  uint32_t woff[2 * RO];
+#pragma unroll
+  for (int i = 0; i < 2 * RO; ++i) woff[i] = 8 * i + crow < live ? uint32_t(8 * i + crow) * uint32_t(d) : kOOB8;
 
-  for (int64_t m0 = m_begin; m0 < m_end; m0 += 16 * C) {
+  // the wave's share of the reduction axis, and its ring
+  const int b_begin = nb * wave / WAVES, b_end = nb * (wave + 1) / WAVES;
+  const unsigned char* ring = lds + wave * D * T::kStage;
+  const uint32_t ring_at = lds_addr(ring);
+  const int o0 = 128 * col + 16 * (g ^ (col & 7));       // operand chunks g and g + 4 of row col
+
+  for (int64_t m0 = m_begin; m0 < m_end; m0 += kRows) {
     // activation rows: dense rows are based at the pass's first row; grouped
     // rows can be anywhere in x (below 2 GiB, checked by the caller)
     __amdgpu_buffer_rsrc_t xr, sr;
-    uint32_t xoff[C], soff[C];
-    bool bad_row[C];
     if constexpr (GROUPED) {
       xr = make_rsrc(x, uint32_t(grp.t_x) * uint32_t(d));
       sr = make_rsrc(xs, uint32_t(grp.t_x) * uint32_t(nb) * 4u);
     } else {
-      const uint32_t rows = uint32_t(min(int64_t(16 * C), m_end - m0));
+      const uint32_t rows = uint32_t(min(int64_t(kRows), m_end - m0));
       xr = make_rsrc(x + m0 * d, rows * uint32_t(d));
       sr = make_rsrc(xs + m0 * nb, rows * uint32_t(nb) * 4u);
     }
+    auto source = [&](int row) -> int {            // the row of x (dense: of the pass), or -1
+      if (m0 + row >= m_end) return -1;
+      if constexpr (!GROUPED) return row;
+      const int src = grp.row_index ? grp.row_index[m0 + row] : int(m0 + row);
+      return bad_expert || src < 0 || src >= grp.t_x ? -1 : src;
+    };
+    uint32_t xoff[X8], soff[T::kSc];
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      uint32_t row = uint32_t(16 * c + col);
-      bool ok = m0 + row < m_end;
-      bad_row[c] = false;
-      if constexpr (GROUPED) {
-        const int64_t at = m0 + row;
-        const int src = ok ? (grp.row_index ? grp.row_index[at] : int(at)) : 0;
-        bad_row[c] = bad_expert || src < 0 || src >= grp.t_x;
-        ok = ok && !bad_row[c];
-        row = uint32_t(src);
-      }
-      xoff[c] = ok ? row * uint32_t(d) : kOOB8;
-      soff[c] = ok ? row * uint32_t(nb) * 4u : kOOB8;
+    for (int i = 0; i < X8; ++i) {
+      const int src = source(8 * i + crow);
+      xoff[i] = src >= 0 ? uint32_t(src) * uint32_t(d) : kOOB8;
     }
+#pragma unroll
+    for (int i = 0; i < T::kSc; ++i) {
+      const int src = 64 * i + lane < kRows ? source(64 * i + lane) : -1;
+      soff[i] = src >= 0 ? uint32_t(src) * uint32_t(nb) * 4u : kOOB8;
+    }
+    auto copy = [&](int b, int stage) {
+      const uint32_t at = ring_at + uint32_t(stage * T::kStage);
+      const uint32_t k = uint32_t(kFp8Block * b + cchunk);
+      const uint32_t ko = b < b_end && k < uint32_t(d) ? k : kOOB8;   // past the wave's share: zeros, no reads
+#pragma unroll
+      for (int i = 0; i < 2 * R; ++i) {
+        const uint32_t o = woff[i % (2 * RO)];
+        copy16_to_lds(i < 2 * RO ? wr0 : wr1, (o + ko) | ((o | ko) & kOOB8), at + 1024u * i);
+      }
+#pragma unroll
+      for (int i = 0; i < X8; ++i)
+        copy16_to_lds(xr, (xoff[i] + ko) | ((xoff[i] | ko) & kOOB8), at + T::kX + 1024u * i);
+#pragma unroll
+      for (int i = 0; i < T::kSc; ++i)
+        copy4_to_lds(sr, b < b_end ? soff[i] + 4u * uint32_t(b) : kOOB8, at + T::kS + 256u * i);
+    };
 
     f32x4_t acc[R][C];
 #pragma unroll
@@ -129,101 +197,88 @@ __global__ __launch_bounds__(64 * WAVES) void fp8_rows_kernel(
 #pragma unroll
       for (int c = 0; c < C; ++c) acc[r][c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-    struct Block {
-      u32x4_t a[R][2], b[C][2];
-      float s[C], w0, w1;
-    };
-    auto load = [&](Block& v, int b) {
-      const bool in = b < nb;                      // uniform
-      const int bs = in ? b : 0;
-      v.w0 = ws0[bs];
-      v.w1 = GLU ? ws1[bs] : 0.f;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int k = kFp8Block * b + 64 * h + 16 * g;
-        const uint32_t ko = k < d ? uint32_t(k) : kOOB8;   // also past the last block
+    for (int i = 0; i < D; ++i) copy(b_begin + i, i);
+    float w0 = ws0[min(b_begin, nb - 1)], w1 = GLU ? ws1[min(b_begin, nb - 1)] : 0.f;
+    int stage = 0;
+    for (int b = b_begin; b < b_end; ++b) {
+      const int next = min(b + 1, nb - 1);
+      const float w0n = ws0[next], w1n = GLU ? ws1[next] : 0.f;
+      wait_copies<(D - 1) * T::kOps>();   // block b has landed
+      const unsigned char* st = ring + stage * T::kStage;
+      u32x4_t a[R][2], x2[C][2];
+      float s[C];
 #pragma unroll
-        for (int r = 0; r < R; ++r)
-          v.a[r][h] = buf_load16(r < RO ? wr0 : wr1, (uint32_t(16 * (r % RO) + col) * uint32_t(d) + ko) | (ko & kOOB8));
+      for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int c = 0; c < C; ++c) v.b[c][h] = buf_load16(xr, (xoff[c] + ko) | ((xoff[c] | ko) & kOOB8));
-      }
-#pragma unroll
-      for (int c = 0; c < C; ++c)
-        v.s[c] = __uint_as_float(buf_load4(sr, in ? (soff[c] + 4u * uint32_t(b)) | (soff[c] & kOOB8) : kOOB8));
-    };
-    auto use = [&](const Block& v) {
-      f32x4_t p[R][C];
-#pragma unroll
-      for (int h = 0; h < 4; ++h) {   // codes 16·g + 8·(h & 1) .. + 7 of half h >> 1
-        bf16x8_t a[R];
-#pragma unroll
-        for (int r = 0; r < R; ++r) a[r] = e4m3x8_to_bf16(v.a[r][h >> 1][2 * (h & 1)], v.a[r][h >> 1][2 * (h & 1) + 1]);
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-          const bf16x8_t b = e4m3x8_to_bf16(v.b[c][h >> 1][2 * (h & 1)], v.b[c][h >> 1][2 * (h & 1) + 1]);
-#pragma unroll
-          for (int r = 0; r < R; ++r)
-            p[r][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[r], b, h ? p[r][c] : f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
-        }
-      }
+        for (int h = 0; h < 2; ++h) a[r][h] = *reinterpret_cast<const u32x4_t*>(st + 2048 * r + (o0 ^ (64 * h)));
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        const float s0 = v.s[c] * v.w0, s1 = GLU ? v.s[c] * v.w1 : 0.f;
 #pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[r][c][i] = __builtin_fmaf(p[r][c][i], r < RO ? s0 : s1, acc[r][c][i]);
+        for (int h = 0; h < 2; ++h) x2[c][h] = *reinterpret_cast<const u32x4_t*>(st + T::kX + 2048 * c + (o0 ^ (64 * h)));
+        s[c] = *reinterpret_cast<const float*>(st + T::kS + 4 * (16 * c + col));
       }
-    };
-
-    // runs of U blocks, the next run loaded while the present one is used; a
-    // run past the end reads zeros
-    Block v0[U], v1[U];
+      wait_lds_reads();                   // ... and is in registers: its stage is free
+      copy(b + D, stage);
+      stage = stage + 1 == D ? 0 : stage + 1;
 #pragma unroll
-    for (int u = 0; u < U; ++u) load(v0[u], wave * U + u);
-    for (int b = wave * U; b < nb; b += 2 * WAVES * U) {
+      for (int c = 0; c < C; ++c) {
+        const float s0 = s[c] * w0, s1 = GLU ? s[c] * w1 : 0.f;
 #pragma unroll
-      for (int u = 0; u < U; ++u) load(v1[u], b + WAVES * U + u);
+        for (int r = 0; r < R; ++r) {
+          f32x4_t p = {0.f, 0.f, 0.f, 0.f};
+          if constexpr (T::kExact) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) use(v0[u]);
+            for (int q = 0; q < 4; ++q)
+              p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                  e4m3x8_to_bf16(a[r][q >> 1][2 * (q & 1)], a[r][q >> 1][2 * (q & 1) + 1]),
+                  e4m3x8_to_bf16(x2[c][q >> 1][2 * (q & 1)], x2[c][q >> 1][2 * (q & 1) + 1]), p, 0, 0, 0);
+          } else {
+            // formats 0: e4m3; block exponents 0 select the unscaled instruction
+            p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(join(a[r][0], a[r][1]), join(x2[c][0], x2[c][1]), p,
+                                                                 0, 0, 0, 0, 0, 0);
+          }
 #pragma unroll
-      for (int u = 0; u < U; ++u) load(v0[u], b + 2 * WAVES * U + u);
-#pragma unroll
-      for (int u = 0; u < U; ++u) use(v1[u]);
+          for (int i = 0; i < 4; ++i) acc[r][c][i] = __builtin_fmaf(p[i], r < RO ? s0 : s1, acc[r][c][i]);
+        }
+      }
+      w0 = w0n;
+      w1 = w1n;
     }
 
+    // the ring becomes the waves' sums: [wave][R·C][64]
+    wait_copies<0>();
+    __syncthreads();
+    f32x4_t* part = reinterpret_cast<f32x4_t*>(lds);
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
-      for (int c = 0; c < C; ++c) part[wave][r * C + c][lane] = acc[r][c];
+      for (int c = 0; c < C; ++c) part[(wave * R * C + r * C + c) * 64 + lane] = acc[r][c];
     __syncthreads();
-    // unit u: block (r, c) of the outputs, a lane's four values
     const bool wide = (ldy & 3) == 0 && (reinterpret_cast<uintptr_t>(y) & 7) == 0;
-    for (int u = wave; u < RO * C; u += WAVES) {
-      const int r = u / C, c = u % C;
-      f32x4_t v = part[0][u][lane];
+    auto summed = [&](int u) {
+      f32x4_t v = part[u * 64 + lane];
+#pragma unroll
       for (int p = 1; p < WAVES; ++p) {
-        const f32x4_t o = part[p][u][lane];
+        const f32x4_t o = part[(p * R * C + u) * 64 + lane];
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] += o[i];
       }
+      return v;
+    };
+    // unit u: output block (r, c), a lane's four columns of one row
+    for (int u = wave; u < RO * C; u += WAVES) {
+      const int r = u / C, c = u % C;
+      const int64_t row = m0 + 16 * c + col;
+      const int j = n0 + 16 * r + 4 * g;
+      f32x4_t v = summed(u);
       if constexpr (GLU) {
-        f32x4_t up = part[0][u + RO * C][lane];
-        for (int p = 1; p < WAVES; ++p) {
-          const f32x4_t o = part[p][u + RO * C][lane];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) up[i] += o[i];
-        }
+        const f32x4_t up = summed(u + RO * C);
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = silu(v[i]) * up[i];
       }
-      const int64_t row = m0 + 16 * c + col;
-      const int j = n0 + 16 * r + 4 * g;
-      bool bad = false;
-#pragma unroll
-      for (int cc = 0; cc < C; ++cc) bad = cc == c ? bad_row[cc] : bad;
-      if (row < m_end) {
+      if (16 * c + col < kRows && row < m_end) {
+        const bool bad = GROUPED && source(16 * c + col) < 0;
         uint16_t* to = y + row * ldy + j;
         uint16_t b16[4];
 #pragma unroll
@@ -238,17 +293,18 @@ __global__ __launch_bounds__(64 * WAVES) void fp8_rows_kernel(
         }
       }
     }
-    __syncthreads();   // part is written again by the next pass
+    __syncthreads();   // the next pass fills the ring again
   }
 }
 
-template <int WAVES, int R, int C, int U, bool GROUPED, bool GLU>
+template <int WAVES, int R, int X8, int D, bool GROUPED, bool GLU>
 int go(const Fp8GemmArgs& a, int max_rows, hipStream_t s) {
-  const int nout = GLU ? a.n / 2 : a.n, per = 16 * (GLU ? R / 2 : R);
+  using T = Fp8Rows<WAVES, R, X8, D, GROUPED, GLU>;
+  const int nout = GLU ? a.n / 2 : a.n, per = 16 * T::RO;
   const Fp8Grouped grp{a.row_index, a.seg_expert, a.seg_offsets, a.n_experts, a.m_total, int(a.t_x), max_rows};
-  const unsigned gy = GROUPED ? unsigned(a.n_seg) : unsigned((a.t + 16 * C - 1) / (16 * C));
-  launch_kernel(fp8_rows_kernel<WAVES, R, C, U, GROUPED, GLU>, dim3(unsigned((nout + per - 1) / per), gy),
-                dim3(64 * WAVES), s, a.w, a.ws, a.n, a.d, fp8_blocks(a.d), a.x, a.xs, a.t, a.y, a.ldy, grp);
+  const unsigned gy = GROUPED ? unsigned(a.n_seg) : unsigned((a.t + 8 * X8 - 1) / (8 * X8));
+  launch_kernel_lds(fp8_rows_kernel<WAVES, R, X8, D, GROUPED, GLU>, dim3(unsigned((nout + per - 1) / per), gy),
+                    dim3(64 * WAVES), T::kLds, s, a.w, a.ws, a.n, a.d, fp8_blocks(a.d), a.x, a.xs, a.t, a.y, a.ldy, grp);
   return int(hipGetLastError());
 }
 
@@ -259,17 +315,20 @@ int launch_fp8_rows(const Fp8GemmArgs& a, int max_rows, void* stream) {
   const int64_t rows = a.n_seg > 0 ? (max_rows ? std::min(max_rows, a.max_seg_rows) : a.max_seg_rows) : a.t;
   if (a.n_seg > 0) {
     if (a.glu) {
-      if (rows <= 16) return go<4, 2, 1, 2, true, true>(a, max_rows, s);
-      if (rows <= 32) return go<4, 2, 2, 2, true, true>(a, max_rows, s);
-      return go<4, 4, 4, 1, true, true>(a, max_rows, s);
+      if (rows <= 8) return go<4, 2, 1, 4, true, true>(a, max_rows, s);
+      if (rows <= 16) return go<4, 2, 2, 4, true, true>(a, max_rows, s);
+      if (rows <= 32) return go<4, 2, 4, 3, true, true>(a, max_rows, s);
+      return go<4, 2, 8, 3, true, true>(a, max_rows, s);
     }
-    if (rows <= 16) return go<4, 1, 1, 4, true, false>(a, max_rows, s);
-    if (rows <= 32) return go<4, 2, 2, 2, true, false>(a, max_rows, s);
-    return go<4, 4, 4, 1, true, false>(a, max_rows, s);
+    if (rows <= 8) return go<4, 2, 1, 4, true, false>(a, max_rows, s);
+    if (rows <= 16) return go<4, 2, 2, 4, true, false>(a, max_rows, s);
+    if (rows <= 32) return go<4, 2, 4, 3, true, false>(a, max_rows, s);
+    return go<4, 2, 8, 3, true, false>(a, max_rows, s);
   }
-  if (rows <= 16) return go<4, 1, 1, 4, false, false>(a, 0, s);
-  if (rows <= 32) return go<4, 2, 2, 2, false, false>(a, 0, s);
-  return go<4, 4, 4, 1, false, false>(a, 0, s);
+  if (rows <= 8) return go<4, 2, 1, 4, false, false>(a, 0, s);
+  if (rows <= 16) return go<4, 2, 2, 4, false, false>(a, 0, s);
+  if (rows <= 32) return go<4, 2, 4, 3, false, false>(a, 0, s);
+  return go<4, 2, 8, 3, false, false>(a, 0, s);
 }
 
 }  // namespace qmm
