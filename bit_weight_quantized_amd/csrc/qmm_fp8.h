@@ -37,14 +37,34 @@ struct Fp8GemmArgs {
   int n_experts, n_seg, m_total, max_seg_rows;
   bool glu;              // gate rows [0, n/2), up rows [n/2, n): y = silu(gate)·up
 };
-// Rows one workgroup of the few-row kernel takes in a pass, and the longest
-// segment (dense: row count) that goes to it.
+// Shape of the few-row kernel: 16·r weight rows a workgroup and 8·x8 activation
+// rows a pass.  x8 is the smallest that holds the rows (8 at most), r the largest
+// that still gives 160 workgroups, that is work for most of the 256 CUs: a larger
+// r reads the activations less often (64 x 13824 x 5120: 20.6 us with r = 4, 27.3
+// with 2), a smaller one fills the chip (64 x 5120 x 13824: 37.4, 29.2 and 44.0 us
+// with r = 4, 2 and 1; 64 x 4096 x 7168: 21.2, 16.4, 14.3).  Up to 16 rows r = 4 was
+// never faster than 2.  Grouped rows count one pass a segment.
 constexpr int kFp8RowsMax = 64;
+struct Fp8RowsShape {
+  int r, x8;
+  int64_t workgroups;
+};
+inline Fp8RowsShape fp8_rows_shape(const Fp8GemmArgs& a, int max_rows) {
+  const int64_t rows = a.n_seg == 0 ? a.t : (max_rows && max_rows < a.max_seg_rows ? max_rows : a.max_seg_rows);
+  const int x8 = rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 32 ? 4 : 8;
+  const int64_t passes = a.n_seg == 0 ? (a.t + 8 * x8 - 1) / (8 * x8) : (a.n_seg < a.m_total ? a.n_seg : a.m_total);
+  int r = x8 <= 2 ? 2 : 4;
+  const int least = a.glu ? 2 : 1;
+  auto workgroups = [&](int rr) { return (int64_t(a.n) + 16 * rr - 1) / (16 * rr) * passes; };
+  while (r > least && workgroups(r) < 160) r /= 2;
+  return {r, x8, workgroups(r)};
+}
 // few rows: every weight read once for up to 64 rows; segments longer than
 // max_rows are left out (0: none)
 int launch_fp8_rows(const Fp8GemmArgs& a, int max_rows, void* stream);
-// many rows: LDS tiles; segments of up to skip_rows rows are left out
-int launch_fp8_tile(const Fp8GemmArgs& a, int skip_rows, void* stream);
+// many rows: LDS tiles of 256 x 256 (large) or 128 x 128; segments of up to
+// skip_rows rows are left out
+int launch_fp8_tile(const Fp8GemmArgs& a, bool large, int skip_rows, void* stream);
 // the choice between them
 int launch_fp8_product(const Fp8GemmArgs& a, void* stream);
 

@@ -46,6 +46,13 @@ __device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float
   return uint32_t(v);
 }
 
+// A value at a uniform address of memory that the kernel does not write, as a
+// scalar load (a vector load would count among the copies in flight).
+__device__ __forceinline__ float scalar_load(const float* p, int i) {
+  typedef const __attribute__((address_space(4))) float* constant_ptr;
+  return reinterpret_cast<constant_ptr>(reinterpret_cast<uintptr_t>(p))[i];
+}
+
 __device__ __forceinline__ float silu(float v) { return v / (1.0f + expf(-v)); }
 
 }  // namespace qmm

@@ -23,6 +23,7 @@
 
 #include "qmm_fp8.h"
 #include "qmm_fp8_device.h"
+#include "qmm_fp8_tile.h"
 #include "qmm_launch.h"
 #include "qmm_lds_copy.h"
 
@@ -30,14 +31,6 @@
 
 namespace qmm {
 namespace {
-
-// Waits for the ring, as asm so that no LDS read is moved across them: at most N
-// copies of this wave in flight; every LDS read of this wave done.
-template <int N>
-__device__ __forceinline__ void wait_copies() {
-  asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
-}
-__device__ __forceinline__ void wait_lds_reads() { asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory"); }
 
 struct Fp8Grouped {
   const int32_t* row_index;
@@ -58,16 +51,6 @@ __device__ __forceinline__ bf16x8_t e4m3x8_to_bf16(uint32_t lo, uint32_t hi) {
   return __builtin_bit_cast(bf16x8_t, r);
 }
 
-__device__ __forceinline__ i32x8_t join(const u32x4_t a, const u32x4_t b) {
-  i32x8_t r;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    r[i] = int(a[i]);
-    r[4 + i] = int(b[i]);
-  }
-  return r;
-}
-
 // WAVES waves split the reduction axis; R blocks of 16 weight rows, X8 groups of
 // 8 activation rows, D ring stages.  GLU: the upper half of the R blocks are the
 // up rows of the same outputs.
@@ -76,19 +59,21 @@ struct Fp8Rows {
   static constexpr int C = (X8 + 1) / 2;                 // blocks of 16 activation rows
   static constexpr int RO = GLU ? R / 2 : R;             // blocks of output columns
   static constexpr bool kExact = C == 1;
-  static constexpr int kSc = (X8 * 8 + 63) / 64;         // scale copies of a stage
-  static constexpr int kOps = 2 * R + X8 + kSc;          // copies of a stage
-  static constexpr int kX = 2048 * R, kS = kX + 2048 * C; // stage: weights, activations, scales
-  static constexpr int kStage = kS + 256 * kSc;
-  static constexpr int kRing = WAVES * D * kStage, kPart = WAVES * R * C * 1024;
+  static constexpr int kOps = 2 * R + X8;                // copies of a stage
+  static constexpr int kX = 2048 * R;                    // stage: weights, activations
+  static constexpr int kStage = kX + 2048 * C;
+  static constexpr int kSc = (X8 * 8 + 63) / 64;         // copies of the scales of four blocks
+  static constexpr int kChunk = 1024 * kSc, kChunks = (D + 3) / 4 + 1;
+  static constexpr int kWave = D * kStage + kChunks * kChunk;
+  static constexpr int kRing = WAVES * kWave, kPart = WAVES * R * C * 1024;
   static constexpr int kLds = kRing > kPart ? kRing : kPart;
   static_assert(!GLU || R % 2 == 0, "gate and up blocks come in pairs");
-  static_assert((D - 1) * kOps <= 63, "the waits count the copies in flight");
+  static_assert(D <= 4 && (D - 1) * kOps + kSc <= 63, "the waits count the copies in flight");
   static_assert(kLds <= 160 * 1024, "LDS");
 };
 
 template <int WAVES, int R, int X8, int D, bool GROUPED, bool GLU>
-__global__ __launch_bounds__(64 * WAVES) void fp8_rows_kernel(
+__global__ __launch_bounds__(64 * WAVES, 2) void fp8_rows_kernel(
     const uint8_t* __restrict__ w, const float* __restrict__ ws, int n, int d, int nb,
     const uint8_t* __restrict__ x, const float* __restrict__ xs, int64_t t, uint16_t* __restrict__ y, int64_t ldy,
     Fp8Grouped grp) {
@@ -132,31 +117,26 @@ __global__ __launch_bounds__(64 * WAVES) void fp8_rows_kernel(
   // 32-bit offsets stay small; rows past the matrix read zero.
   const int crow = lane >> 3, cchunk = 16 * ((lane & 7) ^ crow);
   const int live = min(16 * RO, nout - n0);
-  const __amdgpu_buffer_rsrc_t wr0 = make_rsrc(wm + int64_t(n0) * d, uint32_t(live) * uint32_t(d));
-  const __amdgpu_buffer_rsrc_t wr1 =
-      GLU ? make_rsrc(wm + int64_t(nout + n0) * d, uint32_t(live) * uint32_t(d)) : wr0;
+  const uint8_t* w0p = wm + int64_t(n0) * d;
+  const uint8_t* w1p = GLU ? wm + int64_t(nout + n0) * d : w0p;
+  const uint32_t w_bytes = uint32_t(live) * uint32_t(d);
   uint32_t woff[2 * RO];
 #pragma unroll
-  for (int i = 0; i < 2 * RO; ++i) woff[i] = 8 * i + crow < live ? uint32_t(8 * i + crow) * uint32_t(d) : kOOB8;
+  for (int i = 0; i < 2 * RO; ++i) woff[i] = 8 * i + crow < live ? uint32_t(8 * i + crow) * uint32_t(d) + uint32_t(cchunk) : kOOB8;
 
   // the wave's share of the reduction axis, and its ring
   const int b_begin = nb * wave / WAVES, b_end = nb * (wave + 1) / WAVES;
-  const unsigned char* ring = lds + wave * D * T::kStage;
+  const unsigned char* ring = lds + wave * T::kWave;
   const uint32_t ring_at = lds_addr(ring);
   const int o0 = 128 * col + 16 * (g ^ (col & 7));       // operand chunks g and g + 4 of row col
 
   for (int64_t m0 = m_begin; m0 < m_end; m0 += kRows) {
     // activation rows: dense rows are based at the pass's first row; grouped
     // rows can be anywhere in x (below 2 GiB, checked by the caller)
-    __amdgpu_buffer_rsrc_t xr, sr;
-    if constexpr (GROUPED) {
-      xr = make_rsrc(x, uint32_t(grp.t_x) * uint32_t(d));
-      sr = make_rsrc(xs, uint32_t(grp.t_x) * uint32_t(nb) * 4u);
-    } else {
-      const uint32_t rows = uint32_t(min(int64_t(kRows), m_end - m0));
-      xr = make_rsrc(x + m0 * d, rows * uint32_t(d));
-      sr = make_rsrc(xs + m0 * nb, rows * uint32_t(nb) * 4u);
-    }
+    const int64_t x_first = GROUPED ? 0 : m0;
+    const uint32_t x_rows = GROUPED ? uint32_t(grp.t_x) : uint32_t(min(int64_t(kRows), m_end - m0));
+    const uint8_t* xp = x + x_first * d;
+    const float* sp = xs + x_first * nb;
     auto source = [&](int row) -> int {            // the row of x (dense: of the pass), or -1
       if (m0 + row >= m_end) return -1;
       if constexpr (!GROUPED) return row;
@@ -167,28 +147,42 @@ __global__ __launch_bounds__(64 * WAVES) void fp8_rows_kernel(
 #pragma unroll
     for (int i = 0; i < X8; ++i) {
       const int src = source(8 * i + crow);
-      xoff[i] = src >= 0 ? uint32_t(src) * uint32_t(d) : kOOB8;
+      xoff[i] = src >= 0 ? uint32_t(src) * uint32_t(d) + uint32_t(cchunk) : kOOB8;
     }
 #pragma unroll
     for (int i = 0; i < T::kSc; ++i) {
       const int src = 64 * i + lane < kRows ? source(64 * i + lane) : -1;
       soff[i] = src >= 0 ? uint32_t(src) * uint32_t(nb) * 4u : kOOB8;
     }
-    auto copy = [&](int b, int stage) {
-      const uint32_t at = ring_at + uint32_t(stage * T::kStage);
-      const uint32_t k = uint32_t(kFp8Block * b + cchunk);
-      const uint32_t ko = b < b_end && k < uint32_t(d) ? k : kOOB8;   // past the wave's share: zeros, no reads
-#pragma unroll
-      for (int i = 0; i < 2 * R; ++i) {
-        const uint32_t o = woff[i % (2 * RO)];
-        copy16_to_lds(i < 2 * RO ? wr0 : wr1, (o + ko) | ((o | ko) & kOOB8), at + 1024u * i);
-      }
-#pragma unroll
-      for (int i = 0; i < X8; ++i)
-        copy16_to_lds(xr, (xoff[i] + ko) | ((xoff[i] | ko) & kOOB8), at + T::kX + 1024u * i);
+    // Copy `i` of block b into a stage.  The block's place in a row is the scalar
+    // offset, so the lanes' offsets stay as they are; past the wave's share the
+    // buffers are empty (zeros, no reads, the same count of copies), and in a short
+    // last block the chunks past d are out of range.
+    struct Cursor {
+      bool in;
+      uint32_t at, k, past;
+      uint32_t chunk;   // where the scales of its four blocks are
+    };
+    auto cursor = [&](int b, int stage) {
+      return Cursor{b < b_end, ring_at + uint32_t(stage * T::kStage), uint32_t(kFp8Block * b),
+                    kFp8Block * b + cchunk < d ? 0u : kOOB8,
+                    uint32_t(D * T::kStage + ((b - b_begin) >> 2) % T::kChunks * T::kChunk)};
+    };
+    auto copy = [&](const Cursor& c, int i) {
+      if (i < 2 * R)
+        copy16_to_lds_from(make_rsrc(i < 2 * RO ? w0p : w1p, c.in ? w_bytes : 0u), woff[i % (2 * RO)] | c.past, c.k,
+                           c.at + 1024u * i);
+      else
+        copy16_to_lds_from(make_rsrc(xp, c.in ? x_rows * uint32_t(d) : 0u), xoff[(i - 2 * R) % X8] | c.past, c.k,
+                           c.at + T::kX + 1024u * (i - 2 * R));
+    };
+    // The scales of four blocks at once, before the first of them (rows lie far
+    // apart: a copy costs a cache line for each row, whatever it takes of it).
+    auto copy_scales = [&](const Cursor& c) {
 #pragma unroll
       for (int i = 0; i < T::kSc; ++i)
-        copy4_to_lds(sr, b < b_end ? soff[i] + 4u * uint32_t(b) : kOOB8, at + T::kS + 256u * i);
+        copy16_to_lds_from(make_rsrc(sp, c.in ? x_rows * uint32_t(nb) * 4u : 0u), soff[i], c.k / 32u,
+                           ring_at + c.chunk + 1024u * i);
     };
 
     f32x4_t acc[R][C];
@@ -198,14 +192,25 @@ __global__ __launch_bounds__(64 * WAVES) void fp8_rows_kernel(
       for (int c = 0; c < C; ++c) acc[r][c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
 #pragma unroll
-    for (int i = 0; i < D; ++i) copy(b_begin + i, i);
-    float w0 = ws0[min(b_begin, nb - 1)], w1 = GLU ? ws1[min(b_begin, nb - 1)] : 0.f;
+    for (int i = 0; i < D; ++i) {
+      const Cursor c = cursor(b_begin + i, i);
+      if (i == 0) copy_scales(c);
+#pragma unroll
+      for (int k = 0; k < T::kOps; ++k) copy(c, k);
+    }
+    float w0 = scalar_load(ws0, min(b_begin, nb - 1)), w1 = GLU ? scalar_load(ws1, min(b_begin, nb - 1)) : 0.f;
     int stage = 0;
     for (int b = b_begin; b < b_end; ++b) {
       const int next = min(b + 1, nb - 1);
-      const float w0n = ws0[next], w1n = GLU ? ws1[next] : 0.f;
-      wait_copies<(D - 1) * T::kOps>();   // block b has landed
+      const float w0n = scalar_load(ws0, next), w1n = GLU ? scalar_load(ws1, next) : 0.f;
+      // block b has landed: D - 1 blocks are in flight behind it, and scales if one
+      // of them is the first of four
+      if (((b - b_begin) & 3) + D - 1 >= 4)
+        wait_copies<(D - 1) * T::kOps + T::kSc>();
+      else
+        wait_copies<(D - 1) * T::kOps>();
       const unsigned char* st = ring + stage * T::kStage;
+      const float* sc = reinterpret_cast<const float*>(ring + cursor(b, 0).chunk) + ((b - b_begin) & 3);
       u32x4_t a[R][2], x2[C][2];
       float s[C];
 #pragma unroll
@@ -216,30 +221,46 @@ __global__ __launch_bounds__(64 * WAVES) void fp8_rows_kernel(
       for (int c = 0; c < C; ++c) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) x2[c][h] = *reinterpret_cast<const u32x4_t*>(st + T::kX + 2048 * c + (o0 ^ (64 * h)));
-        s[c] = *reinterpret_cast<const float*>(st + T::kS + 4 * (16 * c + col));
+        s[c] = sc[4 * (16 * c + col)];
       }
-      wait_lds_reads();                   // ... and is in registers: its stage is free
-      copy(b + D, stage);
+      wait_reads();                       // ... and is in registers: its stage is free
+      const Cursor nx = cursor(b + D, stage);
       stage = stage + 1 == D ? 0 : stage + 1;
+      if (((b + D - b_begin) & 3) == 0) copy_scales(nx);
+      if constexpr (T::kExact) {
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
-        const float s0 = s[c] * w0, s1 = GLU ? s[c] * w1 : 0.f;
+        for (int k = 0; k < T::kOps; ++k) copy(nx, k);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           f32x4_t p = {0.f, 0.f, 0.f, 0.f};
-          if constexpr (T::kExact) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-              p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                  e4m3x8_to_bf16(a[r][q >> 1][2 * (q & 1)], a[r][q >> 1][2 * (q & 1) + 1]),
-                  e4m3x8_to_bf16(x2[c][q >> 1][2 * (q & 1)], x2[c][q >> 1][2 * (q & 1) + 1]), p, 0, 0, 0);
-          } else {
-            // formats 0: e4m3; block exponents 0 select the unscaled instruction
-            p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(join(a[r][0], a[r][1]), join(x2[c][0], x2[c][1]), p,
-                                                                 0, 0, 0, 0, 0, 0);
+          for (int q = 0; q < 4; ++q)
+            p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                e4m3x8_to_bf16(a[r][q >> 1][2 * (q & 1)], a[r][q >> 1][2 * (q & 1) + 1]),
+                e4m3x8_to_bf16(x2[0][q >> 1][2 * (q & 1)], x2[0][q >> 1][2 * (q & 1) + 1]), p, 0, 0, 0);
+          const float sv = s[0] * (r < RO ? w0 : w1);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[r][0][i] = __builtin_fmaf(p[i], sv, acc[r][0][i]);
+        }
+      } else {
+        // block sums, their multiply-adds two matrix instructions later, and the
+        // copies spread between them: a copy holds the wave while the memory
+        // pipeline is busy, the matrix unit works on meanwhile
+        constexpr int N = R * C, kAhead = 2;
+        f32x4_t p[kAhead + 1];
+#pragma unroll
+        for (int m = 0; m < N + kAhead; ++m) {
+          if (m < N) p[m % (kAhead + 1)] = mfma_e4m3(join(a[m % R][0], a[m % R][1]), join(x2[m / R][0], x2[m / R][1]));
+#pragma unroll
+          for (int k = 0; k < T::kOps; ++k)
+            if (k * N / T::kOps == m) copy(nx, k);
+          if (m >= kAhead) {
+            const int u = m - kAhead, r = u % R, c = u / R;
+            const float sv = s[c] * (r < RO ? w0 : w1);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[r][c][i] = __builtin_fmaf(p[u % (kAhead + 1)][i], sv, acc[r][c][i]);
           }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[r][c][i] = __builtin_fmaf(p[i], r < RO ? s0 : s1, acc[r][c][i]);
+          __builtin_amdgcn_sched_barrier(0);
         }
       }
       w0 = w0n;
@@ -297,38 +318,45 @@ __global__ __launch_bounds__(64 * WAVES) void fp8_rows_kernel(
   }
 }
 
-template <int WAVES, int R, int X8, int D, bool GROUPED, bool GLU>
+constexpr int kWaves = 4, kDepth = 2;   // a deeper ring or more waves measured no faster anywhere
+
+template <int R, int X8, bool GROUPED, bool GLU>
 int go(const Fp8GemmArgs& a, int max_rows, hipStream_t s) {
-  using T = Fp8Rows<WAVES, R, X8, D, GROUPED, GLU>;
+  using T = Fp8Rows<kWaves, R, X8, kDepth, GROUPED, GLU>;
   const int nout = GLU ? a.n / 2 : a.n, per = 16 * T::RO;
   const Fp8Grouped grp{a.row_index, a.seg_expert, a.seg_offsets, a.n_experts, a.m_total, int(a.t_x), max_rows};
   const unsigned gy = GROUPED ? unsigned(a.n_seg) : unsigned((a.t + 8 * X8 - 1) / (8 * X8));
-  launch_kernel_lds(fp8_rows_kernel<WAVES, R, X8, D, GROUPED, GLU>, dim3(unsigned((nout + per - 1) / per), gy),
-                    dim3(64 * WAVES), T::kLds, s, a.w, a.ws, a.n, a.d, fp8_blocks(a.d), a.x, a.xs, a.t, a.y, a.ldy, grp);
+  launch_kernel_lds(fp8_rows_kernel<kWaves, R, X8, kDepth, GROUPED, GLU>, dim3(unsigned((nout + per - 1) / per), gy),
+                    dim3(64 * kWaves), T::kLds, s, a.w, a.ws, a.n, a.d, fp8_blocks(a.d), a.x, a.xs, a.t, a.y, a.ldy, grp);
   return int(hipGetLastError());
+}
+
+template <int R, bool GROUPED, bool GLU>
+int go(int x8, const Fp8GemmArgs& a, int max_rows, hipStream_t s) {
+  if (x8 == 4) return go<R, 4, GROUPED, GLU>(a, max_rows, s);
+  if (x8 == 8) return go<R, 8, GROUPED, GLU>(a, max_rows, s);
+  if constexpr (R <= 2) {
+    if (x8 == 1) return go<R, 1, GROUPED, GLU>(a, max_rows, s);
+    return go<R, 2, GROUPED, GLU>(a, max_rows, s);
+  }
+  return int(hipErrorInvalidValue);
+}
+
+template <bool GROUPED, bool GLU>
+int go(const Fp8RowsShape& p, const Fp8GemmArgs& a, int max_rows, hipStream_t s) {
+  if (p.r == 4) return go<4, GROUPED, GLU>(p.x8, a, max_rows, s);
+  if constexpr (!GLU)
+    if (p.r == 1) return go<1, GROUPED, GLU>(p.x8, a, max_rows, s);
+  return go<2, GROUPED, GLU>(p.x8, a, max_rows, s);
 }
 
 }  // namespace
 
 int launch_fp8_rows(const Fp8GemmArgs& a, int max_rows, void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const int64_t rows = a.n_seg > 0 ? (max_rows ? std::min(max_rows, a.max_seg_rows) : a.max_seg_rows) : a.t;
-  if (a.n_seg > 0) {
-    if (a.glu) {
-      if (rows <= 8) return go<4, 2, 1, 4, true, true>(a, max_rows, s);
-      if (rows <= 16) return go<4, 2, 2, 4, true, true>(a, max_rows, s);
-      if (rows <= 32) return go<4, 2, 4, 3, true, true>(a, max_rows, s);
-      return go<4, 2, 8, 3, true, true>(a, max_rows, s);
-    }
-    if (rows <= 8) return go<4, 2, 1, 4, true, false>(a, max_rows, s);
-    if (rows <= 16) return go<4, 2, 2, 4, true, false>(a, max_rows, s);
-    if (rows <= 32) return go<4, 2, 4, 3, true, false>(a, max_rows, s);
-    return go<4, 2, 8, 3, true, false>(a, max_rows, s);
-  }
-  if (rows <= 8) return go<4, 2, 1, 4, false, false>(a, 0, s);
-  if (rows <= 16) return go<4, 2, 2, 4, false, false>(a, 0, s);
-  if (rows <= 32) return go<4, 2, 4, 3, false, false>(a, 0, s);
-  return go<4, 2, 8, 3, false, false>(a, 0, s);
+  const Fp8RowsShape p = fp8_rows_shape(a, max_rows);
+  if (a.n_seg == 0) return go<false, false>(p, a, 0, s);
+  return a.glu ? go<true, true>(p, a, max_rows, s) : go<true, false>(p, a, max_rows, s);
 }
 
 }  // namespace qmm

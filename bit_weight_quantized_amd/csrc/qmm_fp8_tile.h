@@ -1,0 +1,164 @@
+// What the LDS tile kernels of the block-scaled e4m3 product share: waits, the
+// place of a workgroup's tile, and the rows that it reads.
+#pragma once
+
+#include "qmm_fp8.h"
+#include "qmm_fp8_device.h"
+
+namespace qmm {
+
+// Waits and barriers as fences of their own (the copies are asm): at most N
+// copies of the wave in flight; every LDS read of the wave done; end of a phase.
+template <int N>
+__device__ __forceinline__ void wait_copies() { asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory"); }
+__device__ __forceinline__ void wait_reads() { asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory"); }
+__device__ __forceinline__ void phase_end() {
+  asm volatile("" : : : "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" : : : "memory");
+}
+
+// Arguments of the kernels, as they come from the entry points.
+struct Fp8TileArgs {
+  const uint8_t* w;
+  const float* ws;
+  int n, d, nb;
+  const uint8_t* x;
+  const float* xs;
+  int64_t t;
+  uint16_t* y;
+  int64_t ldy;
+  int tiles_n;
+  // grouped
+  const int32_t* row_index;
+  const int32_t* seg_expert;
+  const int32_t* seg_offsets;
+  int n_experts, n_seg, m_total, t_x;
+  int skip_rows;          // segments of up to so many rows are left out
+};
+
+// A workgroup's tile: rows [m0, m_end) of the grouped or dense rows, output
+// columns from n0, the matrix of its expert.
+struct Fp8Place {
+  int64_t m0, m_end;
+  int n0;
+  bool bad_expert;
+  const uint8_t* w;
+  const float* ws;
+  int sb;                 // scale rows of the gate half
+};
+
+// The tile of this workgroup, kT rows by kOut columns; false where the grid's
+// bound has more row tiles than there are.  XCD id mod 8 takes a contiguous run
+// of tiles, in blocks of 8 weight tiles by all activation tiles, activation
+// tiles slowest: the 32 workgroups at work on an XCD share 8 weight and 4
+// activation tiles in its L2.
+template <int kT, int kOut, bool GROUPED, bool GLU>
+__device__ __forceinline__ bool fp8_place(const Fp8TileArgs& a, Fp8Place& p) {
+  const int total = gridDim.x;
+  const int xcd = blockIdx.x & 7, share = total >> 3, extra = total & 7;
+  const int id = xcd * share + min(xcd, extra) + (blockIdx.x >> 3);
+  const int tiles_t = total / a.tiles_n;
+  const int strip = id / (8 * tiles_t), in_strip = id - strip * 8 * tiles_t;
+  const int width = min(8, a.tiles_n - 8 * strip);
+  const int tt = in_strip / width, tn = 8 * strip + in_strip - tt * width;
+  const int nout = GLU ? a.n / 2 : a.n;
+  p.n0 = tn * kOut;
+  p.bad_expert = false;
+  p.w = a.w;
+  p.ws = a.ws;
+  p.sb = GLU ? (nout + kFp8Block - 1) / kFp8Block : 0;
+  if constexpr (!GROUPED) {
+    p.m0 = int64_t(tt) * kT;
+    p.m_end = min(a.t, p.m0 + kT);
+    return true;
+  }
+  // the tt-th row tile of the segments longer than skip_rows; every wave looks
+  // for itself, 64 segments at a time
+  const int lane = threadIdx.x & 63;
+  int before = 0;
+  for (int s0 = 0; s0 < a.n_seg; s0 += 64) {
+    const int s = s0 + lane;
+    int lo = 0, hi = 0;
+    if (s < a.n_seg) {
+      lo = min(max(a.seg_offsets[s], 0), a.m_total);
+      hi = min(max(a.seg_offsets[s + 1], lo), a.m_total);
+    }
+    const int tiles = hi - lo > a.skip_rows ? (hi - lo + kT - 1) / kT : 0;
+    int incl = tiles;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int up = __shfl_up(incl, o);
+      if (lane >= o) incl += up;
+    }
+    const int at = before + incl - tiles;
+    const uint64_t who = __ballot(tt >= at && tt < at + tiles);
+    if (who) {
+      const int src = __builtin_ctzll(who);
+      p.m0 = __builtin_amdgcn_readlane(lo + (tt - at) * kT, src);
+      p.m_end = min(p.m0 + kT, int64_t(__builtin_amdgcn_readlane(hi, src)));
+      const int e = a.seg_expert[s0 + src];
+      p.bad_expert = e < 0 || e >= a.n_experts;
+      if (!p.bad_expert) {
+        p.w += int64_t(e) * a.n * a.d;
+        p.ws += int64_t(e) * (GLU ? 2 * p.sb : (a.n + kFp8Block - 1) / kFp8Block) * a.nb;
+      }
+      return true;
+    }
+    before += __builtin_amdgcn_readlane(incl, 63);
+  }
+  return false;
+}
+
+// Activation rows as the copies address them: dense rows from the tile's first
+// row, grouped rows anywhere in x (below 2 GiB, checked by the caller).
+template <bool GROUPED>
+struct Fp8Source {
+  __amdgpu_buffer_rsrc_t x, s;
+  __device__ __forceinline__ Fp8Source(const Fp8TileArgs& a, const Fp8Place& p) {
+    const uint32_t rows = GROUPED ? uint32_t(a.t_x) : uint32_t(p.m_end - p.m0);
+    const int64_t first = GROUPED ? 0 : p.m0;
+    x = make_rsrc(a.x + first * a.d, rows * uint32_t(a.d));
+    s = make_rsrc(a.xs + first * a.nb, rows * uint32_t(a.nb) * 4u);
+  }
+  // row of the tile -> row of the buffers; -1 past the tile, or (grouped) for a
+  // bad row or expert
+  __device__ __forceinline__ int operator()(const Fp8TileArgs& a, const Fp8Place& p, int row) const {
+    if (p.m0 + row >= p.m_end) return -1;
+    if constexpr (!GROUPED) return row;
+    const int src = a.row_index ? a.row_index[p.m0 + row] : int(p.m0 + row);
+    return p.bad_expert || src < 0 || src >= a.t_x ? -1 : src;
+  }
+};
+
+__device__ __forceinline__ i32x8_t join(const u32x4_t a, const u32x4_t b) {
+  i32x8_t r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    r[i] = int(a[i]);
+    r[4 + i] = int(b[i]);
+  }
+  return r;
+}
+
+// formats 0: e4m3; block exponents 0 select the unscaled instruction
+__device__ __forceinline__ f32x4_t mfma_e4m3(const i32x8_t a, const i32x8_t b) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+}
+
+// Stores a lane's four consecutive columns c .. c + 3 of one output row.
+__device__ __forceinline__ void store4(uint16_t* row, int c, int nout, const float* f, bool bad, bool wide) {
+  uint16_t v[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = bad ? uint16_t(0x7FC0) : f32_to_bf16(f[e]);
+  if (wide && c + 4 <= nout) {
+    *reinterpret_cast<u32x2_t*>(row + c) =
+        u32x2_t{uint32_t(v[0]) | uint32_t(v[1]) << 16, uint32_t(v[2]) | uint32_t(v[3]) << 16};
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (c + e < nout) row[c + e] = v[e];
+  }
+}
+
+}  // namespace qmm

@@ -10,19 +10,32 @@
 // product and the sum over the blocks is one fp32 multiply-add per value, which
 // the vector unit does while the matrix unit works on the next block sums.
 //
-// Both tiles go global -> LDS without passing registers, double-buffered: the
-// copies of step k + 1 are in flight during the whole of step k, one barrier a
-// step.  A row's eight 16-byte chunks are stored at chunk ^ (row mod 8), done on
-// the global side of the copy, so the operand reads of eight neighbouring rows
-// fall into different banks.
+// Both tiles go global -> LDS without passing registers, double-buffered.  A
+// row's eight 16-byte chunks are stored at chunk ^ (row mod 8), done on the
+// global side of the copy, so the operand reads of eight neighbouring rows fall
+// into different banks.
+//
+// Eight waves, two on every SIMD, work in opposite phases: while one reads the
+// operands of half a step from LDS, the other multiplies, with a barrier between
+// phases, so the matrix unit never waits for LDS.  A wave's step is
+//   L1: read its weights and the first half of its activations   C1: multiply
+//   L2: read the second half of its activations                  C2: multiply
+// and the waves of the second group run one phase behind.  A part of the tiles
+// that both groups have read is filled again at once: L1 of step b issues the
+// second half of the activations of step b + 1, L2 the weights and the first half
+// of step b + 2, so every copy has four phases to land, counted by vmcnt: after
+// the copies that a phase needs, each wave has issued one set of each, kAfter
+// copies, and never waits for the last ones.
 #include <hip/hip_runtime.h>
 
 #include "qmm_fp8.h"
 #include "qmm_fp8_device.h"
+#include "qmm_fp8_tile.h"
 #include "qmm_launch.h"
 #include "qmm_lds_copy.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace qmm {
 namespace {
@@ -36,136 +49,55 @@ struct Fp8Tile {
   static constexpr int kT = 16 * TS * WT;              // activation rows
   static constexpr int kN = 16 * WS * WN;              // weight rows
   static constexpr int kOut = GLU ? kN / 2 : kN;       // output columns
-  static constexpr int kStage = (kT + kN) * 128 + kT * 4;
-  static_assert((kT + kN) / 8 % kWaves == 0 && kT % 64 == 0, "whole copies per wave");
-  static constexpr int kXCopies = kT / 8 / kWaves, kWCopies = kN / 8 / kWaves;
+  static constexpr int kStage = (kT + kN) * 128;       // both tiles of a step
+  static constexpr int kScales = kT * 16;              // activation scales of four steps
+  static constexpr int kLds = 2 * kStage + 2 * kScales;
+  static_assert(kT / 16 % kWaves == 0 && kN / 8 % kWaves == 0 && kT / 64 <= kWaves, "whole copies per wave");
+  static constexpr int kXCopies = kT / 16 / kWaves, kWCopies = kN / 8 / kWaves;   // of half the activations
+  static constexpr int kAfter = 2 * kXCopies + kWCopies;
 };
 
 template <int TS, int WS, int WT, int WN, bool GROUPED, bool GLU>
-__global__ __launch_bounds__(64 * WT * WN) void fp8_tile_kernel(
-    const uint8_t* __restrict__ w, const float* __restrict__ ws, int n, int d, int nb, const uint8_t* __restrict__ x,
-    const float* __restrict__ xs, int64_t t, uint16_t* __restrict__ y, int64_t ldy, int tiles_n,
-    const int32_t* __restrict__ row_index, const int32_t* __restrict__ seg_expert,
-    const int32_t* __restrict__ seg_offsets, int n_experts, int n_seg, int m_total, int t_x, int skip_rows) {
+__global__ __launch_bounds__(64 * WT * WN) void fp8_tile_kernel(Fp8TileArgs A) {
   using T = Fp8Tile<TS, WS, WT, WN, GROUPED, GLU>;
   extern __shared__ __attribute__((aligned(1024))) unsigned char lds[];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, g = lane >> 4;
   const int wt = wave % WT, wn = wave / WT;
-  const int nout = GLU ? n / 2 : n;
-
-  // tile: XCD id mod 8 takes a contiguous run of tiles, activation tiles
-  // fastest, so the workgroups of an XCD share weight rows in its L2
-  const int total = gridDim.x;
-  const int xcd = blockIdx.x & 7, share = total >> 3, extra = total & 7;
-  const int id = xcd * share + min(xcd, extra) + (blockIdx.x >> 3);
-  const int tiles_t = total / tiles_n;
-  const int tn = id / tiles_t, tt = id % tiles_t;
-  const int n0 = tn * T::kOut;
-
-  int64_t m0, m_end;
-  bool bad_expert = false;
-  const uint8_t* wm = w;
-  const float* wsm = ws;
-  const int sb = GLU ? (nout + kFp8Block - 1) / kFp8Block : 0;
-  if constexpr (GROUPED) {
-    // the tt-th row tile of the segments longer than skip_rows
-    __shared__ int32_t found[3];
-    if (threadIdx.x < 64) {
-      int before = 0, hit = -1, first = 0, end = 0;
-      for (int s0 = 0; s0 < n_seg; s0 += 64) {
-        const int s = s0 + lane;
-        int lo = 0, hi = 0;
-        if (s < n_seg) {
-          lo = min(max(seg_offsets[s], 0), m_total);
-          hi = min(max(seg_offsets[s + 1], lo), m_total);
-        }
-        const int tiles = hi - lo > skip_rows ? (hi - lo + T::kT - 1) / T::kT : 0;
-        int incl = tiles;
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-          const int up = __shfl_up(incl, o);
-          if (lane >= o) incl += up;
-        }
-        const int at = before + incl - tiles;
-        const bool mine = tt >= at && tt < at + tiles;
-        const uint64_t who = __ballot(mine);
-        if (who) {
-          const int src = __builtin_ctzll(who);
-          hit = s0 + src;
-          first = __shfl(lo + (tt - at) * T::kT, src);
-          end = __shfl(hi, src);
-          break;
-        }
-        before += __shfl(incl, 63);
-      }
-      if (lane == 0) {
-        found[0] = hit;
-        found[1] = first;
-        found[2] = end;
-      }
-    }
-    __syncthreads();
-    const int s = found[0];
-    if (s < 0) return;                                  // fewer tiles than the grid's bound
-    m0 = found[1];
-    m_end = found[2];
-    const int e = seg_expert[s];
-    bad_expert = e < 0 || e >= n_experts;
-    if (!bad_expert) {
-      wm += int64_t(e) * n * d;
-      wsm += int64_t(e) * (GLU ? 2 * sb : (n + kFp8Block - 1) / kFp8Block) * nb;
-    }
-  } else {
-    m0 = int64_t(tt) * T::kT;
-    m_end = min(t, m0 + T::kT);
-  }
+  const int d = A.d, nb = A.nb, nout = GLU ? A.n / 2 : A.n;
+  Fp8Place P;
+  if (!fp8_place<T::kT, T::kOut, GROUPED, GLU>(A, P)) return;
+  const int n0 = P.n0;
 
   // ---- copies: row 8·i + lane / 8 of a copy, LDS chunk lane % 8 holding the
   // global chunk (lane % 8) ^ (row % 8)
   const int crow = lane >> 3, cchunk = (lane & 7) ^ crow;
-  uint32_t xoff[T::kXCopies], woff[T::kWCopies], soff = kOOB8;
-  __amdgpu_buffer_rsrc_t xr, sr;
-  auto source = [&](int64_t at) -> int {                // grouped: the row of x, or -1
-    if (at >= m_end || bad_expert) return -1;
-    const int src = row_index ? row_index[at] : int(at);
-    return src < 0 || src >= t_x ? -1 : src;
+  uint32_t xoff[2][T::kXCopies], woff[T::kWCopies], soff = kOOB8;
+  const Fp8Source<GROUPED> src(A, P);
+  // half h of the activations: the blocks H·h .. H·h + H - 1 of every wave row
+  auto x_row = [&](int h, int i) {                      // first row of a wave's i-th copy
+    const int c = wave * T::kXCopies + i;
+    return 16 * TS * (c / TS) + 8 * TS * h + 8 * (c % TS);
   };
-  if constexpr (GROUPED) {
-    xr = make_rsrc(x, uint32_t(t_x) * uint32_t(d));
-    sr = make_rsrc(xs, uint32_t(t_x) * uint32_t(nb) * 4u);
-  } else {
-    const uint32_t rows = uint32_t(m_end - m0);
-    xr = make_rsrc(x + m0 * d, rows * uint32_t(d));
-    sr = make_rsrc(xs + m0 * nb, rows * uint32_t(nb) * 4u);
-  }
 #pragma unroll
-  for (int i = 0; i < T::kXCopies; ++i) {
-    const int row = 8 * (wave * T::kXCopies + i) + crow;
-    if constexpr (GROUPED) {
-      const int src = source(m0 + row);
-      xoff[i] = src >= 0 ? uint32_t(src) * uint32_t(d) : kOOB8;
-    } else {
-      xoff[i] = m0 + row < m_end ? uint32_t(row) * uint32_t(d) : kOOB8;
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int i = 0; i < T::kXCopies; ++i) {
+      const int row = src(A, P, x_row(h, i) + crow);
+      xoff[h][i] = row >= 0 ? uint32_t(row) * uint32_t(d) : kOOB8;
     }
-  }
   if (wave < T::kT / 64) {                              // scales of 64 rows a wave
-    const int row = 64 * wave + lane;
-    if constexpr (GROUPED) {
-      const int src = source(m0 + row);
-      soff = src >= 0 ? uint32_t(src) * uint32_t(nb) * 4u : kOOB8;
-    } else {
-      soff = m0 + row < m_end ? uint32_t(row) * uint32_t(nb) * 4u : kOOB8;
-    }
+    const int row = src(A, P, 64 * wave + lane);
+    soff = row >= 0 ? uint32_t(row) * uint32_t(nb) * 4u : kOOB8;
   }
   // weight rows: a wave's WS blocks are consecutive LDS rows; with the
   // activation their upper half comes from the up rows (8·WS rows are whole
   // copies, so a copy reads one of the two halves)
   const int live = min(T::kOut, nout - n0);
-  const __amdgpu_buffer_rsrc_t wr0 = make_rsrc(wm + int64_t(n0) * d, uint32_t(live) * uint32_t(d));
+  const __amdgpu_buffer_rsrc_t wr0 = make_rsrc(P.w + int64_t(n0) * d, uint32_t(live) * uint32_t(d));
   const __amdgpu_buffer_rsrc_t wr1 =
-      GLU ? make_rsrc(wm + int64_t(nout + n0) * d, uint32_t(live) * uint32_t(d)) : wr0;
+      GLU ? make_rsrc(P.w + int64_t(nout + n0) * d, uint32_t(live) * uint32_t(d)) : wr0;
 #pragma unroll
   for (int i = 0; i < T::kWCopies; ++i) {
     int row = 8 * (wave * T::kWCopies + i) + crow;
@@ -173,24 +105,33 @@ __global__ __launch_bounds__(64 * WT * WN) void fp8_tile_kernel(
     woff[i] = row < live ? uint32_t(row) * uint32_t(d) : kOOB8;
   }
   const uint32_t base = lds_addr(lds);
-  auto copy = [&](int b, int stage) {
-    const uint32_t at = base + uint32_t(stage) * T::kStage;
+  // a block past the last is all zeros and reads nothing: the counts stay the same
+  auto at_block = [&](int b) {
     const uint32_t k = uint32_t(kFp8Block * b + 16 * cchunk);
-    const uint32_t ko = k < uint32_t(d) ? k : kOOB8;
+    return k < uint32_t(d) ? k : kOOB8;
+  };
+  auto copy_x = [&](int b, int h) {
+    const uint32_t at = base + uint32_t(b & 1) * T::kStage, ko = at_block(b);
 #pragma unroll
     for (int i = 0; i < T::kXCopies; ++i)
-      copy16_to_lds(xr, (xoff[i] + ko) | ((xoff[i] | ko) & kOOB8), at + 1024u * uint32_t(wave * T::kXCopies + i));
+      copy16_to_lds(src.x, (xoff[h][i] + ko) | ((xoff[h][i] | ko) & kOOB8), at + 128u * uint32_t(x_row(h, i)));
+  };
+  auto copy_w = [&](int b) {
+    const uint32_t at = base + uint32_t(b & 1) * T::kStage + 128u * T::kT, ko = at_block(b);
+    // scales of four steps at a time, 64 rows a wave (rows lie far apart: a copy
+    // costs a cache line for each row, whatever it takes of it)
+    if ((b & 3) == 0 && wave < T::kT / 64)
+      copy16_to_lds(src.s, (soff + 4u * uint32_t(b)) | (soff & kOOB8),
+                    base + 2u * T::kStage + uint32_t(b >> 2 & 1) * T::kScales + 1024u * uint32_t(wave));
 #pragma unroll
     for (int i = 0; i < T::kWCopies; ++i)
       copy16_to_lds(GLU && ((wave * T::kWCopies + i) / WS & 1) ? wr1 : wr0, (woff[i] + ko) | ((woff[i] | ko) & kOOB8),
-                    at + 128u * T::kT + 1024u * uint32_t(wave * T::kWCopies + i));
-    if (wave < T::kT / 64)
-      copy4_to_lds(sr, soff + 4u * uint32_t(b), at + 128u * (T::kT + T::kN) + 256u * uint32_t(wave));
+                    at + 1024u * uint32_t(wave * T::kWCopies + i));
   };
 
   // ---- operands
-  const float* ws0 = wsm + int64_t((n0 + (GLU ? 8 : 16) * WS * wn) / kFp8Block) * nb;
-  const float* ws1 = wsm + int64_t(sb + (n0 + 8 * WS * wn) / kFp8Block) * nb;
+  const float* ws0 = P.ws + int64_t((n0 + (GLU ? 8 : 16) * WS * wn) / kFp8Block) * nb;
+  const float* ws1 = P.ws + int64_t(P.sb + (n0 + 8 * WS * wn) / kFp8Block) * nb;
   const int o0 = 16 * (g ^ (col & 7));
   f32x4_t acc[TS][WS];
 #pragma unroll
@@ -198,77 +139,107 @@ __global__ __launch_bounds__(64 * WT * WN) void fp8_tile_kernel(
 #pragma unroll
     for (int j = 0; j < WS; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-  copy(0, 0);
-  float w0 = ws0[0], w1 = GLU ? ws1[0] : 0.f;
-  for (int b = 0; b < nb; ++b) {
-    __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
-    __syncthreads();                                    // step b copied; step b - 1 read by every wave
-    const int next = min(b + 1, nb - 1);
-    if (b + 1 < nb) copy(b + 1, (b + 1) & 1);
-    const float w0n = ws0[next], w1n = GLU ? ws1[next] : 0.f;
-    const unsigned char* st = lds + (b & 1) * T::kStage;
-    const unsigned char* xt = st + 128 * (16 * TS * wt + col);
-    const unsigned char* wt_ = st + 128 * (T::kT + 16 * WS * wn + col);
-    const float* sc = reinterpret_cast<const float*>(st + 128 * (T::kT + T::kN)) + 16 * TS * wt + col;
-    auto operand = [&](const unsigned char* p) {
-      const u32x4_t lo = *reinterpret_cast<const u32x4_t*>(p + o0);
-      const u32x4_t hi = *reinterpret_cast<const u32x4_t*>(p + (o0 ^ 64));
-      i32x8_t r;
+  constexpr int H = TS / 2;                             // activation blocks of a half step
+  i32x8_t a[WS], bx[H];
+  float sx[H];
+  const unsigned char* st = lds;
+  const float* sc = nullptr;
+  auto operand = [&](const unsigned char* p) {
+    return join(*reinterpret_cast<const u32x4_t*>(p + o0), *reinterpret_cast<const u32x4_t*>(p + (o0 ^ 64)));
+  };
+  auto read_w = [&]() {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        r[i] = int(lo[i]);
-        r[4 + i] = int(hi[i]);
-      }
-      return r;
-    };
-    i32x8_t a[WS];
+    for (int j = 0; j < WS; ++j) a[j] = operand(st + 128 * (T::kT + 16 * WS * wn + col) + 2048 * j);
+  };
+  auto read_x = [&](int half) {
 #pragma unroll
-    for (int j = 0; j < WS; ++j) a[j] = operand(wt_ + 2048 * j);
+    for (int i = 0; i < H; ++i) {
+      bx[i] = operand(st + 128 * (16 * TS * wt + col) + 2048 * (H * half + i));
+      sx[i] = sc[64 * (H * half + i)];
+    }
+  };
+  // block sums and their multiply-adds, kAhead matrix instructions apart: the
+  // order is fixed, since the scheduler would start all the block sums first and
+  // keep them in registers that the accumulators need
+  auto multiply = [&](auto half, float w0, float w1) {
+    constexpr int h = decltype(half)::value, kAhead = 4, N = H * WS;
+    f32x4_t p[kAhead + 1];
 #pragma unroll
-    for (int i = 0; i < TS; ++i) {
-      const i32x8_t bx = operand(xt + 2048 * i);
-      const float s = sc[16 * i];
-      const float s0 = s * w0, s1 = GLU ? s * w1 : 0.f;
-#pragma unroll
-      for (int j = 0; j < WS; ++j) {
-        const f32x4_t p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a[j], bx, f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0,
-                                                                           0, 0, 0, 0);
+    for (int m = 0; m < N + kAhead; ++m) {
+      if (m < N)
+        p[m % (kAhead + 1)] = mfma_e4m3(a[m % WS], bx[m / WS]);
+      if (m >= kAhead) {
+        const int u = m - kAhead, i = u / WS, j = u % WS;
+        const float s = sx[i] * (GLU && j >= WS / 2 ? w1 : w0);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          acc[i][j][e] = __builtin_fmaf(p[e], GLU && j >= WS / 2 ? s1 : s0, acc[i][j][e]);
+          acc[H * h + i][j][e] = __builtin_fmaf(p[u % (kAhead + 1)][e], s, acc[H * h + i][j][e]);
+        asm volatile("" : "+v"(acc[H * h + i][j]));      // and not later
       }
+      __builtin_amdgcn_sched_barrier(0);
     }
+  };
+  const bool behind = wave >= T::kWaves / 2;            // the second group: one phase later
+
+  copy_w(0);
+  copy_x(0, 0);
+  copy_x(0, 1);
+  copy_w(1);
+  copy_x(1, 0);
+  wait_copies<T::kAfter>();
+  phase_end();
+  if (behind) phase_end();
+  float w0 = scalar_load(ws0, 0), w1 = GLU ? scalar_load(ws1, 0) : 0.f;
+  for (int b = 0; b < nb; ++b) {
+    st = lds + (b & 1) * T::kStage;
+    sc = reinterpret_cast<const float*>(lds + 2 * T::kStage + (b >> 2 & 1) * T::kScales) +
+         4 * (16 * TS * wt + col) + (b & 3);
+    const int next = min(b + 1, nb - 1);
+    const float w0n = scalar_load(ws0, next), w1n = GLU ? scalar_load(ws1, next) : 0.f;
+    __builtin_amdgcn_s_setprio(1);                      // the reader's few instructions first
+    read_w();
+    read_x(0);
+    copy_x(b + 1, 1);                                   // both groups have read that half of step b - 1
+    __builtin_amdgcn_s_setprio(0);
+    wait_reads();
+    // second half of step b (a scale copy of this wave may be among the later ones)
+    if (b % 4 == 3 && wave < T::kT / 64) wait_copies<T::kAfter + 1>();
+    else wait_copies<T::kAfter>();
+    phase_end();
+    multiply(std::integral_constant<int, 0>{}, w0, w1);
+    phase_end();
+    __builtin_amdgcn_s_setprio(1);
+    read_x(1);
+    copy_w(b + 2);                                      // both groups have read these of step b
+    copy_x(b + 2, 0);
+    __builtin_amdgcn_s_setprio(0);
+    wait_reads();
+    // weights and first half of step b + 1
+    if (b % 4 == 2 && wave < T::kT / 64) wait_copies<T::kAfter + 1>();
+    else wait_copies<T::kAfter>();
+    phase_end();
+    multiply(std::integral_constant<int, 1>{}, w0, w1);
+    phase_end();
     w0 = w0n;
     w1 = w1n;
   }
+  if (!behind) phase_end();                             // the groups' barrier counts match
+  wait_copies<0>();
 
   // ---- epilogue: lane (col, g) holds output columns 4g .. 4g + 3 of activation row col
-  const bool wide = (ldy & 3) == 0 && (reinterpret_cast<uintptr_t>(y) & 7) == 0;
+  const bool wide = (A.ldy & 3) == 0 && (reinterpret_cast<uintptr_t>(A.y) & 7) == 0;
   constexpr int WO = GLU ? WS / 2 : WS;
 #pragma unroll
   for (int i = 0; i < TS; ++i) {
-    const int64_t row = m0 + 16 * (TS * wt + i) + col;
-    if (row >= m_end) continue;
-    const bool bad = GROUPED && source(row) < 0;
+    const int row = 16 * (TS * wt + i) + col;
+    if (P.m0 + row >= P.m_end) continue;
+    const bool bad = GROUPED && src(A, P, row) < 0;
 #pragma unroll
     for (int j = 0; j < WO; ++j) {
-      const int c = n0 + 16 * (WO * wn + j) + 4 * g;
-      uint16_t v[4];
+      float f[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float f = acc[i][j][e];
-        if constexpr (GLU) f = silu(f) * acc[i][WO + j][e];
-        v[e] = bad ? uint16_t(0x7FC0) : f32_to_bf16(f);
-      }
-      uint16_t* to = y + row * ldy + c;
-      if (wide && c + 4 <= nout) {
-        *reinterpret_cast<u32x2_t*>(to) =
-            u32x2_t{uint32_t(v[0]) | uint32_t(v[1]) << 16, uint32_t(v[2]) | uint32_t(v[3]) << 16};
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (c + e < nout) to[e] = v[e];
-      }
+      for (int e = 0; e < 4; ++e) f[e] = GLU ? silu(acc[i][j][e]) * acc[i][WS - WO + j][e] : acc[i][j][e];
+      store4(A.y + (P.m0 + row) * A.ldy, n0 + 16 * (WO * wn + j) + 4 * g, nout, f, bad, wide);
     }
   }
 }
@@ -277,7 +248,7 @@ template <int TS, int WS, int WT, int WN, bool GROUPED, bool GLU>
 int go(const Fp8GemmArgs& a, int skip_rows, hipStream_t s) {
   using T = Fp8Tile<TS, WS, WT, WN, GROUPED, GLU>;
   auto kernel = fp8_tile_kernel<TS, WS, WT, WN, GROUPED, GLU>;
-  const size_t bytes = 2 * size_t(T::kStage);
+  const size_t bytes = T::kLds;
   const int nout = GLU ? a.n / 2 : a.n;
   const int64_t tiles_n = (int64_t(nout) + T::kOut - 1) / T::kOut;
   // grouped: no more row tiles than whole tiles of rows and one part tile a segment
@@ -285,22 +256,47 @@ int go(const Fp8GemmArgs& a, int skip_rows, hipStream_t s) {
                                   : (a.t + T::kT - 1) / T::kT;
   if (tiles_t == 0) return 0;
   if (tiles_n * tiles_t >= (int64_t(1) << 22)) return int(hipErrorInvalidValue);
-  launch_kernel_lds(kernel, dim3(unsigned(tiles_n * tiles_t)), dim3(64 * T::kWaves), bytes, s, a.w, a.ws, a.n, a.d,
-                    fp8_blocks(a.d), a.x, a.xs, a.t, a.y, a.ldy, int(tiles_n), a.row_index, a.seg_expert,
-                    a.seg_offsets, a.n_experts, a.n_seg, a.m_total, int(a.t_x), skip_rows);
+  const Fp8TileArgs k{a.w, a.ws, a.n, a.d, fp8_blocks(a.d), a.x, a.xs, a.t, a.y, a.ldy, int(tiles_n), a.row_index,
+                      a.seg_expert, a.seg_offsets, a.n_experts, a.n_seg, a.m_total, int(a.t_x), skip_rows};
+  launch_kernel_lds(kernel, dim3(unsigned(tiles_n * tiles_t)), dim3(64 * T::kWaves), bytes, s, k);
   return int(hipGetLastError());
 }
 
 }  // namespace
 
-int launch_fp8_tile(const Fp8GemmArgs& a, int skip_rows, void* stream) {
+namespace {
+
+template <bool GROUPED, bool GLU>
+int go(bool large, const Fp8GemmArgs& a, int skip_rows, hipStream_t s) {
+  return large ? go<8, 4, 2, 4, GROUPED, GLU>(a, skip_rows, s) : go<4, 2, 2, 4, GROUPED, GLU>(a, skip_rows, s);
+}
+
+}  // namespace
+
+int launch_fp8_tile(const Fp8GemmArgs& a, bool large, int skip_rows, void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (a.n_seg > 0) return a.glu ? go<8, 4, 2, 4, true, true>(a, skip_rows, s) : go<8, 4, 2, 4, true, false>(a, skip_rows, s);
-  return go<8, 4, 2, 4, false, false>(a, 0, s);
+  if (a.n_seg == 0) return go<false, false>(large, a, 0, s);
+  return a.glu ? go<true, true>(large, a, skip_rows, s) : go<true, false>(large, a, skip_rows, s);
 }
 
 int launch_fp8_product(const Fp8GemmArgs& a, void* stream) {
-  if (a.n_seg == 0) return a.t <= kFp8RowsMax ? launch_fp8_rows(a, 0, stream) : launch_fp8_tile(a, 0, stream);
+  if (a.n_seg == 0) {
+    // Estimates in us of the three kernels, from the time of one step of one
+    // workgroup: few-row 0.7, 0.85 or 1.3 for its waves' blocks (r = 1, 2, 4), 128 x
+    // 128 tiles 0.66 and 0.1 for each round, 256 x 256 tiles 1.7, times the rounds of
+    // workgroups that 256 CUs take.  Measured on either side: 13824 x 5120 with 128
+    // rows 32.3 us few-row, 36.0 (128), with 192 rows 45.2, 36.2; with 512 rows 54.7
+    // (128), 66.7 (256), with 1024 rows 97.0, 72.0; 4096 x 7168 with 512 rows 39.8
+    // few-row, 42.2 (128), with 1024 rows 43.6 (128), 78.5 (256).
+    auto rounds = [](int64_t workgroups) { return double((workgroups + 255) / 256); };
+    auto tiles = [&](int side) { return ((a.t + side - 1) / side) * ((int64_t(a.n) + side - 1) / side); };
+    const Fp8RowsShape p = fp8_rows_shape(a, 0);
+    const int nb = fp8_blocks(a.d);
+    const double few = ((nb + 3) / 4) * (p.r == 4 ? 1.3 : p.r == 2 ? 0.85 : 0.7) * rounds(p.workgroups);
+    const double small = nb * (0.66 * rounds(tiles(128)) + 0.1), large = nb * 1.7 * rounds(tiles(256));
+    if (a.t <= kFp8RowsMax || (few <= small && few <= large)) return launch_fp8_rows(a, 0, stream);
+    return launch_fp8_tile(a, large < small, 0, stream);
+  }
   if (a.max_seg_rows <= kFp8RowsMax) return launch_fp8_rows(a, 0, stream);
   // two launches that split the segments on the device; armed events: the
   // start with the first, the stop with the second
@@ -308,7 +304,8 @@ int launch_fp8_product(const Fp8GemmArgs& a, void* stream) {
   arm_profile_events({pe.start, nullptr});
   const int err = launch_fp8_rows(a, kFp8RowsMax, stream);
   arm_profile_events({nullptr, err ? nullptr : pe.stop});
-  return err ? err : launch_fp8_tile(a, kFp8RowsMax, stream);
+  if (err) return err;
+  return launch_fp8_tile(a, int64_t(a.m_total) >= int64_t(192) * a.n_seg, kFp8RowsMax, stream);
 }
 
 }  // namespace qmm
