@@ -129,11 +129,10 @@ def load():
 
 
 def _ptr(v):
-    if v is None:
-        return None
-    if isinstance(v, int):
+    try:
+        return v.data_ptr()
+    except AttributeError:   # None or an address
         return v
-    return v.data_ptr()
 
 
 def _nbytes(v):
@@ -144,12 +143,19 @@ def _nbytes(v):
     return v.numel() * v.element_size()
 
 
+_raw_stream = None   # (current stream's handle, current device) of torch, once a GPU was seen
+
+
 def _stream(s):
+    global _raw_stream
     if s is None:
-        import torch
-        if torch.cuda.is_available():
-            return torch.cuda.current_stream().cuda_stream
-        return None
+        if _raw_stream is None:
+            import torch
+            if not torch.cuda.is_available():
+                return None
+            _raw_stream = (torch._C._cuda_getCurrentRawStream, torch.cuda.current_device)
+        handle, device = _raw_stream
+        return handle(device())
     if isinstance(s, int):
         return s
     return s.cuda_stream
