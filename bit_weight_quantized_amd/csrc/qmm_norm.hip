@@ -56,85 +56,99 @@ __device__ __forceinline__ F8 load_f32x8(const float* p) {
 // the waves' sums in wave order.
 template <int WAVES>
 __device__ __forceinline__ float block_sum(float v, float* lds) {
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o);
-  if constexpr (WAVES == 1) return v;
-  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+  v = sum16(v);
+  const int i = __float_as_int(v);
+  float s = (__int_as_float(__builtin_amdgcn_readlane(i, 0)) + __int_as_float(__builtin_amdgcn_readlane(i, 16))) +
+            (__int_as_float(__builtin_amdgcn_readlane(i, 32)) + __int_as_float(__builtin_amdgcn_readlane(i, 48)));
+  if constexpr (WAVES == 1) return s;
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = s;
   __syncthreads();
-  float s = 0.f;
+  s = 0.f;
 #pragma unroll
-  for (int i = 0; i < WAVES; ++i) s += lds[i];
+  for (int w = 0; w < WAVES; ++w) s += lds[w];
   return s;
 }
 
+// One row a workgroup, V groups of 8 elements a lane.  Up to 16384 columns every
+// load of the row is issued before the first sum, so a row waits for memory once
+// (beyond, the registers do not hold them).
 template <int WAVES, int V, bool RF32>
 __global__ __launch_bounds__(64 * WAVES) void norm_kernel(NormArgs a) {
   __shared__ float sums[2][WAVES];
+  constexpr bool kEarly = WAVES * V <= 32;
   const int64_t row = blockIdx.x;
   const int n8 = a.d >> 3;
   const float inv_d = 1.0f / float(a.d);
-  F8 v[V];
-  // the block's output, its norm and its gate
-  if (a.o) {
-    const uint16_t* o = a.o + row * a.ldo;
-    float ss = 0.f;
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int i = threadIdx.x + 64 * WAVES * j;
-      v[j] = widen(i < n8 ? load16(o + 8 * i) : u32x4_t{0, 0, 0, 0});
-#pragma unroll
-      for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(v[j].f[e], v[j].f[e], ss);
+  const u32x4_t zero = {0, 0, 0, 0};
+  const uint16_t* o = a.o ? a.o + row * a.ldo : nullptr;
+  const uint16_t* g = a.gate ? a.gate + row / a.gate_rows * a.ldg : nullptr;
+  auto at = [&](int j) { return int(threadIdx.x) + 64 * WAVES * j; };
+  auto load = [&](const uint16_t* p, int j) { return p && at(j) < n8 ? load16(p + 8 * at(j)) : zero; };
+  auto load_r = [&](int j) {
+    F8 r = widen(zero);
+    if (at(j) < n8) {
+      if constexpr (RF32)
+        r = load_f32x8(static_cast<const float*>(a.r) + row * a.ldr + 8 * at(j));
+      else
+        r = widen(load16(static_cast<const uint16_t*>(a.r) + row * a.ldr + 8 * at(j)));
     }
-    if (a.post_w) {
-      const float k = 1.0f / sqrtf(block_sum<WAVES>(ss, sums[0]) * inv_d + a.eps);
+    return r;
+  };
+  u32x4_t ov[V], wv[V], gv[V], pv[V];
+  F8 rv[V];
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const int i = threadIdx.x + 64 * WAVES * j;
-        const F8 w = widen(i < n8 ? load16(a.post_w + 8 * i) : u32x4_t{0, 0, 0, 0});
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[j].f[e] = v[j].f[e] * k * (a.w_offset + w.f[e]);
-      }
+  for (int j = 0; j < V; ++j) {
+    ov[j] = load(o, j);
+    if constexpr (kEarly) {
+      rv[j] = load_r(j);
+      wv[j] = load(a.post_w, j);
+      gv[j] = load(g, j);
+      pv[j] = load(a.pre_w, j);
     }
-    if (a.gate) {
-      const uint16_t* g = a.gate + row / a.gate_rows * a.ldg;
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const int i = threadIdx.x + 64 * WAVES * j;
-        const F8 w = widen(i < n8 ? load16(g + 8 * i) : u32x4_t{0, 0, 0, 0});
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[j].f[e] *= w.f[e];
-      }
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < V; ++j)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[j].f[e] = 0.f;
   }
-  // the residual
+  // the block's output, its norm and its gate
+  F8 v[V];
   float ss = 0.f;
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    const int i = threadIdx.x + 64 * WAVES * j;
-    F8 r = widen(u32x4_t{0, 0, 0, 0});
-    if (i < n8) {
-      if constexpr (RF32)
-        r = load_f32x8(static_cast<const float*>(a.r) + row * a.ldr + 8 * i);
-      else
-        r = widen(load16(static_cast<const uint16_t*>(a.r) + row * a.ldr + 8 * i));
+    v[j] = widen(ov[j]);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(v[j].f[e], v[j].f[e], ss);
+  }
+  if (a.post_w) {
+    const float k = 1.0f / sqrtf(block_sum<WAVES>(ss, sums[0]) * inv_d + a.eps);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const F8 w = widen(kEarly ? wv[j] : load(a.post_w, j));
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[j].f[e] = v[j].f[e] * k * (a.w_offset + w.f[e]);
     }
+  }
+  if (g) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const F8 w = widen(kEarly ? gv[j] : load(g, j));
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[j].f[e] *= w.f[e];
+    }
+  }
+  // the residual
+  ss = 0.f;
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const F8 r = kEarly ? rv[j] : load_r(j);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       v[j].f[e] = __builtin_fmaf(a.res_scale, r.f[e], v[j].f[e]);
       ss = __builtin_fmaf(v[j].f[e], v[j].f[e], ss);
     }
-    if (a.r_out && i < n8) {
+    if (a.r_out && at(j) < n8) {
       if constexpr (RF32) {
-        float* to = static_cast<float*>(a.r_out) + row * a.ldr_out + 8 * i;
+        float* to = static_cast<float*>(a.r_out) + row * a.ldr_out + 8 * at(j);
         *reinterpret_cast<f32x4_t*>(to) = f32x4_t{v[j].f[0], v[j].f[1], v[j].f[2], v[j].f[3]};
         *reinterpret_cast<f32x4_t*>(to + 4) = f32x4_t{v[j].f[4], v[j].f[5], v[j].f[6], v[j].f[7]};
       } else {
-        *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(a.r_out) + row * a.ldr_out + 8 * i) = narrow(v[j]);
+        *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(a.r_out) + row * a.ldr_out + 8 * at(j)) = narrow(v[j]);
       }
     }
   }
@@ -144,8 +158,8 @@ __global__ __launch_bounds__(64 * WAVES) void norm_kernel(NormArgs a) {
   const int nb = (a.d + kFp8Block - 1) / kFp8Block;
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    const int i = threadIdx.x + 64 * WAVES * j;
-    const F8 w = widen(i < n8 ? load16(a.pre_w + 8 * i) : u32x4_t{0, 0, 0, 0});
+    const int i = at(j);
+    const F8 w = widen(kEarly ? pv[j] : load(a.pre_w, j));
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[j].f[e] = v[j].f[e] * k * (a.w_offset + w.f[e]);
     if (a.h && i < n8) *reinterpret_cast<u32x4_t*>(a.h + row * a.ldh + 8 * i) = narrow(v[j]);
@@ -180,11 +194,19 @@ int go(const NormArgs& a, hipStream_t s) {
 
 int launch_norm_residual(const NormArgs& a, void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
+  // Waves by width: eight, with as few groups a lane as hold the row (8192 rows of
+  // 7168: 104.6 us, 111.4 with four waves, 114.7 with sixteen), but four where
+  // eight would leave half the lanes without work (8192 of 5120: 79.4, 83.7 with
+  // eight, 91.4 with sixteen), and sixteen for few rows, which wait for memory once
+  // whatever they hold (64 of 5120: 4.8 us, 6.1 with four).
   const int n8 = a.d / 8;
   if (n8 <= 64) return go<1, 1>(a, s);
   if (n8 <= 256) return go<4, 1>(a, s);
-  if (n8 <= 512) return go<4, 2>(a, s);
-  if (n8 <= 1024) return go<4, 4>(a, s);
+  if (n8 <= 512) return go<8, 1>(a, s);
+  if (a.t <= 256 && n8 <= 1024) return go<16, 1>(a, s);
+  if (n8 <= 768) return go<4, 3>(a, s);
+  if (n8 <= 1024) return go<8, 2>(a, s);
+  if (n8 <= 1536) return go<8, 3>(a, s);
   if (n8 <= 2048) return go<8, 4>(a, s);
   if (n8 <= 4096) return go<16, 4>(a, s);
   return go<16, 8>(a, s);
