@@ -4,6 +4,8 @@
 
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "qmm_internal.h"
 
 namespace qmm {
@@ -37,27 +39,44 @@ struct Fp8GemmArgs {
   int n_experts, n_seg, m_total, max_seg_rows;
   bool glu;              // gate rows [0, n/2), up rows [n/2, n): y = silu(gate)·up
 };
-// Shape of the few-row kernel: 16·r weight rows a workgroup and 8·x8 activation
-// rows a pass.  x8 is the smallest that holds the rows (8 at most), r the largest
-// that still gives 160 workgroups, that is work for most of the 256 CUs: a larger
-// r reads the activations less often (64 x 13824 x 5120: 20.6 us with r = 4, 27.3
-// with 2), a smaller one fills the chip (64 x 5120 x 13824: 37.4, 29.2 and 44.0 us
-// with r = 4, 2 and 1; 64 x 4096 x 7168: 21.2, 16.4, 14.3).  Up to 16 rows r = 4 was
-// never faster than 2.  Grouped rows count one pass a segment.
+// Shape of the few-row kernel: 16·r weight rows a workgroup, whose waves split the
+// reduction axis, and 8·x8 activation rows a pass (the smallest of 1, 2, 4, 8 that
+// holds the rows, in several passes beyond 64).
+//
+// Dense: four waves; r the largest that still gives 160 workgroups, that is work
+// for most of 256 CUs: a larger r reads the activations less often (64 x 13824 x
+// 5120: 20.6 us with r = 4, 27.3 with 2), a smaller one fills the chip (64 x 5120 x
+// 13824: 37.4, 29.2 and 44.0 us with r = 4, 2 and 1; 64 x 4096 x 7168: 21.2, 16.4,
+// 14.3).  Up to 16 rows r = 4 was never faster than 2.
+//
+// Grouped: x8 holds a usual segment and a third more; a longer one takes another
+// pass over weights that are still in L2.  Segments give workgroups enough, so two
+// waves, each with a longer run of blocks, and r = 4 from 16 rows on (256 tokens, 6
+// of 64 experts, 2816 x 2048: 78.5 us, 103.6 with four waves and r = 2), but four
+// waves and r = 2 where there may be fewer than 512 workgroups (1 token, 8 experts,
+// 1024 x 3584: 8.8 us, 10.1 with r = 4).
 constexpr int kFp8RowsMax = 64;
+inline int64_t fp8_usual_rows(const Fp8GemmArgs& a) { return (int64_t(a.m_total) + a.n_seg - 1) / a.n_seg; }
 struct Fp8RowsShape {
-  int r, x8;
-  int64_t workgroups;
+  int r, x8, waves;
+  int64_t workgroups;   // dense
 };
 inline Fp8RowsShape fp8_rows_shape(const Fp8GemmArgs& a, int max_rows) {
-  const int64_t rows = a.n_seg == 0 ? a.t : (max_rows && max_rows < a.max_seg_rows ? max_rows : a.max_seg_rows);
+  int64_t rows = a.t;
+  if (a.n_seg > 0) {
+    rows = max_rows && max_rows < a.max_seg_rows ? max_rows : a.max_seg_rows;
+    rows = std::min(rows, std::max<int64_t>(8, fp8_usual_rows(a) * 4 / 3));
+  }
   const int x8 = rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 32 ? 4 : 8;
-  const int64_t passes = a.n_seg == 0 ? (a.t + 8 * x8 - 1) / (8 * x8) : (a.n_seg < a.m_total ? a.n_seg : a.m_total);
+  if (a.n_seg > 0) {
+    const int64_t items = (int64_t(a.n) + 31) / 32 * std::min(a.n_seg, a.m_total);
+    if (x8 <= 2 && items < 512) return {2, x8, 4, 0};
+    return {x8 == 1 ? 2 : 4, x8, 2, 0};
+  }
+  auto workgroups = [&](int r) { return (int64_t(a.n) + 16 * r - 1) / (16 * r) * ((a.t + 8 * x8 - 1) / (8 * x8)); };
   int r = x8 <= 2 ? 2 : 4;
-  const int least = a.glu ? 2 : 1;
-  auto workgroups = [&](int rr) { return (int64_t(a.n) + 16 * rr - 1) / (16 * rr) * passes; };
-  while (r > least && workgroups(r) < 160) r /= 2;
-  return {r, x8, workgroups(r)};
+  while (r > 1 && workgroups(r) < 160) r /= 2;
+  return {r, x8, 4, workgroups(r)};
 }
 // few rows: every weight read once for up to 64 rows; segments longer than
 // max_rows are left out (0: none)
@@ -88,11 +107,11 @@ struct TopkArgs {
   int32_t* slot_row;    // [t][k]
   int32_t* ws;          // counts [chunks][ne], or NULL for one chunk
 };
-// Tokens of one workgroup: 16 waves, up to 8 tokens each, and no more than 128
-// chunks (the second kernel adds every chunk's counts up itself).
+// Tokens of one workgroup: 16 waves, up to 8 tokens each, and no more than 256
+// chunks, one for each CU (the second kernel adds every chunk's counts up itself).
 constexpr int kTopkWaves = 16;
 constexpr int kTopkChunk = 128;
-constexpr int64_t kTopkMaxChunks = 128;
+constexpr int64_t kTopkMaxChunks = 256;
 inline int64_t topk_chunk(int64_t t) {
   if (t <= kTopkChunk) return kTopkChunk;
   int64_t c = 2 * kTopkWaves;

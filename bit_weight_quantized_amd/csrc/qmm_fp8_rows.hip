@@ -39,6 +39,7 @@ struct Fp8Grouped {
   int n_experts, m_total;
   int t_x;
   int max_rows;   // longer segments are left out (0: none)
+  int n_seg;
 };
 
 // eight codes -> eight bf16
@@ -50,6 +51,43 @@ __device__ __forceinline__ bf16x8_t e4m3x8_to_bf16(uint32_t lo, uint32_t hi) {
   r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true));
   return __builtin_bit_cast(bf16x8_t, r);
 }
+
+// The i-th segment that this kernel takes (1 .. max_rows rows), for ascending i:
+// 256 segments at a time, one bit each.
+struct Fp8Segments {
+  int s0 = -256, before = 0;
+  uint64_t m[4] = {0, 0, 0, 0};
+
+  __device__ __forceinline__ int find(int i, const Fp8Grouped& grp, int n_seg) {
+    const int lane = threadIdx.x & 63;
+    for (;;) {
+      int r = i - before, found = -1;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int c = __builtin_popcountll(m[u]);
+        if (found < 0 && r < c) {
+          const int rank = __builtin_amdgcn_mbcnt_hi(uint32_t(m[u] >> 32), __builtin_amdgcn_mbcnt_lo(uint32_t(m[u]), 0));
+          found = s0 + 64 * u + __builtin_ctzll(__ballot(((m[u] >> lane) & 1) && rank == r));
+        }
+        r -= c;
+      }
+      if (found >= 0) return found;
+      before = i - r;
+      s0 += 256;
+      if (s0 >= n_seg) return -1;
+      int rows[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int s = min(s0 + 64 * u + lane, n_seg - 1);
+        const int lo = min(max(grp.seg_offsets[s], 0), grp.m_total);
+        rows[u] = min(max(grp.seg_offsets[s + 1], lo), grp.m_total) - lo;
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        m[u] = __ballot(s0 + 64 * u + lane < n_seg && rows[u] > 0 && (!grp.max_rows || rows[u] <= grp.max_rows));
+    }
+  }
+};
 
 // WAVES waves split the reduction axis; R blocks of 16 weight rows, X8 groups of
 // 8 activation rows, D ring stages.  GLU: the upper half of the R blocks are the
@@ -87,267 +125,279 @@ __global__ __launch_bounds__(64 * WAVES, 2) void fp8_rows_kernel(
   const int nout = GLU ? n / 2 : n;
   const int n0 = blockIdx.x * 16 * RO;             // first output column
 
-  int64_t m_begin, m_end;
-  bool bad_expert = false;
-  const uint8_t* wm = w;
-  const float* wsm = ws;
-  const int sb = GLU ? (nout + kFp8Block - 1) / kFp8Block : 0;   // scale rows of the gate half
-  if constexpr (GROUPED) {
-    const int s = blockIdx.y;
-    m_begin = min(max(grp.seg_offsets[s], 0), grp.m_total);
-    m_end = min(max(grp.seg_offsets[s + 1], int(m_begin)), grp.m_total);
-    if (m_begin == m_end || (grp.max_rows && m_end - m_begin > grp.max_rows)) return;
-    const int e = grp.seg_expert[s];
-    bad_expert = e < 0 || e >= grp.n_experts;
-    if (!bad_expert) {
-      wm += int64_t(e) * n * d;
-      wsm += int64_t(e) * (GLU ? 2 * sb : (n + kFp8Block - 1) / kFp8Block) * nb;
+  // grouped: the workgroups of a column share out the segments
+  Fp8Segments segments;
+  for (int turn = blockIdx.y;; turn += gridDim.y) {
+    int64_t m_begin, m_end;
+    bool bad_expert = false;
+    const uint8_t* wm = w;
+    const float* wsm = ws;
+    const int sb = GLU ? (nout + kFp8Block - 1) / kFp8Block : 0;   // scale rows of the gate half
+    if constexpr (GROUPED) {
+      const int s = segments.find(turn, grp, grp.n_seg);
+      if (s < 0) return;
+      m_begin = min(max(grp.seg_offsets[s], 0), grp.m_total);
+      m_end = min(max(grp.seg_offsets[s + 1], int(m_begin)), grp.m_total);
+      const int e = grp.seg_expert[s];
+      bad_expert = e < 0 || e >= grp.n_experts;
+      if (!bad_expert) {
+        wm += int64_t(e) * n * d;
+        wsm += int64_t(e) * (GLU ? 2 * sb : (n + kFp8Block - 1) / kFp8Block) * nb;
+      }
+    } else {
+      m_begin = int64_t(turn) * kRows;
+      if (m_begin >= t) return;
+      m_end = min(t, m_begin + kRows);
     }
-  } else {
-    m_begin = int64_t(blockIdx.y) * kRows;
-    m_end = min(t, m_begin + kRows);
-  }
-  const float* ws0 = wsm + int64_t(n0 / kFp8Block) * nb;
-  const float* ws1 = wsm + int64_t(sb + n0 / kFp8Block) * nb;
+    const float* ws0 = wsm + int64_t(n0 / kFp8Block) * nb;
+    const float* ws1 = wsm + int64_t(sb + n0 / kFp8Block) * nb;
 
-  // Copies: lane / 8 is the row of a copy's eight, LDS chunk lane % 8 holds the
-  // row's 16-byte chunk (lane % 8) ^ (row % 8), so that the operand reads of
-  // eight neighbouring rows fall into different banks.
-  // Weight rows: one buffer per half, based at the tile's first row, so the
-  // 32-bit offsets stay small; rows past the matrix read zero.
-  const int crow = lane >> 3, cchunk = 16 * ((lane & 7) ^ crow);
-  const int live = min(16 * RO, nout - n0);
-  const uint8_t* w0p = wm + int64_t(n0) * d;
-  const uint8_t* w1p = GLU ? wm + int64_t(nout + n0) * d : w0p;
-  const uint32_t w_bytes = uint32_t(live) * uint32_t(d);
-  uint32_t woff[2 * RO];
+    // Copies: lane / 8 is the row of a copy's eight, LDS chunk lane % 8 holds the
+    // row's 16-byte chunk (lane % 8) ^ (row % 8), so that the operand reads of
+    // eight neighbouring rows fall into different banks.
+    // Weight rows: one buffer per half, based at the tile's first row, so the
+    // 32-bit offsets stay small; rows past the matrix read zero.
+    const int crow = lane >> 3, cchunk = 16 * ((lane & 7) ^ crow);
+    const int live = min(16 * RO, nout - n0);
+    const uint8_t* w0p = wm + int64_t(n0) * d;
+    const uint8_t* w1p = GLU ? wm + int64_t(nout + n0) * d : w0p;
+    const uint32_t w_bytes = uint32_t(live) * uint32_t(d);
+    uint32_t woff[2 * RO];
 #pragma unroll
-  for (int i = 0; i < 2 * RO; ++i) woff[i] = 8 * i + crow < live ? uint32_t(8 * i + crow) * uint32_t(d) + uint32_t(cchunk) : kOOB8;
+    for (int i = 0; i < 2 * RO; ++i)
+      woff[i] = 8 * i + crow < live ? uint32_t(8 * i + crow) * uint32_t(d) + uint32_t(cchunk) : kOOB8;
 
-  // the wave's share of the reduction axis, and its ring
-  const int b_begin = nb * wave / WAVES, b_end = nb * (wave + 1) / WAVES;
-  const unsigned char* ring = lds + wave * T::kWave;
-  const uint32_t ring_at = lds_addr(ring);
-  const int o0 = 128 * col + 16 * (g ^ (col & 7));       // operand chunks g and g + 4 of row col
+    // the wave's share of the reduction axis, and its ring
+    const int b_begin = nb * wave / WAVES, b_end = nb * (wave + 1) / WAVES;
+    const unsigned char* ring = lds + wave * T::kWave;
+    const uint32_t ring_at = lds_addr(ring);
+    const int o0 = 128 * col + 16 * (g ^ (col & 7));       // operand chunks g and g + 4 of row col
 
-  for (int64_t m0 = m_begin; m0 < m_end; m0 += kRows) {
-    // activation rows: dense rows are based at the pass's first row; grouped
-    // rows can be anywhere in x (below 2 GiB, checked by the caller)
-    const int64_t x_first = GROUPED ? 0 : m0;
-    const uint32_t x_rows = GROUPED ? uint32_t(grp.t_x) : uint32_t(min(int64_t(kRows), m_end - m0));
-    const uint8_t* xp = x + x_first * d;
-    const float* sp = xs + x_first * nb;
-    auto source = [&](int row) -> int {            // the row of x (dense: of the pass), or -1
-      if (m0 + row >= m_end) return -1;
-      if constexpr (!GROUPED) return row;
-      const int src = grp.row_index ? grp.row_index[m0 + row] : int(m0 + row);
-      return bad_expert || src < 0 || src >= grp.t_x ? -1 : src;
-    };
-    uint32_t xoff[X8], soff[T::kSc];
+    for (int64_t m0 = m_begin; m0 < m_end; m0 += kRows) {
+      // activation rows: dense rows are based at the pass's first row; grouped
+      // rows can be anywhere in x (below 2 GiB, checked by the caller)
+      const int64_t x_first = GROUPED ? 0 : m0;
+      const uint32_t x_rows = GROUPED ? uint32_t(grp.t_x) : uint32_t(min(int64_t(kRows), m_end - m0));
+      const uint8_t* xp = x + x_first * d;
+      const float* sp = xs + x_first * nb;
+      auto source = [&](int row) -> int {            // the row of x (dense: of the pass), or -1
+        if (m0 + row >= m_end) return -1;
+        if constexpr (!GROUPED) return row;
+        const int src = grp.row_index ? grp.row_index[m0 + row] : int(m0 + row);
+        return bad_expert || src < 0 || src >= grp.t_x ? -1 : src;
+      };
+      uint32_t xoff[X8], soff[T::kSc];
 #pragma unroll
-    for (int i = 0; i < X8; ++i) {
-      const int src = source(8 * i + crow);
-      xoff[i] = src >= 0 ? uint32_t(src) * uint32_t(d) + uint32_t(cchunk) : kOOB8;
-    }
+      for (int i = 0; i < X8; ++i) {
+        const int src = source(8 * i + crow);
+        xoff[i] = src >= 0 ? uint32_t(src) * uint32_t(d) + uint32_t(cchunk) : kOOB8;
+      }
 #pragma unroll
-    for (int i = 0; i < T::kSc; ++i) {
-      const int src = 64 * i + lane < kRows ? source(64 * i + lane) : -1;
-      soff[i] = src >= 0 ? uint32_t(src) * uint32_t(nb) * 4u : kOOB8;
-    }
-    // Copy `i` of block b into a stage.  The block's place in a row is the scalar
-    // offset, so the lanes' offsets stay as they are; past the wave's share the
-    // buffers are empty (zeros, no reads, the same count of copies), and in a short
-    // last block the chunks past d are out of range.
-    struct Cursor {
-      bool in;
-      uint32_t at, k, past;
-      uint32_t chunk;   // where the scales of its four blocks are
-    };
-    auto cursor = [&](int b, int stage) {
-      return Cursor{b < b_end, ring_at + uint32_t(stage * T::kStage), uint32_t(kFp8Block * b),
-                    kFp8Block * b + cchunk < d ? 0u : kOOB8,
-                    uint32_t(D * T::kStage + ((b - b_begin) >> 2) % T::kChunks * T::kChunk)};
-    };
-    auto copy = [&](const Cursor& c, int i) {
-      if (i < 2 * R)
-        copy16_to_lds_from(make_rsrc(i < 2 * RO ? w0p : w1p, c.in ? w_bytes : 0u), woff[i % (2 * RO)] | c.past, c.k,
-                           c.at + 1024u * i);
-      else
-        copy16_to_lds_from(make_rsrc(xp, c.in ? x_rows * uint32_t(d) : 0u), xoff[(i - 2 * R) % X8] | c.past, c.k,
-                           c.at + T::kX + 1024u * (i - 2 * R));
-    };
-    // The scales of four blocks at once, before the first of them (rows lie far
-    // apart: a copy costs a cache line for each row, whatever it takes of it).
-    auto copy_scales = [&](const Cursor& c) {
+      for (int i = 0; i < T::kSc; ++i) {
+        const int src = 64 * i + lane < kRows ? source(64 * i + lane) : -1;
+        soff[i] = src >= 0 ? uint32_t(src) * uint32_t(nb) * 4u : kOOB8;
+      }
+      // Copy `i` of block b into a stage.  The block's place in a row is the scalar
+      // offset, so the lanes' offsets stay as they are; past the wave's share the
+      // buffers are empty (zeros, no reads, the same count of copies), and in a short
+      // last block the chunks past d are out of range.
+      struct Cursor {
+        bool in;
+        uint32_t at, k, past;
+        uint32_t chunk;   // where the scales of its four blocks are
+      };
+      auto cursor = [&](int b, int stage) {
+        return Cursor{b < b_end, ring_at + uint32_t(stage * T::kStage), uint32_t(kFp8Block * b),
+                      kFp8Block * b + cchunk < d ? 0u : kOOB8,
+                      uint32_t(D * T::kStage + ((b - b_begin) >> 2) % T::kChunks * T::kChunk)};
+      };
+      auto copy = [&](const Cursor& c, int i) {
+        if (i < 2 * R)
+          copy16_to_lds_from(make_rsrc(i < 2 * RO ? w0p : w1p, c.in ? w_bytes : 0u), woff[i % (2 * RO)] | c.past, c.k,
+                             c.at + 1024u * i);
+        else
+          copy16_to_lds_from(make_rsrc(xp, c.in ? x_rows * uint32_t(d) : 0u), xoff[(i - 2 * R) % X8] | c.past, c.k,
+                             c.at + T::kX + 1024u * (i - 2 * R));
+      };
+      // The scales of four blocks at once, before the first of them (rows lie far
+      // apart: a copy costs a cache line for each row, whatever it takes of it).
+      auto copy_scales = [&](const Cursor& c) {
 #pragma unroll
-      for (int i = 0; i < T::kSc; ++i)
-        copy16_to_lds_from(make_rsrc(sp, c.in ? x_rows * uint32_t(nb) * 4u : 0u), soff[i], c.k / 32u,
-                           ring_at + c.chunk + 1024u * i);
-    };
+        for (int i = 0; i < T::kSc; ++i)
+          copy16_to_lds_from(make_rsrc(sp, c.in ? x_rows * uint32_t(nb) * 4u : 0u), soff[i], c.k / 32u,
+                             ring_at + c.chunk + 1024u * i);
+      };
 
-    f32x4_t acc[R][C];
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-      for (int c = 0; c < C; ++c) acc[r][c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-
-#pragma unroll
-    for (int i = 0; i < D; ++i) {
-      const Cursor c = cursor(b_begin + i, i);
-      if (i == 0) copy_scales(c);
-#pragma unroll
-      for (int k = 0; k < T::kOps; ++k) copy(c, k);
-    }
-    float w0 = scalar_load(ws0, min(b_begin, nb - 1)), w1 = GLU ? scalar_load(ws1, min(b_begin, nb - 1)) : 0.f;
-    int stage = 0;
-    for (int b = b_begin; b < b_end; ++b) {
-      const int next = min(b + 1, nb - 1);
-      const float w0n = scalar_load(ws0, next), w1n = GLU ? scalar_load(ws1, next) : 0.f;
-      // block b has landed: D - 1 blocks are in flight behind it, and scales if one
-      // of them is the first of four
-      if (((b - b_begin) & 3) + D - 1 >= 4)
-        wait_copies<(D - 1) * T::kOps + T::kSc>();
-      else
-        wait_copies<(D - 1) * T::kOps>();
-      const unsigned char* st = ring + stage * T::kStage;
-      const float* sc = reinterpret_cast<const float*>(ring + cursor(b, 0).chunk) + ((b - b_begin) & 3);
-      u32x4_t a[R][2], x2[C][2];
-      float s[C];
+      f32x4_t acc[R][C];
 #pragma unroll
       for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) a[r][h] = *reinterpret_cast<const u32x4_t*>(st + 2048 * r + (o0 ^ (64 * h)));
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) x2[c][h] = *reinterpret_cast<const u32x4_t*>(st + T::kX + 2048 * c + (o0 ^ (64 * h)));
-        s[c] = sc[4 * (16 * c + col)];
-      }
-      wait_reads();                       // ... and is in registers: its stage is free
-      const Cursor nx = cursor(b + D, stage);
-      stage = stage + 1 == D ? 0 : stage + 1;
-      if (((b + D - b_begin) & 3) == 0) copy_scales(nx);
-      if constexpr (T::kExact) {
-#pragma unroll
-        for (int k = 0; k < T::kOps; ++k) copy(nx, k);
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          f32x4_t p = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                e4m3x8_to_bf16(a[r][q >> 1][2 * (q & 1)], a[r][q >> 1][2 * (q & 1) + 1]),
-                e4m3x8_to_bf16(x2[0][q >> 1][2 * (q & 1)], x2[0][q >> 1][2 * (q & 1) + 1]), p, 0, 0, 0);
-          const float sv = s[0] * (r < RO ? w0 : w1);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[r][0][i] = __builtin_fmaf(p[i], sv, acc[r][0][i]);
-        }
-      } else {
-        // block sums, their multiply-adds two matrix instructions later, and the
-        // copies spread between them: a copy holds the wave while the memory
-        // pipeline is busy, the matrix unit works on meanwhile
-        constexpr int N = R * C, kAhead = 2;
-        f32x4_t p[kAhead + 1];
-#pragma unroll
-        for (int m = 0; m < N + kAhead; ++m) {
-          if (m < N) p[m % (kAhead + 1)] = mfma_e4m3(join(a[m % R][0], a[m % R][1]), join(x2[m / R][0], x2[m / R][1]));
-#pragma unroll
-          for (int k = 0; k < T::kOps; ++k)
-            if (k * N / T::kOps == m) copy(nx, k);
-          if (m >= kAhead) {
-            const int u = m - kAhead, r = u % R, c = u / R;
-            const float sv = s[c] * (r < RO ? w0 : w1);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[r][c][i] = __builtin_fmaf(p[u % (kAhead + 1)][i], sv, acc[r][c][i]);
-          }
-          __builtin_amdgcn_sched_barrier(0);
-        }
-      }
-      w0 = w0n;
-      w1 = w1n;
-    }
+        for (int c = 0; c < C; ++c) acc[r][c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-    // the ring becomes the waves' sums: [wave][R·C][64]
-    wait_copies<0>();
-    __syncthreads();
-    f32x4_t* part = reinterpret_cast<f32x4_t*>(lds);
 #pragma unroll
-    for (int r = 0; r < R; ++r)
+      for (int i = 0; i < D; ++i) {
+        const Cursor c = cursor(b_begin + i, i);
+        if (i == 0) copy_scales(c);
 #pragma unroll
-      for (int c = 0; c < C; ++c) part[(wave * R * C + r * C + c) * 64 + lane] = acc[r][c];
-    __syncthreads();
-    const bool wide = (ldy & 3) == 0 && (reinterpret_cast<uintptr_t>(y) & 7) == 0;
-    auto summed = [&](int u) {
-      f32x4_t v = part[u * 64 + lane];
-#pragma unroll
-      for (int p = 1; p < WAVES; ++p) {
-        const f32x4_t o = part[(p * R * C + u) * 64 + lane];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] += o[i];
+        for (int k = 0; k < T::kOps; ++k) copy(c, k);
       }
-      return v;
-    };
-    // unit u: output block (r, c), a lane's four columns of one row
-    for (int u = wave; u < RO * C; u += WAVES) {
-      const int r = u / C, c = u % C;
-      const int64_t row = m0 + 16 * c + col;
-      const int j = n0 + 16 * r + 4 * g;
-      f32x4_t v = summed(u);
-      if constexpr (GLU) {
-        const f32x4_t up = summed(u + RO * C);
+      float w0 = scalar_load(ws0, min(b_begin, nb - 1)), w1 = GLU ? scalar_load(ws1, min(b_begin, nb - 1)) : 0.f;
+      int stage = 0;
+      for (int b = b_begin; b < b_end; ++b) {
+        const int next = min(b + 1, nb - 1);
+        const float w0n = scalar_load(ws0, next), w1n = GLU ? scalar_load(ws1, next) : 0.f;
+        // block b has landed: D - 1 blocks are in flight behind it, and scales if one
+        // of them is the first of four
+        if (((b - b_begin) & 3) + D - 1 >= 4)
+          wait_copies<(D - 1) * T::kOps + T::kSc>();
+        else
+          wait_copies<(D - 1) * T::kOps>();
+        const unsigned char* st = ring + stage * T::kStage;
+        const float* sc = reinterpret_cast<const float*>(ring + cursor(b, 0).chunk) + ((b - b_begin) & 3);
+        u32x4_t a[R][2], x2[C][2];
+        float s[C];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = silu(v[i]) * up[i];
-      }
-      if (16 * c + col < kRows && row < m_end) {
-        const bool bad = GROUPED && source(16 * c + col) < 0;
-        uint16_t* to = y + row * ldy + j;
-        uint16_t b16[4];
+        for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) b16[i] = bad ? uint16_t(0x7FC0) : f32_to_bf16(v[i]);
-        if (wide && j + 4 <= nout) {
-          *reinterpret_cast<u32x2_t*>(to) =
-              u32x2_t{uint32_t(b16[0]) | uint32_t(b16[1]) << 16, uint32_t(b16[2]) | uint32_t(b16[3]) << 16};
+          for (int h = 0; h < 2; ++h)
+            a[r][h] = *reinterpret_cast<const u32x4_t*>(st + 2048 * r + (o0 ^ (64 * h)));
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) x2[c][h] = *reinterpret_cast<const u32x4_t*>(st + T::kX + 2048 * c + (o0 ^ (64 * h)));
+          s[c] = sc[4 * (16 * c + col)];
+        }
+        wait_reads();                       // ... and is in registers: its stage is free
+        const Cursor nx = cursor(b + D, stage);
+        stage = stage + 1 == D ? 0 : stage + 1;
+        if (((b + D - b_begin) & 3) == 0) copy_scales(nx);
+        if constexpr (T::kExact) {
+#pragma unroll
+          for (int k = 0; k < T::kOps; ++k) copy(nx, k);
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            f32x4_t p = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                  e4m3x8_to_bf16(a[r][q >> 1][2 * (q & 1)], a[r][q >> 1][2 * (q & 1) + 1]),
+                  e4m3x8_to_bf16(x2[0][q >> 1][2 * (q & 1)], x2[0][q >> 1][2 * (q & 1) + 1]), p, 0, 0, 0);
+            const float sv = s[0] * (r < RO ? w0 : w1);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[r][0][i] = __builtin_fmaf(p[i], sv, acc[r][0][i]);
+          }
         } else {
+          // block sums, their multiply-adds two matrix instructions later, and the
+          // copies spread between them: a copy holds the wave while the memory
+          // pipeline is busy, the matrix unit works on meanwhile
+          constexpr int N = R * C, kAhead = 2;
+          f32x4_t p[kAhead + 1];
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (j + i < nout) to[i] = b16[i];
+          for (int m = 0; m < N + kAhead; ++m) {
+            if (m < N) p[m % (kAhead + 1)] = mfma_e4m3(join(a[m % R][0], a[m % R][1]), join(x2[m / R][0], x2[m / R][1]));
+#pragma unroll
+            for (int k = 0; k < T::kOps; ++k)
+              if (k * N / T::kOps == m) copy(nx, k);
+            if (m >= kAhead) {
+              const int u = m - kAhead, r = u % R, c = u / R;
+              const float sv = s[c] * (r < RO ? w0 : w1);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) acc[r][c][i] = __builtin_fmaf(p[u % (kAhead + 1)][i], sv, acc[r][c][i]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        }
+        w0 = w0n;
+        w1 = w1n;
+      }
+
+      // the ring becomes the waves' sums: [wave][R·C][64]
+      wait_copies<0>();
+      __syncthreads();
+      f32x4_t* part = reinterpret_cast<f32x4_t*>(lds);
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int c = 0; c < C; ++c) part[(wave * R * C + r * C + c) * 64 + lane] = acc[r][c];
+      __syncthreads();
+      const bool wide = (ldy & 3) == 0 && (reinterpret_cast<uintptr_t>(y) & 7) == 0;
+      auto summed = [&](int u) {
+        f32x4_t v = part[u * 64 + lane];
+#pragma unroll
+        for (int p = 1; p < WAVES; ++p) {
+          const f32x4_t o = part[(p * R * C + u) * 64 + lane];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] += o[i];
+        }
+        return v;
+      };
+      // unit u: output block (r, c), a lane's four columns of one row
+      for (int u = wave; u < RO * C; u += WAVES) {
+        const int r = u / C, c = u % C;
+        const int64_t row = m0 + 16 * c + col;
+        const int j = n0 + 16 * r + 4 * g;
+        f32x4_t v = summed(u);
+        if constexpr (GLU) {
+          const f32x4_t up = summed(u + RO * C);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = silu(v[i]) * up[i];
+        }
+        if (16 * c + col < kRows && row < m_end) {
+          const bool bad = GROUPED && source(16 * c + col) < 0;
+          uint16_t* to = y + row * ldy + j;
+          uint16_t b16[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) b16[i] = bad ? uint16_t(0x7FC0) : f32_to_bf16(v[i]);
+          if (wide && j + 4 <= nout) {
+            *reinterpret_cast<u32x2_t*>(to) =
+                u32x2_t{uint32_t(b16[0]) | uint32_t(b16[1]) << 16, uint32_t(b16[2]) | uint32_t(b16[3]) << 16};
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (j + i < nout) to[i] = b16[i];
+          }
         }
       }
+      __syncthreads();   // the next pass fills the ring again
     }
-    __syncthreads();   // the next pass fills the ring again
   }
 }
 
-constexpr int kWaves = 4, kDepth = 2;   // a deeper ring or more waves measured no faster anywhere
+constexpr int kDepth = 2;   // a deeper ring measured no faster anywhere
 
-template <int R, int X8, bool GROUPED, bool GLU>
+template <int WAVES, int R, int X8, bool GROUPED, bool GLU>
 int go(const Fp8GemmArgs& a, int max_rows, hipStream_t s) {
-  using T = Fp8Rows<kWaves, R, X8, kDepth, GROUPED, GLU>;
+  using T = Fp8Rows<WAVES, R, X8, kDepth, GROUPED, GLU>;
   const int nout = GLU ? a.n / 2 : a.n, per = 16 * T::RO;
-  const Fp8Grouped grp{a.row_index, a.seg_expert, a.seg_offsets, a.n_experts, a.m_total, int(a.t_x), max_rows};
-  const unsigned gy = GROUPED ? unsigned(a.n_seg) : unsigned((a.t + 8 * X8 - 1) / (8 * X8));
-  launch_kernel_lds(fp8_rows_kernel<kWaves, R, X8, kDepth, GROUPED, GLU>, dim3(unsigned((nout + per - 1) / per), gy),
-                    dim3(64 * kWaves), T::kLds, s, a.w, a.ws, a.n, a.d, fp8_blocks(a.d), a.x, a.xs, a.t, a.y, a.ldy, grp);
+  const Fp8Grouped grp{a.row_index, a.seg_expert, a.seg_offsets, a.n_experts, a.m_total, int(a.t_x), max_rows, a.n_seg};
+  const int64_t tiles = (nout + per - 1) / per;
+  int64_t gy = std::min<int64_t>((a.t + 8 * X8 - 1) / (8 * X8), 65535);   // the grid's limit: more take turns
+  if (GROUPED) {
+    // no more segments than rows have any; two rounds of the workgroups that the
+    // LDS lets 256 CUs hold, each taking several segments (one workgroup for each
+    // of 896 segments and 112 columns, 8 of them with a row: 36.6 us, 6.6 shared)
+    const int64_t resident = 2 * 256 * (160 * 1024 / T::kLds);
+    gy = std::max<int64_t>(1, std::min<int64_t>(std::min(a.n_seg, a.m_total), resident / tiles));
+  }
+  launch_kernel_lds(fp8_rows_kernel<WAVES, R, X8, kDepth, GROUPED, GLU>, dim3(unsigned(tiles), unsigned(gy)),
+                    dim3(64 * WAVES), T::kLds, s, a.w, a.ws, a.n, a.d, fp8_blocks(a.d), a.x, a.xs, a.t, a.y, a.ldy, grp);
   return int(hipGetLastError());
 }
 
-template <int R, bool GROUPED, bool GLU>
-int go(int x8, const Fp8GemmArgs& a, int max_rows, hipStream_t s) {
-  if (x8 == 4) return go<R, 4, GROUPED, GLU>(a, max_rows, s);
-  if (x8 == 8) return go<R, 8, GROUPED, GLU>(a, max_rows, s);
-  if constexpr (R <= 2) {
-    if (x8 == 1) return go<R, 1, GROUPED, GLU>(a, max_rows, s);
-    return go<R, 2, GROUPED, GLU>(a, max_rows, s);
-  }
+template <int R>
+int dense(int x8, const Fp8GemmArgs& a, hipStream_t s) {
+  if (x8 == 4) return go<4, R, 4, false, false>(a, 0, s);
+  if (x8 == 8) return go<4, R, 8, false, false>(a, 0, s);
+  if constexpr (R <= 2) return x8 == 1 ? go<4, R, 1, false, false>(a, 0, s) : go<4, R, 2, false, false>(a, 0, s);
   return int(hipErrorInvalidValue);
 }
 
-template <bool GROUPED, bool GLU>
-int go(const Fp8RowsShape& p, const Fp8GemmArgs& a, int max_rows, hipStream_t s) {
-  if (p.r == 4) return go<4, GROUPED, GLU>(p.x8, a, max_rows, s);
-  if constexpr (!GLU)
-    if (p.r == 1) return go<1, GROUPED, GLU>(p.x8, a, max_rows, s);
-  return go<2, GROUPED, GLU>(p.x8, a, max_rows, s);
+template <bool GLU>
+int grouped(const Fp8RowsShape& p, const Fp8GemmArgs& a, int max_rows, hipStream_t s) {
+  if (p.waves == 4) return p.x8 == 1 ? go<4, 2, 1, true, GLU>(a, max_rows, s) : go<4, 2, 2, true, GLU>(a, max_rows, s);
+  if (p.x8 == 1) return go<2, 2, 1, true, GLU>(a, max_rows, s);
+  if (p.x8 == 2) return go<2, 4, 2, true, GLU>(a, max_rows, s);
+  return p.x8 == 4 ? go<2, 4, 4, true, GLU>(a, max_rows, s) : go<2, 4, 8, true, GLU>(a, max_rows, s);
 }
 
 }  // namespace
@@ -355,8 +405,8 @@ int go(const Fp8RowsShape& p, const Fp8GemmArgs& a, int max_rows, hipStream_t s)
 int launch_fp8_rows(const Fp8GemmArgs& a, int max_rows, void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
   const Fp8RowsShape p = fp8_rows_shape(a, max_rows);
-  if (a.n_seg == 0) return go<false, false>(p, a, 0, s);
-  return a.glu ? go<true, true>(p, a, max_rows, s) : go<true, false>(p, a, max_rows, s);
+  if (a.n_seg == 0) return p.r == 4 ? dense<4>(p.x8, a, s) : p.r == 2 ? dense<2>(p.x8, a, s) : dense<1>(p.x8, a, s);
+  return a.glu ? grouped<true>(p, a, max_rows, s) : grouped<false>(p, a, max_rows, s);
 }
 
 }  // namespace qmm

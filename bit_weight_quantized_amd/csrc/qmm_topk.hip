@@ -12,12 +12,12 @@
 // holds experts J·i .. J·i + J-1 as order-preserving integer keys, so the
 // lowest lane and the lowest j among equal keys is the lowest expert.  A round
 // takes the largest key of the wave (DPP, then scalar registers) and the
-// winning lane looks for its next best.
+// winning lane drops it.
 //
 // Grouping counts the chunk's tokens per expert in LDS (integer atomics, order
 // free).  One chunk: the same workgroup scans the counts and places its rows.
 // More: the counts go to the workspace, and a second kernel, one workgroup per
-// chunk, adds up every chunk's counts (at most 128 per expert) and places the
+// chunk, adds up every chunk's counts (at most 256 per expert) and places the
 // chunk's rows.  Rows of an expert ascend with the token, found from a bitmap
 // of the chunk's tokens per expert, so nothing depends on timing.
 #include <hip/hip_runtime.h>
@@ -31,10 +31,8 @@
 namespace qmm {
 namespace {
 
-constexpr int kTkThreads = 64 * kTopkWaves;
 constexpr int kTkWords = kTopkChunk / 32;        // bitmap words of an expert and pass
-constexpr int kTkMaxExperts = kRouteMaxExperts;  // one per thread of the workgroup
-static_assert(kTkMaxExperts == kTkThreads, "a thread owns an expert");
+static_assert(kRouteMaxExperts == 64 * kTopkWaves, "a thread of the workgroup owns an expert");
 
 // Order-preserving map to an unsigned key; 0 marks an expert that cannot be
 // chosen: masked (-inf), NaN, or taken.
@@ -51,10 +49,38 @@ __device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
   return umax(umax(r0, r1), umax(r2, r3));
 }
 
+__device__ __forceinline__ float readlane_f(float v, int lane) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
+}
+
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o);
-  return v;
+  v = sum16(v);
+  return (readlane_f(v, 0) + readlane_f(v, 16)) + (readlane_f(v, 32) + readlane_f(v, 48));
+}
+
+__device__ __forceinline__ float wave_max(float v) {
+  v = fmaxf(v, dpp_f<0xB1>(v));
+  v = fmaxf(v, dpp_f<0x4E>(v));
+  v = fmaxf(v, dpp_f<0x141>(v));
+  v = fmaxf(v, dpp_f<0x140>(v));
+  return fmaxf(fmaxf(readlane_f(v, 0), readlane_f(v, 16)), fmaxf(readlane_f(v, 32), readlane_f(v, 48)));
+}
+
+// The two largest of a set, and of the sets of two lanes.
+struct Two {
+  float first, second;
+};
+__device__ __forceinline__ void take(Two& t, float v) {
+  t.second = fmaxf(t.second, fminf(t.first, v));
+  t.first = fmaxf(t.first, v);
+}
+__device__ __forceinline__ void merge(Two& t, float first, float second) {
+  t.second = fmaxf(fmaxf(t.second, second), fminf(t.first, first));
+  t.first = fmaxf(t.first, first);
+}
+template <int CTRL>
+__device__ __forceinline__ void merge_dpp(Two& t) {
+  merge(t, dpp_f<CTRL>(t.first), dpp_f<CTRL>(t.second));
 }
 
 __device__ __forceinline__ float sigmoid(float l) { return 1.0f / (1.0f + expf(-l)); }
@@ -65,14 +91,17 @@ __device__ __forceinline__ float logit(const void* p, int64_t i) {
   return static_cast<const float*>(p)[i];
 }
 
+template <int WAVES>
 struct TopkLds {
-  int32_t count[kTkMaxExperts];
-  uint32_t bits[kTkMaxExperts][kTkWords];
-  int32_t first[kTkMaxExperts];      // the next row of each expert
-  int32_t wsum[kTopkWaves];
+  static constexpr int kThreads = 64 * WAVES;    // a thread owns an expert
+  int32_t count[kThreads];
+  int32_t first[kThreads];                       // the next row of each expert
+  uint32_t bits[kThreads][kTkWords];
+  int32_t wsum[WAVES];
 };
 
 // Exclusive sum over the workgroup's threads; every thread gets the total too.
+template <int WAVES>
 __device__ __forceinline__ int block_scan(int c, int32_t* wsum, int* total) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int incl = c;
@@ -84,7 +113,8 @@ __device__ __forceinline__ int block_scan(int c, int32_t* wsum, int* total) {
   if (lane == 63) wsum[wave] = incl;
   __syncthreads();
   int before = 0, all = 0;
-  for (int w = 0; w < kTopkWaves; ++w) {
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) {
     before += w < wave ? wsum[w] : 0;
     all += wsum[w];
   }
@@ -92,23 +122,24 @@ __device__ __forceinline__ int block_scan(int c, int32_t* wsum, int* total) {
   return before + incl - c;
 }
 
-// Writes the rows of tokens [t0, t1), whose first row of expert e is
-// lds.first[e]: 128 tokens at a time, one bit per (expert, token).
-__device__ void place_rows(TopkLds& lds, const int32_t* topk, int64_t t0, int64_t t1, int k,
-                           int32_t* row_index, int32_t* slot_row) {
+// Writes the rows of tokens [t0, t1), whose ids are ids[0 ..] and whose first row
+// of expert e is lds.first[e]: 128 tokens at a time, one bit per (expert, token).
+template <int WAVES>
+__device__ __forceinline__ void place_rows(TopkLds<WAVES>& lds, const int32_t* ids, int64_t t0, int64_t t1, int k,
+                                           int32_t* row_index, int32_t* slot_row) {
   const int tid = threadIdx.x;
   for (int64_t b0 = t0; b0 < t1; b0 += kTopkChunk) {
     const int nb = int(min(int64_t(kTopkChunk), t1 - b0)) * k;
 #pragma unroll
     for (int h = 0; h < kTkWords; ++h) lds.bits[tid][h] = 0u;
     __syncthreads();
-    for (int i = tid; i < nb; i += kTkThreads) {
-      const int e = topk[b0 * k + i], tl = i / k;
+    for (int i = tid; i < nb; i += 64 * WAVES) {
+      const int e = ids[(b0 - t0) * k + i], tl = i / k;
       if (e >= 0) atomicOr(&lds.bits[e][tl >> 5], 1u << (tl & 31));
     }
     __syncthreads();
-    for (int i = tid; i < nb; i += kTkThreads) {
-      const int e = topk[b0 * k + i], tl = i / k;
+    for (int i = tid; i < nb; i += 64 * WAVES) {
+      const int e = ids[(b0 - t0) * k + i], tl = i / k;
       int row = -1;
       if (e >= 0) {
         row = lds.first[e] + __builtin_popcount(lds.bits[e][tl >> 5] & ((1u << (tl & 31)) - 1u));
@@ -125,122 +156,160 @@ __device__ void place_rows(TopkLds& lds, const int32_t* topk, int64_t t0, int64_
 
 // J experts a lane; ONE: all tokens are one chunk, and the workgroup groups
 // them itself.
-template <int J, bool BF16, bool ONE>
-__global__ __launch_bounds__(kTkThreads) void topk_kernel(TopkArgs a, int chunk) {
-  __shared__ TopkLds lds;
-  __shared__ float cs[kTopkWaves][64 * J];       // a wave's c, for the groups' values
+template <int WAVES, int J, bool BF16, bool SIGMOID, bool ONE>
+__global__ __launch_bounds__(64 * WAVES) void topk_kernel(TopkArgs a, int chunk) {
+  __shared__ TopkLds<WAVES> lds;
+  __shared__ float cs[WAVES][64 * J];            // a wave's scores by expert
+  __shared__ int32_t chosen[ONE ? kTopkChunk * kRouteMaxK : 1];
   const int tid = threadIdx.x;
   const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t t0 = int64_t(blockIdx.x) * chunk, t1 = min(a.t, t0 + chunk);
   const int ne = a.ne, k = a.k, groups = a.groups;
   const int gs = ne / groups;                     // experts of a group
-  int per = 64;                                   // lanes that share a group's experts
+  const bool by_logit = !SIGMOID && !a.bias && (groups == 1 || !a.top2);
+  // Lanes of a group.  Where a group is a power of two of whole lanes (2 .. 16, as
+  // 256 experts in 8 groups) a lane's experts share its group, and the lanes of a
+  // group exchange by DPP; otherwise `per` lanes go over a group's scores in LDS.
+  const int own = gs % J == 0 ? gs / J : 0;
+  const bool aligned = own == 2 || own == 4 || own == 8 || own == 16;
+  int per = aligned ? own : 64;
   while (per * groups > 64) per >>= 1;
-  const bool by_logit = !a.sigmoid && !a.bias && (groups == 1 || !a.top2);
 
   lds.count[tid] = 0;
-  __syncthreads();
+  // What a lane's experts need for every token is kept where the registers allow it.
+  constexpr bool kKeep = J <= 8;
+  int base = J * lane;                            // the lane's first expert
+  auto bias_of = [&](int j) { return a.bias ? a.bias[min(base + j, ne - 1)] : 0.f; };
+  auto first_lane = [&](int j) { return min(base + j, ne - 1) / gs * per; };   // of the expert's group
   float bias[J];
-  int gid[J];                                     // first lane of the expert's group
-#pragma unroll
-  for (int j = 0; j < J; ++j) {
-    const int e = J * lane + j;
-    bias[j] = a.bias && e < ne ? a.bias[e] : 0.f;
-    gid[j] = e < ne ? e / gs * per : 0;
-  }
-
-  for (int64_t tok = t0 + wave; tok < t1; tok += kTopkWaves) {
-    float l[J], c[J];
+  int gid[J];
+  if constexpr (kKeep) {
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      const int e = J * lane + j;
-      l[j] = e < ne ? logit<BF16>(a.logits, tok * a.ld + e) : -INFINITY;
+      bias[j] = bias_of(j);
+      gid[j] = first_lane(j);
     }
+  }
+  float next[J];
+  auto load = [&](int64_t tok) {
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const int e = base + j;
+      const float v = logit<BF16>(a.logits, tok * a.ld + min(e, ne - 1));
+      next[j] = e < ne ? v : -INFINITY;
+    }
+  };
+  if (kKeep && t0 + wave < t1) load(t0 + wave);
+  __syncthreads();
+
+  for (int64_t tok = t0 + wave; tok < t1; tok += WAVES) {
+    float l[J], c[J];
+    if constexpr (!kKeep) {
+      asm volatile("" : "+v"(base));              // what hangs on it is not kept from token to token
+      load(tok);
+    }
+#pragma unroll
+    for (int j = 0; j < J; ++j) l[j] = next[j];
+    if (kKeep && tok + WAVES < t1) load(tok + WAVES);
     float top = 0.f, total = 1.f;
-    if (!a.sigmoid) {
+    if constexpr (!SIGMOID) {
       float m = l[0];
 #pragma unroll
       for (int j = 1; j < J; ++j) m = fmaxf(m, l[j]);
-#pragma unroll
-      for (int o = 1; o < 64; o <<= 1) m = fmaxf(m, __shfl_xor(m, o));
+      m = wave_max(m);
       top = m > -INFINITY ? m : 0.f;              // nothing left: every e^(l - top) is 0
       float z = 0.f;
 #pragma unroll
       for (int j = 0; j < J; ++j) z += expf(l[j] - top);
       total = wave_sum(z);
     }
-    auto prob = [&](float v) { return a.sigmoid ? sigmoid(v) : total > 0.f ? expf(v - top) / total : total; };
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-      c[j] = by_logit ? l[j] : prob(l[j]) + bias[j];
-      if (l[j] == -INFINITY) c[j] = -INFINITY;
-    }
+    auto prob = [&](float v) { return SIGMOID ? sigmoid(v) : total > 0.f ? expf(v - top) / total : total; };
     uint32_t key[J];
 #pragma unroll
-    for (int j = 0; j < J; ++j) key[j] = choice_key(c[j]);
+    for (int j = 0; j < J; ++j) {
+      const float p = by_logit ? l[j] : prob(l[j]);
+      c[j] = by_logit ? p : p + (kKeep ? bias[j] : bias_of(j));
+      if (l[j] == -INFINITY) c[j] = -INFINITY;
+      key[j] = choice_key(c[j]);
+      if (key[j] == 0u) c[j] = -INFINITY;         // NaN ranks with the masked
+      l[j] = SIGMOID ? p : l[j];                  // what the weight is made from
+    }
 
+    float* mine = cs[wave];
     if (groups > 1) {
-      // the groups' values: `per` lanes each, their best (two) merged
-      float* mine = cs[wave];
+      Two two = {-INFINITY, -INFINITY};
+      const int q = lane / per;                   // the lane's group
+      if (aligned) {
 #pragma unroll
-      for (int j = 0; j < J; ++j) mine[J * lane + j] = key[j] ? c[j] : -INFINITY;
-      __builtin_amdgcn_wave_barrier();
-      const int q = lane / per;
-      float b1 = -INFINITY, b2 = -INFINITY;
-      if (q < groups)
-        for (int i = lane - q * per; i < gs; i += per) {
-          const float v = mine[q * gs + i];
-          b2 = fmaxf(b2, fminf(b1, v));
-          b1 = fmaxf(b1, v);
-        }
-      for (int o = 1; o < per; o <<= 1) {
-        const float o1 = __shfl_xor(b1, o), o2 = __shfl_xor(b2, o);
-        b2 = fmaxf(fmaxf(b2, o2), fminf(b1, o1));
-        b1 = fmaxf(b1, o1);
+        for (int j = 0; j < J; ++j) take(two, c[j]);
+        merge_dpp<0xB1>(two);
+        if (per > 2) merge_dpp<0x4E>(two);
+        if (per > 4) merge_dpp<0x141>(two);
+        if (per > 8) merge_dpp<0x140>(two);
+      } else {
+#pragma unroll
+        for (int j = 0; j < J; ++j) mine[J * lane + j] = c[j];
+        __builtin_amdgcn_wave_barrier();
+        if (q < groups)
+          for (int i = lane - q * per; i < gs; i += per) take(two, mine[q * gs + i]);
+        for (int o = 1; o < per; o <<= 1) merge(two, __shfl_xor(two.first, o), __shfl_xor(two.second, o));
+        __builtin_amdgcn_wave_barrier();
       }
-      const float value = a.top2 && b2 > -INFINITY ? b1 + b2 : b1;
+      const float value = a.top2 && two.second > -INFINITY ? two.first + two.second : two.first;
       // rank among the groups: larger values first, equal ones by index
       int rank = 0;
       for (int o = 0; o < groups; ++o) {
-        const float v = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(value), o * per));
+        const float v = readlane_f(value, o * per);
         rank += v > value || (v == value && o < q) ? 1 : 0;
       }
-      const uint64_t kept = __ballot(q < groups && rank < a.keep);
+      const bool keep = q < groups && rank < a.keep;
+      const uint64_t kept = __ballot(keep);
 #pragma unroll
-      for (int j = 0; j < J; ++j) key[j] = (kept >> gid[j]) & 1 ? key[j] : 0u;
-      __builtin_amdgcn_wave_barrier();
+      for (int j = 0; j < J; ++j) key[j] = (aligned ? keep : (kept >> (kKeep ? gid[j] : first_lane(j))) & 1) ? key[j] : 0u;
     }
+    // probabilities (softmax: logits) by expert, for the weights of the chosen
+#pragma unroll
+    for (int j = 0; j < J; ++j) mine[J * lane + j] = l[j];
 
     int mine_e = -1;
     for (int r = 0; r < k; ++r) {
-      uint32_t bk = key[0];
-      int be = J * lane;
+      uint32_t best = key[0];
 #pragma unroll
-      for (int j = 1; j < J; ++j) {
-        const bool gt = key[j] > bk;
-        bk = gt ? key[j] : bk;
-        be = gt ? J * lane + j : be;
-      }
-      const uint32_t m = wave_umax(bk);
+      for (int j = 1; j < J; ++j) best = umax(best, key[j]);
+      const uint32_t m = wave_umax(best);
       if (m == 0) break;                          // nothing left (uniform)
-      const int first = __builtin_ctzll(__ballot(bk == m));
-      const int win = __builtin_amdgcn_readlane(be, first);
+      // the lowest lane that holds it, and its lowest expert: scalar work on the
+      // comparisons' masks
+      uint64_t has[J], any = 0;
 #pragma unroll
-      for (int j = 0; j < J; ++j) key[j] = J * lane + j == win ? 0u : key[j];
+      for (int j = 0; j < J; ++j) {
+        has[j] = __ballot(key[j] == m);
+        any |= has[j];
+      }
+      const int at = __builtin_ctzll(any);
+      int j0 = J - 1;
+#pragma unroll
+      for (int j = J - 2; j >= 0; --j) j0 = (has[j] >> at) & 1 ? j : j0;
+      const bool here = lane == at;
+#pragma unroll
+      for (int j = 0; j < J; ++j) key[j] = here && j == j0 ? 0u : key[j];
+      const int win = J * at + j0;
       mine_e = lane == r ? win : mine_e;
     }
-    // the weights, from the logits of the chosen
+    __builtin_amdgcn_wave_barrier();
     float w = 0.f;
-    if (mine_e >= 0) w = prob(logit<BF16>(a.logits, tok * a.ld + mine_e));
+    if (mine_e >= 0) w = SIGMOID ? mine[mine_e] : prob(mine[mine_e]);
     if (a.renorm) {
       const float sum = wave_sum(w);
       w = sum == 0.f ? 0.f : w / sum;             // a NaN stays one
     }
+    __builtin_amdgcn_wave_barrier();
     if (lane < k) {
       a.topk[tok * k + lane] = mine_e;
       a.weights[tok * k + lane] = w * a.scale;
       if (mine_e >= 0) atomicAdd(&lds.count[mine_e], 1);
+      if constexpr (ONE) chosen[(tok - t0) * k + lane] = mine_e;
     }
   }
   __syncthreads();                                // counts; the ids of the chunk
@@ -248,49 +317,52 @@ __global__ __launch_bounds__(kTkThreads) void topk_kernel(TopkArgs a, int chunk)
     if (tid < ne) a.ws[int64_t(blockIdx.x) * ne + tid] = lds.count[tid];
   } else {
     int total;
-    const int at = block_scan(lds.count[tid], lds.wsum, &total);
+    const int at = block_scan<WAVES>(lds.count[tid], lds.wsum, &total);
     lds.first[tid] = at;
     if (tid < ne) {
       a.seg_expert[tid] = tid;
       a.seg_offsets[tid] = at;
     }
     if (tid == 0) a.seg_offsets[ne] = total;
-    for (int64_t i = total + tid; i < a.t * k; i += kTkThreads) a.row_index[i] = -1;
-    place_rows(lds, a.topk, t0, t1, k, a.row_index, a.slot_row);
+    for (int64_t i = total + tid; i < a.t * k; i += 64 * WAVES) a.row_index[i] = -1;
+    place_rows(lds, chosen, t0, t1, k, a.row_index, a.slot_row);
   }
 }
 
-__global__ __launch_bounds__(kTkThreads) void topk_place_kernel(const int32_t* __restrict__ topk, int64_t t, int ne,
-                                                                int k, int chunk, const int32_t* __restrict__ counts,
-                                                                int32_t* __restrict__ seg_expert,
-                                                                int32_t* __restrict__ seg_offsets,
-                                                                int32_t* __restrict__ row_index,
-                                                                int32_t* __restrict__ slot_row) {
-  __shared__ TopkLds lds;
+__global__ __launch_bounds__(64 * kTopkWaves) void topk_place_kernel(
+    const int32_t* __restrict__ topk, int64_t t, int ne, int k, int chunk, const int32_t* __restrict__ counts,
+    int32_t* __restrict__ seg_expert, int32_t* __restrict__ seg_offsets, int32_t* __restrict__ row_index,
+    int32_t* __restrict__ slot_row) {
+  constexpr int kThreads = 64 * kTopkWaves;
+  __shared__ TopkLds<kTopkWaves> lds;
   const int tid = threadIdx.x, chunks = gridDim.x, me = blockIdx.x;
-  int before = 0, all = 0;
-  if (tid < ne) {
-    // 8 loads in flight
-    int c0 = 0;
-    for (; c0 + 8 <= chunks; c0 += 8) {
+  // counts of all chunks and of those before this one; the threads go over the
+  // chunks in as many parts as the experts leave room for, 8 loads in flight
+  lds.count[tid] = 0;
+  lds.first[tid] = 0;
+  __syncthreads();
+  const int span = (ne + 63) / 64 * 64, parts = kThreads / span;
+  const int e = tid % span, part = tid / span;
+  if (e < ne && part < parts) {
+    int before = 0, all = 0;
+    for (int c0 = part; c0 < chunks; c0 += 8 * parts) {
       int v[8];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) v[u] = counts[int64_t(c0 + u) * ne + tid];
+      for (int u = 0; u < 8; ++u) v[u] = counts[int64_t(min(c0 + u * parts, chunks - 1)) * ne + e];
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
-        before += c0 + u < me ? v[u] : 0;
-        all += v[u];
+        const int c = c0 + u * parts;
+        before += c < me ? v[u] : 0;
+        all += c < chunks ? v[u] : 0;
       }
     }
-    for (; c0 < chunks; ++c0) {
-      const int v = counts[int64_t(c0) * ne + tid];
-      before += c0 < me ? v : 0;
-      all += v;
-    }
+    atomicAdd(&lds.count[e], all);
+    atomicAdd(&lds.first[e], before);
   }
+  __syncthreads();
   int total;
-  const int at = block_scan(all, lds.wsum, &total);
-  lds.first[tid] = at + before;
+  const int at = block_scan<kTopkWaves>(lds.count[tid], lds.wsum, &total);
+  lds.first[tid] += at;
   if (me == 0) {
     if (tid < ne) {
       seg_expert[tid] = tid;
@@ -298,27 +370,35 @@ __global__ __launch_bounds__(kTkThreads) void topk_place_kernel(const int32_t* _
     }
     if (tid == 0) seg_offsets[ne] = total;
   }
-  for (int64_t i = total + int64_t(me) * kTkThreads + tid; i < t * k; i += int64_t(chunks) * kTkThreads)
+  for (int64_t i = total + int64_t(me) * kThreads + tid; i < t * k; i += int64_t(chunks) * kThreads)
     row_index[i] = -1;
   const int64_t t0 = int64_t(me) * chunk;
-  place_rows(lds, topk, t0, min(t, t0 + chunk), k, row_index, slot_row);
+  place_rows(lds, topk + t0 * k, t0, min(t, t0 + chunk), k, row_index, slot_row);
 }
 
-template <int J, bool BF16>
+template <int J, bool BF16, bool SIGMOID>
 int go(const TopkArgs& a, hipStream_t s) {
   const int64_t chunk = topk_chunk(a.t);
   const unsigned chunks = a.t <= chunk ? 1u : unsigned((a.t + chunk - 1) / chunk);   // no tokens: the tables alone
   const ProfileEvents pe = take_profile_events();
   const hipEvent_t ev0 = static_cast<hipEvent_t>(pe.start), ev1 = static_cast<hipEvent_t>(pe.stop);
   if (chunks == 1) {
-    hipExtLaunchKernelGGL((topk_kernel<J, BF16, true>), dim3(1), dim3(kTkThreads), 0, s, ev0, ev1, 0, a, int(chunk));
+    // a few tokens: fewer waves, shorter barriers
+    if constexpr (J <= 4) {
+      if (a.t <= 8) {
+        hipExtLaunchKernelGGL((topk_kernel<4, J, BF16, SIGMOID, true>), dim3(1), dim3(256), 0, s, ev0, ev1, 0, a, int(chunk));
+        return int(hipGetLastError());
+      }
+    }
+    hipExtLaunchKernelGGL((topk_kernel<kTopkWaves, J, BF16, SIGMOID, true>), dim3(1), dim3(64 * kTopkWaves), 0, s, ev0,
+                          ev1, 0, a, int(chunk));
     return int(hipGetLastError());
   }
-  hipExtLaunchKernelGGL((topk_kernel<J, BF16, false>), dim3(chunks), dim3(kTkThreads), 0, s, ev0, nullptr, 0, a,
-                        int(chunk));
+  hipExtLaunchKernelGGL((topk_kernel<kTopkWaves, J, BF16, SIGMOID, false>), dim3(chunks), dim3(64 * kTopkWaves), 0, s,
+                        ev0, nullptr, 0, a, int(chunk));
   const int err = int(hipGetLastError());
   if (err) return err;
-  hipExtLaunchKernelGGL(topk_place_kernel, dim3(chunks), dim3(kTkThreads), 0, s, nullptr, ev1, 0,
+  hipExtLaunchKernelGGL(topk_place_kernel, dim3(chunks), dim3(64 * kTopkWaves), 0, s, nullptr, ev1, 0,
                         static_cast<const int32_t*>(a.topk), a.t, a.ne, a.k, int(chunk),
                         static_cast<const int32_t*>(a.ws), a.seg_expert, a.seg_offsets, a.row_index, a.slot_row);
   return int(hipGetLastError());
@@ -326,7 +406,8 @@ int go(const TopkArgs& a, hipStream_t s) {
 
 template <int J>
 int go(const TopkArgs& a, hipStream_t s) {
-  return a.bf16 ? go<J, true>(a, s) : go<J, false>(a, s);
+  if (a.sigmoid) return a.bf16 ? go<J, true, true>(a, s) : go<J, false, true>(a, s);
+  return a.bf16 ? go<J, true, false>(a, s) : go<J, false, false>(a, s);
 }
 
 // Weighted sum of the chosen experts' rows, one workgroup per token and 2048

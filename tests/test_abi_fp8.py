@@ -124,9 +124,9 @@ def test_route_refusals():
 def test_route_workspace():
     w = qmm.qmm_route_topk_workspace_bytes
     assert w(1, 256) == w(128, 256) == w(0, 256) == w(-1, 4) == w(200, 1025) == w(200, 0) == 0
-    for t in (129, 1000, 4096, 4097, 16384, 16385, 100000, 1 << 24):
+    for t in (129, 1000, 8192, 8193, 16384, 32769, 100000, 1 << 24):
         for ne in (1, 60, 1024):
-            assert 0 < w(t, ne) <= 4 * ne * -(-t // 32) and w(t, ne) <= 4 * ne * 128
+            assert 0 < w(t, ne) <= 4 * ne * -(-t // 32) and w(t, ne) <= 4 * ne * 256
 
 
 def test_gather_refusals():
