@@ -55,4 +55,11 @@ __device__ __forceinline__ float scalar_load(const float* p, int i) {
 
 __device__ __forceinline__ float silu(float v) { return v / (1.0f + expf(-v)); }
 
+// The same from the hardware's exponential and reciprocal (a few 2^-23 of its
+// value, less than the sums it is taken of), for tiles of many values: the
+// precise form is 35 instructions a value.
+__device__ __forceinline__ float quick_silu(float v) {
+  return v * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * -1.44269504f));
+}
+
 }  // namespace qmm

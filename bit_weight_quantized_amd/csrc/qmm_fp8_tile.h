@@ -48,21 +48,84 @@ struct Fp8Place {
   int sb;                 // scale rows of the gate half
 };
 
+// Row tiles of 256 segments from s0 on, four neighbouring ones a lane; segments of
+// up to skip_rows rows have none.
+template <int kT>
+struct Fp8Tiles {
+  int at[5], tiles[4], sum, first, all;   // offsets, tiles; of the lane, before it, of the wave
+
+  __device__ __forceinline__ void scan(const Fp8TileArgs& a, int s0) {
+    const int lane = threadIdx.x & 63;
+    sum = 0;
+#pragma unroll
+    for (int u = 0; u < 5; ++u) at[u] = min(max(a.seg_offsets[min(s0 + 4 * lane + u, a.n_seg)], 0), a.m_total);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int rows = at[u + 1] - at[u];
+      tiles[u] = rows > a.skip_rows ? (rows + kT - 1) / kT : 0;
+      sum += tiles[u];
+    }
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int up = __shfl_up(incl, o);
+      if (lane >= o) incl += up;
+    }
+    first = incl - sum;
+    all = __builtin_amdgcn_readlane(incl, 63);
+  }
+
+  // The tt-th tile, if it is one of these: its segment's number from s0, rows [lo, hi).
+  __device__ __forceinline__ int find(int tt, int& lo, int& hi) const {
+    const uint64_t who = __ballot(tt >= first && tt < first + sum);
+    if (!who) return -1;
+    int s = -1, b = 0, e = 0, f = first;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (s < 0 && tt >= f && tt < f + tiles[u]) {
+        s = 4 * int(threadIdx.x & 63) + u;
+        b = at[u] + (tt - f) * kT;
+        e = min(b + kT, at[u + 1]);
+      }
+      f += tiles[u];
+    }
+    const int src = __builtin_ctzll(who);
+    lo = __builtin_amdgcn_readlane(b, src);
+    hi = __builtin_amdgcn_readlane(e, src);
+    return __builtin_amdgcn_readlane(s, src);
+  }
+};
+
 // The tile of this workgroup, kT rows by kOut columns; false where the grid's
 // bound has more row tiles than there are.  XCD id mod 8 takes a contiguous run
 // of tiles, in blocks of 8 weight tiles by all activation tiles, activation
 // tiles slowest: the 32 workgroups at work on an XCD share 8 weight and 4
-// activation tiles in its L2.
+// activation tiles in its L2.  The runs are equal parts of the tiles that there
+// are, not of the grid: with the grid's, whose bound is 192 row tiles where 64
+// segments of 512 rows have 159, two XCDs were idle for most of the time (64 experts
+// of 3584 x 2048, 32768 rows: 367 us, 311 as it is).
 template <int kT, int kOut, bool GROUPED, bool GLU>
 __device__ __forceinline__ bool fp8_place(const Fp8TileArgs& a, Fp8Place& p) {
-  const int total = gridDim.x;
+  const int nout = GLU ? a.n / 2 : a.n;
+  int tiles_t = gridDim.x / a.tiles_n;
+  Fp8Tiles<kT> some;
+  if constexpr (GROUPED) {
+    // every wave looks for itself
+    int all = 0;
+    for (int s0 = 0; s0 < a.n_seg; s0 += 256) {
+      some.scan(a, s0);
+      all += some.all;
+    }
+    tiles_t = min(tiles_t, all);
+  }
+  const int total = tiles_t * a.tiles_n;
   const int xcd = blockIdx.x & 7, share = total >> 3, extra = total & 7;
+  if (int(blockIdx.x >> 3) >= share + (xcd < extra ? 1 : 0)) return false;
   const int id = xcd * share + min(xcd, extra) + (blockIdx.x >> 3);
-  const int tiles_t = total / a.tiles_n;
   const int strip = id / (8 * tiles_t), in_strip = id - strip * 8 * tiles_t;
   const int width = min(8, a.tiles_n - 8 * strip);
-  const int tt = in_strip / width, tn = 8 * strip + in_strip - tt * width;
-  const int nout = GLU ? a.n / 2 : a.n;
+  int tt = in_strip / width;
+  const int tn = 8 * strip + in_strip - tt * width;
   p.n0 = tn * kOut;
   p.bad_expert = false;
   p.w = a.w;
@@ -73,31 +136,14 @@ __device__ __forceinline__ bool fp8_place(const Fp8TileArgs& a, Fp8Place& p) {
     p.m_end = min(a.t, p.m0 + kT);
     return true;
   }
-  // the tt-th row tile of the segments longer than skip_rows; every wave looks
-  // for itself, 64 segments at a time
-  const int lane = threadIdx.x & 63;
-  int before = 0;
-  for (int s0 = 0; s0 < a.n_seg; s0 += 64) {
-    const int s = s0 + lane;
-    int lo = 0, hi = 0;
-    if (s < a.n_seg) {
-      lo = min(max(a.seg_offsets[s], 0), a.m_total);
-      hi = min(max(a.seg_offsets[s + 1], lo), a.m_total);
-    }
-    const int tiles = hi - lo > a.skip_rows ? (hi - lo + kT - 1) / kT : 0;
-    int incl = tiles;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int up = __shfl_up(incl, o);
-      if (lane >= o) incl += up;
-    }
-    const int at = before + incl - tiles;
-    const uint64_t who = __ballot(tt >= at && tt < at + tiles);
-    if (who) {
-      const int src = __builtin_ctzll(who);
-      p.m0 = __builtin_amdgcn_readlane(lo + (tt - at) * kT, src);
-      p.m_end = min(p.m0 + kT, int64_t(__builtin_amdgcn_readlane(hi, src)));
-      const int e = a.seg_expert[s0 + src];
+  for (int s0 = 0; s0 < a.n_seg; s0 += 256) {
+    if (a.n_seg > 256) some.scan(a, s0);
+    int lo, hi;
+    const int s = some.find(tt, lo, hi);
+    if (s >= 0) {
+      p.m0 = lo;
+      p.m_end = hi;
+      const int e = a.seg_expert[s0 + s];
       p.bad_expert = e < 0 || e >= a.n_experts;
       if (!p.bad_expert) {
         p.w += int64_t(e) * a.n * a.d;
@@ -105,7 +151,7 @@ __device__ __forceinline__ bool fp8_place(const Fp8TileArgs& a, Fp8Place& p) {
       }
       return true;
     }
-    before += __builtin_amdgcn_readlane(incl, 63);
+    tt -= some.all;
   }
   return false;
 }
@@ -146,18 +192,16 @@ __device__ __forceinline__ f32x4_t mfma_e4m3(const i32x8_t a, const i32x8_t b) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
 }
 
-// Stores a lane's four consecutive columns c .. c + 3 of one output row.
-__device__ __forceinline__ void store4(uint16_t* row, int c, int nout, const float* f, bool bad, bool wide) {
-  uint16_t v[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) v[e] = bad ? uint16_t(0x7FC0) : f32_to_bf16(f[e]);
-  if (wide && c + 4 <= nout) {
-    *reinterpret_cast<u32x2_t*>(row + c) =
-        u32x2_t{uint32_t(v[0]) | uint32_t(v[1]) << 16, uint32_t(v[2]) | uint32_t(v[3]) << 16};
+// Eight neighbouring output columns c .. c + 7 of a row; `wide`: rows start at
+// multiples of 8 bytes.
+typedef uint32_t u32x4_at8_t __attribute__((ext_vector_type(4), aligned(8)));
+__device__ __forceinline__ void store8(uint16_t* row, int c, int nout, u32x4_t v, bool wide) {
+  if (wide && c + 8 <= nout) {
+    *reinterpret_cast<u32x4_at8_t*>(row + c) = v;
   } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (c + e < nout) row[c + e] = v[e];
+    for (int e = 0; e < 8; ++e)
+      if (c + e < nout) row[c + e] = uint16_t(v[e >> 1] >> (16 * (e & 1)));
   }
 }
 

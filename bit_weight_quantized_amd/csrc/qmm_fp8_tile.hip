@@ -51,7 +51,9 @@ struct Fp8Tile {
   static constexpr int kOut = GLU ? kN / 2 : kN;       // output columns
   static constexpr int kStage = (kT + kN) * 128;       // both tiles of a step
   static constexpr int kScales = kT * 16;              // activation scales of four steps
-  static constexpr int kLds = 2 * kStage + 2 * kScales;
+  static constexpr int kBad = 2 * kStage + 2 * kScales;   // a bit for every row without a source
+  static constexpr int kLds = kBad + kT / 8;
+  static_assert(kT * kOut * 2 <= 2 * kStage, "the output tile takes the place of the operands'");
   static_assert(kT / 16 % kWaves == 0 && kN / 8 % kWaves == 0 && kT / 64 <= kWaves, "whole copies per wave");
   static constexpr int kXCopies = kT / 16 / kWaves, kWCopies = kN / 8 / kWaves;   // of half the activations
   static constexpr int kAfter = 2 * kXCopies + kWCopies;
@@ -73,24 +75,7 @@ __global__ __launch_bounds__(64 * WT * WN) void fp8_tile_kernel(Fp8TileArgs A) {
   // ---- copies: row 8·i + lane / 8 of a copy, LDS chunk lane % 8 holding the
   // global chunk (lane % 8) ^ (row % 8)
   const int crow = lane >> 3, cchunk = (lane & 7) ^ crow;
-  uint32_t xoff[2][T::kXCopies], woff[T::kWCopies], soff = kOOB8;
-  const Fp8Source<GROUPED> src(A, P);
-  // half h of the activations: the blocks H·h .. H·h + H - 1 of every wave row
-  auto x_row = [&](int h, int i) {                      // first row of a wave's i-th copy
-    const int c = wave * T::kXCopies + i;
-    return 16 * TS * (c / TS) + 8 * TS * h + 8 * (c % TS);
-  };
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll
-    for (int i = 0; i < T::kXCopies; ++i) {
-      const int row = src(A, P, x_row(h, i) + crow);
-      xoff[h][i] = row >= 0 ? uint32_t(row) * uint32_t(d) : kOOB8;
-    }
-  if (wave < T::kT / 64) {                              // scales of 64 rows a wave
-    const int row = src(A, P, 64 * wave + lane);
-    soff = row >= 0 ? uint32_t(row) * uint32_t(nb) * 4u : kOOB8;
-  }
+  uint32_t woff[T::kWCopies];
   // weight rows: a wave's WS blocks are consecutive LDS rows; with the
   // activation their upper half comes from the up rows (8·WS rows are whole
   // copies, so a copy reads one of the two halves)
@@ -110,23 +95,44 @@ __global__ __launch_bounds__(64 * WT * WN) void fp8_tile_kernel(Fp8TileArgs A) {
     const uint32_t k = uint32_t(kFp8Block * b + 16 * cchunk);
     return k < uint32_t(d) ? k : kOOB8;
   };
+  auto copy_w = [&](int b) {
+    const uint32_t at = base + uint32_t(b & 1) * T::kStage + 128u * T::kT, ko = at_block(b);
+#pragma unroll
+    for (int i = 0; i < T::kWCopies; ++i)
+      copy16_to_lds(GLU && ((wave * T::kWCopies + i) / WS & 1) ? wr1 : wr0, (woff[i] + ko) | ((woff[i] | ko) & kOOB8),
+                    at + 1024u * uint32_t(wave * T::kWCopies + i));
+  };
+  copy_w(0);                                            // on its way while the rows are looked up
+
+  uint32_t xoff[2][T::kXCopies], soff = kOOB8;
+  const Fp8Source<GROUPED> src(A, P);
+  // first row of a wave's i-th copy of half h of the activations
+  auto x_row = [&](int h, int i) { return T::kT / 2 * h + 8 * (wave * T::kXCopies + i); };
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int i = 0; i < T::kXCopies; ++i) {
+      const int row = src(A, P, x_row(h, i) + crow);
+      xoff[h][i] = row >= 0 ? uint32_t(row) * uint32_t(d) : kOOB8;
+    }
+  if (wave < T::kT / 64) {                              // scales of 64 rows a wave
+    const int row = src(A, P, 64 * wave + lane);
+    soff = row >= 0 ? uint32_t(row) * uint32_t(nb) * 4u : kOOB8;
+    if constexpr (GROUPED)
+      *reinterpret_cast<uint64_t*>(lds + T::kBad + 8 * wave) = __ballot(row < 0);
+  }
   auto copy_x = [&](int b, int h) {
     const uint32_t at = base + uint32_t(b & 1) * T::kStage, ko = at_block(b);
 #pragma unroll
     for (int i = 0; i < T::kXCopies; ++i)
       copy16_to_lds(src.x, (xoff[h][i] + ko) | ((xoff[h][i] | ko) & kOOB8), at + 128u * uint32_t(x_row(h, i)));
   };
-  auto copy_w = [&](int b) {
-    const uint32_t at = base + uint32_t(b & 1) * T::kStage + 128u * T::kT, ko = at_block(b);
-    // scales of four steps at a time, 64 rows a wave (rows lie far apart: a copy
-    // costs a cache line for each row, whatever it takes of it)
+  // scales of four steps at a time, 64 rows a wave (rows lie far apart: a copy
+  // costs a cache line for each row, whatever it takes of it)
+  auto copy_scales = [&](int b) {
     if ((b & 3) == 0 && wave < T::kT / 64)
       copy16_to_lds(src.s, (soff + 4u * uint32_t(b)) | (soff & kOOB8),
                     base + 2u * T::kStage + uint32_t(b >> 2 & 1) * T::kScales + 1024u * uint32_t(wave));
-#pragma unroll
-    for (int i = 0; i < T::kWCopies; ++i)
-      copy16_to_lds(GLU && ((wave * T::kWCopies + i) / WS & 1) ? wr1 : wr0, (woff[i] + ko) | ((woff[i] | ko) & kOOB8),
-                    at + 1024u * uint32_t(wave * T::kWCopies + i));
   };
 
   // ---- operands
@@ -151,21 +157,22 @@ __global__ __launch_bounds__(64 * WT * WN) void fp8_tile_kernel(Fp8TileArgs A) {
 #pragma unroll
     for (int j = 0; j < WS; ++j) a[j] = operand(st + 128 * (T::kT + 16 * WS * wn + col) + 2048 * j);
   };
-  auto read_x = [&](int half) {
+  auto read_x = [&](auto half, auto blocks) {
+    constexpr int h = decltype(half)::value;
 #pragma unroll
-    for (int i = 0; i < H; ++i) {
-      bx[i] = operand(st + 128 * (16 * TS * wt + col) + 2048 * (H * half + i));
-      sx[i] = sc[64 * (H * half + i)];
+    for (int i = 0; i < decltype(blocks)::value; ++i) {
+      bx[i] = operand(st + 128 * (16 * wt + col) + 2048 * WT * (H * h + i));
+      sx[i] = sc[64 * WT * (H * h + i)];
     }
   };
   // block sums and their multiply-adds, kAhead matrix instructions apart: the
   // order is fixed, since the scheduler would start all the block sums first and
   // keep them in registers that the accumulators need
-  auto multiply = [&](auto half, float w0, float w1) {
-    constexpr int h = decltype(half)::value, kAhead = 4, N = H * WS;
+  auto multiply = [&](auto half, auto blocks, float w0, float w1) {
+    constexpr int h = decltype(half)::value, kAhead = 4, N = decltype(blocks)::value * WS;
     f32x4_t p[kAhead + 1];
 #pragma unroll
-    for (int m = 0; m < N + kAhead; ++m) {
+    for (int m = 0; m < (N ? N + kAhead : 0); ++m) {
       if (m < N)
         p[m % (kAhead + 1)] = mfma_e4m3(a[m % WS], bx[m / WS]);
       if (m >= kAhead) {
@@ -181,7 +188,7 @@ __global__ __launch_bounds__(64 * WT * WN) void fp8_tile_kernel(Fp8TileArgs A) {
   };
   const bool behind = wave >= T::kWaves / 2;            // the second group: one phase later
 
-  copy_w(0);
+  copy_scales(0);
   copy_x(0, 0);
   copy_x(0, 1);
   copy_w(1);
@@ -189,58 +196,85 @@ __global__ __launch_bounds__(64 * WT * WN) void fp8_tile_kernel(Fp8TileArgs A) {
   wait_copies<T::kAfter>();
   phase_end();
   if (behind) phase_end();
-  float w0 = scalar_load(ws0, 0), w1 = GLU ? scalar_load(ws1, 0) : 0.f;
-  for (int b = 0; b < nb; ++b) {
-    st = lds + (b & 1) * T::kStage;
-    sc = reinterpret_cast<const float*>(lds + 2 * T::kStage + (b >> 2 & 1) * T::kScales) +
-         4 * (16 * TS * wt + col) + (b & 3);
-    const int next = min(b + 1, nb - 1);
-    const float w0n = scalar_load(ws0, next), w1n = GLU ? scalar_load(ws1, next) : 0.f;
-    __builtin_amdgcn_s_setprio(1);                      // the reader's few instructions first
-    read_w();
-    read_x(0);
-    copy_x(b + 1, 1);                                   // both groups have read that half of step b - 1
-    __builtin_amdgcn_s_setprio(0);
-    wait_reads();
-    // second half of step b (a scale copy of this wave may be among the later ones)
-    if (b % 4 == 3 && wave < T::kT / 64) wait_copies<T::kAfter + 1>();
-    else wait_copies<T::kAfter>();
-    phase_end();
-    multiply(std::integral_constant<int, 0>{}, w0, w1);
-    phase_end();
-    __builtin_amdgcn_s_setprio(1);
-    read_x(1);
-    copy_w(b + 2);                                      // both groups have read these of step b
-    copy_x(b + 2, 0);
-    __builtin_amdgcn_s_setprio(0);
-    wait_reads();
-    // weights and first half of step b + 1
-    if (b % 4 == 2 && wave < T::kT / 64) wait_copies<T::kAfter + 1>();
-    else wait_copies<T::kAfter>();
-    phase_end();
-    multiply(std::integral_constant<int, 1>{}, w0, w1);
-    phase_end();
-    w0 = w0n;
-    w1 = w1n;
-  }
+  // The steps, with `first` and `second` live activation blocks of a half.
+  auto steps = [&](auto first, auto second) {
+    float w0 = scalar_load(ws0, 0), w1 = GLU ? scalar_load(ws1, 0) : 0.f;
+    for (int b = 0; b < nb; ++b) {
+      st = lds + (b & 1) * T::kStage;
+      sc = reinterpret_cast<const float*>(lds + 2 * T::kStage + (b >> 2 & 1) * T::kScales) + 4 * (16 * wt + col) + (b & 3);
+      const int next = min(b + 1, nb - 1);
+      const float w0n = scalar_load(ws0, next), w1n = GLU ? scalar_load(ws1, next) : 0.f;
+      __builtin_amdgcn_s_setprio(1);                      // the reader's few instructions first
+      read_w();
+      read_x(std::integral_constant<int, 0>{}, first);
+      copy_x(b + 1, 1);                                   // both groups have read that half of step b - 1
+      __builtin_amdgcn_s_setprio(0);
+      wait_reads();
+      // second half of step b (a scale copy of this wave may be among the later ones)
+      if (b % 4 == 3 && wave < T::kT / 64) wait_copies<T::kAfter + 1>();
+      else wait_copies<T::kAfter>();
+      phase_end();
+      multiply(std::integral_constant<int, 0>{}, first, w0, w1);
+      phase_end();
+      __builtin_amdgcn_s_setprio(1);
+      read_x(std::integral_constant<int, 1>{}, second);
+      copy_scales(b + 2);
+      copy_w(b + 2);                                      // both groups have read these of step b
+      copy_x(b + 2, 0);
+      __builtin_amdgcn_s_setprio(0);
+      wait_reads();
+      // weights and first half of step b + 1
+      if (b % 4 == 2 && wave < T::kT / 64) wait_copies<T::kAfter + 1>();
+      else wait_copies<T::kAfter>();
+      phase_end();
+      multiply(std::integral_constant<int, 1>{}, second, w0, w1);
+      phase_end();
+      w0 = w0n;
+      w1 = w1n;
+    }
+  };
+  // A tile with few live rows leaves out the block sums of dead ones, a quarter of
+  // the tile at a time: the waves' blocks alternate, so all waves have less to do.
+  const int rows = int(P.m_end - P.m0);
+  using None = std::integral_constant<int, 0>;
+  using Part = std::integral_constant<int, H / 2>;
+  using Whole = std::integral_constant<int, H>;
+  if (rows > T::kT / 4 * 3) steps(Whole{}, Whole{});
+  else if (rows > T::kT / 2) steps(Whole{}, Part{});
+  else if (rows > T::kT / 4) steps(Whole{}, None{});
+  else steps(Part{}, None{});
   if (!behind) phase_end();                             // the groups' barrier counts match
   wait_copies<0>();
+  phase_end();
 
-  // ---- epilogue: lane (col, g) holds output columns 4g .. 4g + 3 of activation row col
-  const bool wide = (A.ldy & 3) == 0 && (reinterpret_cast<uintptr_t>(A.y) & 7) == 0;
-  constexpr int WO = GLU ? WS / 2 : WS;
+  // ---- epilogue: the output tile through LDS, so that a store has whole lines.
+  // Lane (col, g) holds columns 4g .. 4g + 3 of activation row col; a row's 16-byte
+  // chunks lie at chunk ^ (row mod 16 or 8).  (Straight from the registers, 32 bytes
+  // of a row at a time, the stores of a 256 x 256 tile took 6.5 to 7.5 us.)
+  constexpr int WO = GLU ? WS / 2 : WS, kChunks = T::kOut / 8, kMask = kChunks < 16 ? kChunks - 1 : 15;
 #pragma unroll
   for (int i = 0; i < TS; ++i) {
-    const int row = 16 * (TS * wt + i) + col;
-    if (P.m0 + row >= P.m_end) continue;
-    const bool bad = GROUPED && src(A, P, row) < 0;
+    const int row = 16 * (WT * i + wt) + col;
+    bool bad = false;
+    if constexpr (GROUPED) bad = reinterpret_cast<const uint32_t*>(lds + T::kBad)[row >> 5] >> (row & 31) & 1;
 #pragma unroll
     for (int j = 0; j < WO; ++j) {
       float f[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) f[e] = GLU ? silu(acc[i][j][e]) * acc[i][WS - WO + j][e] : acc[i][j][e];
-      store4(A.y + (P.m0 + row) * A.ldy, n0 + 16 * (WO * wn + j) + 4 * g, nout, f, bad, wide);
+      for (int e = 0; e < 4; ++e) f[e] = GLU ? quick_silu(acc[i][j][e]) * acc[i][WS - WO + j][e] : acc[i][j][e];
+      const int chunk = (2 * (WO * wn + j) + (g >> 1)) ^ (col & kMask);
+      *reinterpret_cast<u32x2_t*>(lds + 2 * T::kOut * row + 16 * chunk + 8 * (g & 1)) =
+          bad ? u32x2_t{0x7FC07FC0u, 0x7FC07FC0u} : u32x2_t{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3])};
     }
+  }
+  wait_reads();
+  phase_end();
+  const bool wide = (A.ldy & 3) == 0 && (reinterpret_cast<uintptr_t>(A.y) & 7) == 0;
+#pragma unroll 4
+  for (int q = threadIdx.x; q < rows * kChunks; q += 64 * T::kWaves) {
+    const int row = q / kChunks, chunk = q % kChunks;
+    const u32x4_t v = *reinterpret_cast<const u32x4_t*>(lds + 2 * T::kOut * row + 16 * (chunk ^ (row & kMask)));
+    store8(A.y + (P.m0 + row) * A.ldy, n0 + 8 * chunk, nout, v, wide);
   }
 }
 
@@ -297,7 +331,11 @@ int launch_fp8_product(const Fp8GemmArgs& a, void* stream) {
     if (a.t <= kFp8RowsMax || (few <= small && few <= large)) return launch_fp8_rows(a, 0, stream);
     return launch_fp8_tile(a, large < small, 0, stream);
   }
-  if (a.max_seg_rows <= kFp8RowsMax) return launch_fp8_rows(a, 0, stream);
+  // Few rows a segment: the few-row kernel alone, in several passes where a segment
+  // is longer, as long as there cannot be very many (64 experts of 2816 x 2048: 48
+  // rows a segment 117.6 us alone, 135.5 split; 96 rows 186.2, 165.5).
+  if (a.max_seg_rows <= kFp8RowsMax || (a.max_seg_rows <= 1024 && fp8_usual_rows(a) <= 64))
+    return launch_fp8_rows(a, 0, stream);
   // two launches that split the segments on the device; armed events: the
   // start with the first, the stop with the second
   const ProfileEvents pe = take_profile_events();
@@ -305,7 +343,9 @@ int launch_fp8_product(const Fp8GemmArgs& a, void* stream) {
   const int err = launch_fp8_rows(a, kFp8RowsMax, stream);
   arm_profile_events({nullptr, err ? nullptr : pe.stop});
   if (err) return err;
-  return launch_fp8_tile(a, int64_t(a.m_total) >= int64_t(192) * a.n_seg, kFp8RowsMax, stream);
+  // large tiles from 256 rows a segment (64 experts of 2816 x 2048: 192 rows 157.8 us
+  // small, 166.3 large; 384 rows 246.6, 233.8; of 4096 x 3584, 512 rows 731, 611)
+  return launch_fp8_tile(a, int64_t(a.m_total) >= int64_t(256) * a.n_seg, kFp8RowsMax, stream);
 }
 
 }  // namespace qmm

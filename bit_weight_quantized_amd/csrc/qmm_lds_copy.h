@@ -44,12 +44,6 @@ __device__ __forceinline__ void copy16_to_lds_from(__amdgpu_buffer_rsrc_t r, uin
                : "v"(voff), "s"(r), "s"(lds), "s"(soff)
                : "memory", "m0");
 }
-__device__ __forceinline__ void copy4_to_lds_from(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\tbuffer_load_dword %0, %1, %3 offen lds"
-               :
-               : "v"(voff), "s"(r), "s"(lds), "s"(soff)
-               : "memory", "m0");
-}
 __device__ __forceinline__ uint32_t lds_addr(const void* p) {
   return uint32_t(uintptr_t((lds_ptr_t)p));
 }
