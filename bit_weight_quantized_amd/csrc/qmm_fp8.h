@@ -49,41 +49,27 @@ struct Fp8GemmArgs {
 // 13824: 37.4, 29.2 and 44.0 us with r = 4, 2 and 1; 64 x 4096 x 7168: 21.2, 16.4,
 // 14.3).  Up to 16 rows r = 4 was never faster than 2.
 //
-// Grouped: x8 holds a usual segment and a third more; a longer one takes another
-// pass over weights that are still in L2.  Segments give workgroups enough, so two
-// waves, each with a longer run of blocks, and r = 4 from 16 rows on (256 tokens, 6
-// of 64 experts, 2816 x 2048: 78.5 us, 103.6 with four waves and r = 2), but four
-// waves and r = 2 where there may be fewer than 512 workgroups (1 token, 8 experts,
-// 1024 x 3584: 8.8 us, 10.1 with r = 4).
+// Grouped: 8 rows a pass and r = 2 (the tile kernel has the longer segments).  Two
+// waves, each with a longer run of blocks, but four where there may be fewer than 512
+// workgroups (1 token, 8 experts, 1024 x 3584: 8.3 us, 13 with two).
 constexpr int kFp8RowsMax = 64;
 inline int64_t fp8_usual_rows(const Fp8GemmArgs& a) { return (int64_t(a.m_total) + a.n_seg - 1) / a.n_seg; }
 struct Fp8RowsShape {
   int r, x8, waves;
   int64_t workgroups;   // dense
 };
-inline Fp8RowsShape fp8_rows_shape(const Fp8GemmArgs& a, int max_rows) {
-  int64_t rows = a.t;
-  if (a.n_seg > 0) {
-    rows = max_rows && max_rows < a.max_seg_rows ? max_rows : a.max_seg_rows;
-    rows = std::min(rows, std::max<int64_t>(8, fp8_usual_rows(a) * 4 / 3));
-  }
-  const int x8 = rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 32 ? 4 : 8;
-  if (a.n_seg > 0) {
-    const int64_t items = (int64_t(a.n) + 31) / 32 * std::min(a.n_seg, a.m_total);
-    if (x8 <= 2 && items < 512) return {2, x8, 4, 0};
-    return {x8 == 1 ? 2 : 4, x8, 2, 0};
-  }
+inline Fp8RowsShape fp8_rows_shape(const Fp8GemmArgs& a) {
+  if (a.n_seg > 0) return {2, 1, (int64_t(a.n) + 31) / 32 * std::min(a.n_seg, a.m_total) < 512 ? 4 : 2, 0};
+  const int x8 = a.t <= 8 ? 1 : a.t <= 16 ? 2 : a.t <= 32 ? 4 : 8;
   auto workgroups = [&](int r) { return (int64_t(a.n) + 16 * r - 1) / (16 * r) * ((a.t + 8 * x8 - 1) / (8 * x8)); };
   int r = x8 <= 2 ? 2 : 4;
   while (r > 1 && workgroups(r) < 160) r /= 2;
   return {r, x8, 4, workgroups(r)};
 }
-// few rows: every weight read once for up to 64 rows; segments longer than
-// max_rows are left out (0: none)
-int launch_fp8_rows(const Fp8GemmArgs& a, int max_rows, void* stream);
-// many rows: LDS tiles of 256 x 256 (large) or 128 x 128; segments of up to
-// skip_rows rows are left out
-int launch_fp8_tile(const Fp8GemmArgs& a, bool large, int skip_rows, void* stream);
+// few rows: every weight read once for up to 64 rows
+int launch_fp8_rows(const Fp8GemmArgs& a, void* stream);
+// many rows: LDS tiles of 256 x 256 (large) or 64 x 128
+int launch_fp8_tile(const Fp8GemmArgs& a, bool large, void* stream);
 // the choice between them
 int launch_fp8_product(const Fp8GemmArgs& a, void* stream);
 

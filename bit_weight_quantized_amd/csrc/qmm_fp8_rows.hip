@@ -38,21 +38,10 @@ struct Fp8Grouped {
   const int32_t* seg_offsets;
   int n_experts, m_total;
   int t_x;
-  int max_rows;   // longer segments are left out (0: none)
   int n_seg;
 };
 
-// eight codes -> eight bf16
-__device__ __forceinline__ bf16x8_t e4m3x8_to_bf16(uint32_t lo, uint32_t hi) {
-  u32x4_t r;
-  r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false));
-  r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true));
-  r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false));
-  r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true));
-  return __builtin_bit_cast(bf16x8_t, r);
-}
-
-// The i-th segment that this kernel takes (1 .. max_rows rows), for ascending i:
+// The i-th segment that has rows, for ascending i:
 // 256 segments at a time, one bit each.
 struct Fp8Segments {
   int s0 = -256, before = 0;
@@ -84,7 +73,7 @@ struct Fp8Segments {
       }
 #pragma unroll
       for (int u = 0; u < 4; ++u)
-        m[u] = __ballot(s0 + 64 * u + lane < n_seg && rows[u] > 0 && (!grp.max_rows || rows[u] <= grp.max_rows));
+        m[u] = __ballot(s0 + 64 * u + lane < n_seg && rows[u] > 0);
     }
   }
 };
@@ -106,7 +95,7 @@ struct Fp8Rows {
   static constexpr int kRing = WAVES * kWave, kPart = WAVES * R * C * 1024;
   static constexpr int kLds = kRing > kPart ? kRing : kPart;
   static_assert(!GLU || R % 2 == 0, "gate and up blocks come in pairs");
-  static_assert(D <= 4 && (D - 1) * kOps + kSc <= 63, "the waits count the copies in flight");
+  static_assert(kSc == 1 && D <= 4 && (D - 1) * kOps + kSc <= 63, "the waits count the copies in flight");
   static_assert(kLds <= 160 * 1024, "LDS");
 };
 
@@ -276,12 +265,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void fp8_rows_kernel(
           for (int k = 0; k < T::kOps; ++k) copy(nx, k);
 #pragma unroll
           for (int r = 0; r < R; ++r) {
-            f32x4_t p = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                  e4m3x8_to_bf16(a[r][q >> 1][2 * (q & 1)], a[r][q >> 1][2 * (q & 1) + 1]),
-                  e4m3x8_to_bf16(x2[0][q >> 1][2 * (q & 1)], x2[0][q >> 1][2 * (q & 1) + 1]), p, 0, 0, 0);
+            const f32x4_t p = mfma_e4m3_exact(join(a[r][0], a[r][1]), join(x2[0][0], x2[0][1]));
             const float sv = s[0] * (r < RO ? w0 : w1);
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[r][0][i] = __builtin_fmaf(p[i], sv, acc[r][0][i]);
@@ -311,52 +295,46 @@ __global__ __launch_bounds__(64 * WAVES, 2) void fp8_rows_kernel(
         w1 = w1n;
       }
 
-      // the ring becomes the waves' sums: [wave][R·C][64]
+      // the ring becomes the waves' sums: [wave][R·C][64], a lane's place changed so
+      // that the eight lanes of a row read different banks
       wait_copies<0>();
       __syncthreads();
       f32x4_t* part = reinterpret_cast<f32x4_t*>(lds);
+      auto place = [](int r, int l) { return l ^ r ^ (l >> 5 << 2); };
 #pragma unroll
       for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int c = 0; c < C; ++c) part[(wave * R * C + r * C + c) * 64 + lane] = acc[r][c];
+        for (int c = 0; c < C; ++c) part[(wave * R * C + r * C + c) * 64 + place(r, lane)] = acc[r][c];
       __syncthreads();
-      const bool wide = (ldy & 3) == 0 && (reinterpret_cast<uintptr_t>(y) & 7) == 0;
-      auto summed = [&](int u) {
-        f32x4_t v = part[u * 64 + lane];
+      auto summed = [&](int r, int c, int l) {
+        f32x4_t v = part[(r * C + c) * 64 + place(r, l)];
 #pragma unroll
         for (int p = 1; p < WAVES; ++p) {
-          const f32x4_t o = part[(p * R * C + u) * 64 + lane];
+          const f32x4_t o = part[((p * R + r) * C + c) * 64 + place(r, l)];
 #pragma unroll
           for (int i = 0; i < 4; ++i) v[i] += o[i];
         }
         return v;
       };
-      // unit u: output block (r, c), a lane's four columns of one row
-      for (int u = wave; u < RO * C; u += WAVES) {
-        const int r = u / C, c = u % C;
-        const int64_t row = m0 + 16 * c + col;
-        const int j = n0 + 16 * r + 4 * g;
-        f32x4_t v = summed(u);
-        if constexpr (GLU) {
-          const f32x4_t up = summed(u + RO * C);
+      // eight columns of a row a thread: a row's stores are next to each other
+      const uint64_t no_source = __ballot(soff[0] == kOOB8);
+      for (int q = threadIdx.x; q < kRows * 2 * RO; q += 64 * WAVES) {
+        const int row = q / (2 * RO), chunk = q % (2 * RO), r = chunk >> 1, l = 32 * (chunk & 1) + (row & 15);
+        if (m0 + row >= m_end) break;
+        u32x4_t v16;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = silu(v[i]) * up[i];
-        }
-        if (16 * c + col < kRows && row < m_end) {
-          const bool bad = GROUPED && source(16 * c + col) < 0;
-          uint16_t* to = y + row * ldy + j;
-          uint16_t b16[4];
+        for (int h = 0; h < 2; ++h) {
+          f32x4_t v = summed(r, row >> 4, l + 16 * h);
+          if constexpr (GLU) {
+            const f32x4_t up = summed(r + RO, row >> 4, l + 16 * h);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) b16[i] = bad ? uint16_t(0x7FC0) : f32_to_bf16(v[i]);
-          if (wide && j + 4 <= nout) {
-            *reinterpret_cast<u32x2_t*>(to) =
-                u32x2_t{uint32_t(b16[0]) | uint32_t(b16[1]) << 16, uint32_t(b16[2]) | uint32_t(b16[3]) << 16};
-          } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (j + i < nout) to[i] = b16[i];
+            for (int i = 0; i < 4; ++i) v[i] = silu(v[i]) * up[i];
           }
+          v16[2 * h] = pack_bf16x2(v[0], v[1]);
+          v16[2 * h + 1] = pack_bf16x2(v[2], v[3]);
         }
+        if (GROUPED && (no_source >> row & 1)) v16 = u32x4_t{0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u};
+        store8(y + (m0 + row) * ldy, n0 + 8 * chunk, nout, v16);
       }
       __syncthreads();   // the next pass fills the ring again
     }
@@ -366,10 +344,10 @@ __global__ __launch_bounds__(64 * WAVES, 2) void fp8_rows_kernel(
 constexpr int kDepth = 2;   // a deeper ring measured no faster anywhere
 
 template <int WAVES, int R, int X8, bool GROUPED, bool GLU>
-int go(const Fp8GemmArgs& a, int max_rows, hipStream_t s) {
+int go(const Fp8GemmArgs& a, hipStream_t s) {
   using T = Fp8Rows<WAVES, R, X8, kDepth, GROUPED, GLU>;
   const int nout = GLU ? a.n / 2 : a.n, per = 16 * T::RO;
-  const Fp8Grouped grp{a.row_index, a.seg_expert, a.seg_offsets, a.n_experts, a.m_total, int(a.t_x), max_rows, a.n_seg};
+  const Fp8Grouped grp{a.row_index, a.seg_expert, a.seg_offsets, a.n_experts, a.m_total, int(a.t_x), a.n_seg};
   const int64_t tiles = (nout + per - 1) / per;
   int64_t gy = std::min<int64_t>((a.t + 8 * X8 - 1) / (8 * X8), 65535);   // the grid's limit: more take turns
   if (GROUPED) {
@@ -386,27 +364,24 @@ int go(const Fp8GemmArgs& a, int max_rows, hipStream_t s) {
 
 template <int R>
 int dense(int x8, const Fp8GemmArgs& a, hipStream_t s) {
-  if (x8 == 4) return go<4, R, 4, false, false>(a, 0, s);
-  if (x8 == 8) return go<4, R, 8, false, false>(a, 0, s);
-  if constexpr (R <= 2) return x8 == 1 ? go<4, R, 1, false, false>(a, 0, s) : go<4, R, 2, false, false>(a, 0, s);
+  if (x8 == 4) return go<4, R, 4, false, false>(a, s);
+  if (x8 == 8) return go<4, R, 8, false, false>(a, s);
+  if constexpr (R <= 2) return x8 == 1 ? go<4, R, 1, false, false>(a, s) : go<4, R, 2, false, false>(a, s);
   return int(hipErrorInvalidValue);
 }
 
 template <bool GLU>
-int grouped(const Fp8RowsShape& p, const Fp8GemmArgs& a, int max_rows, hipStream_t s) {
-  if (p.waves == 4) return p.x8 == 1 ? go<4, 2, 1, true, GLU>(a, max_rows, s) : go<4, 2, 2, true, GLU>(a, max_rows, s);
-  if (p.x8 == 1) return go<2, 2, 1, true, GLU>(a, max_rows, s);
-  if (p.x8 == 2) return go<2, 4, 2, true, GLU>(a, max_rows, s);
-  return p.x8 == 4 ? go<2, 4, 4, true, GLU>(a, max_rows, s) : go<2, 4, 8, true, GLU>(a, max_rows, s);
+int grouped(const Fp8RowsShape& p, const Fp8GemmArgs& a, hipStream_t s) {
+  return p.waves == 4 ? go<4, 2, 1, true, GLU>(a, s) : go<2, 2, 1, true, GLU>(a, s);
 }
 
 }  // namespace
 
-int launch_fp8_rows(const Fp8GemmArgs& a, int max_rows, void* stream) {
+int launch_fp8_rows(const Fp8GemmArgs& a, void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const Fp8RowsShape p = fp8_rows_shape(a, max_rows);
+  const Fp8RowsShape p = fp8_rows_shape(a);
   if (a.n_seg == 0) return p.r == 4 ? dense<4>(p.x8, a, s) : p.r == 2 ? dense<2>(p.x8, a, s) : dense<1>(p.x8, a, s);
-  return a.glu ? grouped<true>(p, a, max_rows, s) : grouped<false>(p, a, max_rows, s);
+  return a.glu ? grouped<true>(p, a, s) : grouped<false>(p, a, s);
 }
 
 }  // namespace qmm

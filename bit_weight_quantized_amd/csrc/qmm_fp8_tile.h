@@ -34,7 +34,6 @@ struct Fp8TileArgs {
   const int32_t* seg_expert;
   const int32_t* seg_offsets;
   int n_experts, n_seg, m_total, t_x;
-  int skip_rows;          // segments of up to so many rows are left out
 };
 
 // A workgroup's tile: rows [m0, m_end) of the grouped or dense rows, output
@@ -48,8 +47,7 @@ struct Fp8Place {
   int sb;                 // scale rows of the gate half
 };
 
-// Row tiles of 256 segments from s0 on, four neighbouring ones a lane; segments of
-// up to skip_rows rows have none.
+// Row tiles of 256 segments from s0 on, four neighbouring ones a lane.
 template <int kT>
 struct Fp8Tiles {
   int at[5], tiles[4], sum, first, all;   // offsets, tiles; of the lane, before it, of the wave
@@ -62,7 +60,7 @@ struct Fp8Tiles {
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int rows = at[u + 1] - at[u];
-      tiles[u] = rows > a.skip_rows ? (rows + kT - 1) / kT : 0;
+      tiles[u] = rows > 0 ? (rows + kT - 1) / kT : 0;
       sum += tiles[u];
     }
     int incl = sum;
@@ -177,6 +175,16 @@ struct Fp8Source {
   }
 };
 
+// eight codes -> eight bf16
+__device__ __forceinline__ bf16x8_t e4m3x8_to_bf16(uint32_t lo, uint32_t hi) {
+  u32x4_t r;
+  r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false));
+  r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true));
+  r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false));
+  r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true));
+  return __builtin_bit_cast(bf16x8_t, r);
+}
+
 __device__ __forceinline__ i32x8_t join(const u32x4_t a, const u32x4_t b) {
   i32x8_t r;
 #pragma unroll
@@ -191,13 +199,23 @@ __device__ __forceinline__ i32x8_t join(const u32x4_t a, const u32x4_t b) {
 __device__ __forceinline__ f32x4_t mfma_e4m3(const i32x8_t a, const i32x8_t b) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
 }
+// the same from exact bf16, with fp32 sums
+__device__ __forceinline__ f32x4_t mfma_e4m3_exact(const i32x8_t a, const i32x8_t b) {
+  f32x4_t p = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(e4m3x8_to_bf16(uint32_t(a[2 * q]), uint32_t(a[2 * q + 1])),
+                                                e4m3x8_to_bf16(uint32_t(b[2 * q]), uint32_t(b[2 * q + 1])), p, 0, 0, 0);
+  return p;
+}
 
-// Eight neighbouring output columns c .. c + 7 of a row; `wide`: rows start at
-// multiples of 8 bytes.
-typedef uint32_t u32x4_at8_t __attribute__((ext_vector_type(4), aligned(8)));
-__device__ __forceinline__ void store8(uint16_t* row, int c, int nout, u32x4_t v, bool wide) {
-  if (wide && c + 8 <= nout) {
-    *reinterpret_cast<u32x4_at8_t*>(row + c) = v;
+// Eight neighbouring output columns c .. c + 7 of a row, at any alignment: the
+// memory takes 16 unaligned bytes in one store (rows of an odd length, 1449 x 10945,
+// d = 336: 54 us with single columns).
+typedef uint32_t u32x4_at2_t __attribute__((ext_vector_type(4), aligned(2)));
+__device__ __forceinline__ void store8(uint16_t* row, int c, int nout, u32x4_t v) {
+  if (c + 8 <= nout) {
+    *reinterpret_cast<u32x4_at2_t*>(row + c) = v;
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e)

@@ -170,11 +170,12 @@ __global__ __launch_bounds__(64 * WT * WN) void fp8_tile_kernel(Fp8TileArgs A) {
   // keep them in registers that the accumulators need
   auto multiply = [&](auto half, auto blocks, float w0, float w1) {
     constexpr int h = decltype(half)::value, kAhead = 4, N = decltype(blocks)::value * WS;
+    constexpr bool kExact = GROUPED && decltype(blocks)::value * WT == 1;   // 16 rows at most
     f32x4_t p[kAhead + 1];
 #pragma unroll
     for (int m = 0; m < (N ? N + kAhead : 0); ++m) {
       if (m < N)
-        p[m % (kAhead + 1)] = mfma_e4m3(a[m % WS], bx[m / WS]);
+        p[m % (kAhead + 1)] = kExact ? mfma_e4m3_exact(a[m % WS], bx[m / WS]) : mfma_e4m3(a[m % WS], bx[m / WS]);
       if (m >= kAhead) {
         const int u = m - kAhead, i = u / WS, j = u % WS;
         const float s = sx[i] * (GLU && j >= WS / 2 ? w1 : w0);
@@ -269,83 +270,74 @@ __global__ __launch_bounds__(64 * WT * WN) void fp8_tile_kernel(Fp8TileArgs A) {
   }
   wait_reads();
   phase_end();
-  const bool wide = (A.ldy & 3) == 0 && (reinterpret_cast<uintptr_t>(A.y) & 7) == 0;
 #pragma unroll 4
   for (int q = threadIdx.x; q < rows * kChunks; q += 64 * T::kWaves) {
     const int row = q / kChunks, chunk = q % kChunks;
     const u32x4_t v = *reinterpret_cast<const u32x4_t*>(lds + 2 * T::kOut * row + 16 * (chunk ^ (row & kMask)));
-    store8(A.y + (P.m0 + row) * A.ldy, n0 + 8 * chunk, nout, v, wide);
+    store8(A.y + (P.m0 + row) * A.ldy, n0 + 8 * chunk, nout, v);
   }
 }
 
 template <int TS, int WS, int WT, int WN, bool GROUPED, bool GLU>
-int go(const Fp8GemmArgs& a, int skip_rows, hipStream_t s) {
+int go(const Fp8GemmArgs& a, hipStream_t s) {
   using T = Fp8Tile<TS, WS, WT, WN, GROUPED, GLU>;
   auto kernel = fp8_tile_kernel<TS, WS, WT, WN, GROUPED, GLU>;
   const size_t bytes = T::kLds;
   const int nout = GLU ? a.n / 2 : a.n;
   const int64_t tiles_n = (int64_t(nout) + T::kOut - 1) / T::kOut;
   // grouped: no more row tiles than whole tiles of rows and one part tile a segment
-  const int64_t tiles_t = GROUPED ? int64_t(a.m_total) / T::kT + std::min<int64_t>(a.n_seg, a.m_total / (skip_rows + 1))
+  const int64_t tiles_t = GROUPED ? int64_t(a.m_total) / T::kT + std::min(a.n_seg, a.m_total)
                                   : (a.t + T::kT - 1) / T::kT;
   if (tiles_t == 0) return 0;
   if (tiles_n * tiles_t >= (int64_t(1) << 22)) return int(hipErrorInvalidValue);
   const Fp8TileArgs k{a.w, a.ws, a.n, a.d, fp8_blocks(a.d), a.x, a.xs, a.t, a.y, a.ldy, int(tiles_n), a.row_index,
-                      a.seg_expert, a.seg_offsets, a.n_experts, a.n_seg, a.m_total, int(a.t_x), skip_rows};
+                      a.seg_expert, a.seg_offsets, a.n_experts, a.n_seg, a.m_total, int(a.t_x)};
   launch_kernel_lds(kernel, dim3(unsigned(tiles_n * tiles_t)), dim3(64 * T::kWaves), bytes, s, k);
   return int(hipGetLastError());
 }
 
-}  // namespace
-
-namespace {
-
 template <bool GROUPED, bool GLU>
-int go(bool large, const Fp8GemmArgs& a, int skip_rows, hipStream_t s) {
-  return large ? go<8, 4, 2, 4, GROUPED, GLU>(a, skip_rows, s) : go<4, 2, 2, 4, GROUPED, GLU>(a, skip_rows, s);
+int go(bool large, const Fp8GemmArgs& a, hipStream_t s) {
+  return large ? go<8, 4, 2, 4, GROUPED, GLU>(a, s) : go<4, 2, 1, 4, GROUPED, GLU>(a, s);
 }
 
 }  // namespace
 
-int launch_fp8_tile(const Fp8GemmArgs& a, bool large, int skip_rows, void* stream) {
+int launch_fp8_tile(const Fp8GemmArgs& a, bool large, void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (a.n_seg == 0) return go<false, false>(large, a, 0, s);
-  return a.glu ? go<true, true>(large, a, skip_rows, s) : go<true, false>(large, a, skip_rows, s);
+  if (a.n_seg == 0) return go<false, false>(large, a, s);
+  return a.glu ? go<true, true>(large, a, s) : go<true, false>(large, a, s);
 }
 
 int launch_fp8_product(const Fp8GemmArgs& a, void* stream) {
   if (a.n_seg == 0) {
-    // Estimates in us of the three kernels, from the time of one step of one
-    // workgroup: few-row 0.7, 0.85 or 1.3 for its waves' blocks (r = 1, 2, 4), 128 x
-    // 128 tiles 0.66 and 0.1 for each round, 256 x 256 tiles 1.7, times the rounds of
-    // workgroups that 256 CUs take.  Measured on either side: 13824 x 5120 with 128
-    // rows 32.3 us few-row, 36.0 (128), with 192 rows 45.2, 36.2; with 512 rows 54.7
-    // (128), 66.7 (256), with 1024 rows 97.0, 72.0; 4096 x 7168 with 512 rows 39.8
-    // few-row, 42.2 (128), with 1024 rows 43.6 (128), 78.5 (256).
+    // Estimates in us of the three kernels from nb steps and the rounds of workgroups
+    // that 256 CUs take: a start and end, and a time for each step, which for the
+    // few-row kernel (four waves share the steps) depends on its weight blocks and on
+    // rows that share their cache lines, and of which three 64 x 128 tiles a CU hide
+    // a part from each other.  Measured few-row, 64 x 128, 256 x 256: 768 x 1903 x
+    // 4240 29.6, 24.8, 51.2; 512 x 4096 x 4096 20.1, 23.8, 43.8; 1024 x 4096 x 4096
+    // 40.0, 29.3, 45.8; 1052 x 10215 x 1296 63.4, 32.7, 26.8; 129 x 5619 x 4352 19.6,
+    // 24.4, 42.2.
     auto rounds = [](int64_t workgroups) { return double((workgroups + 255) / 256); };
-    auto tiles = [&](int side) { return ((a.t + side - 1) / side) * ((int64_t(a.n) + side - 1) / side); };
-    const Fp8RowsShape p = fp8_rows_shape(a, 0);
+    auto tiles = [&](int rows, int cols) { return ((a.t + rows - 1) / rows) * ((int64_t(a.n) + cols - 1) / cols); };
+    const Fp8RowsShape p = fp8_rows_shape(a);
     const int nb = fp8_blocks(a.d);
-    const double few = ((nb + 3) / 4) * (p.r == 4 ? 1.3 : p.r == 2 ? 0.85 : 0.7) * rounds(p.workgroups);
-    const double small = nb * (0.66 * rounds(tiles(128)) + 0.1), large = nb * 1.7 * rounds(tiles(256));
-    if (a.t <= kFp8RowsMax || (few <= small && few <= large)) return launch_fp8_rows(a, 0, stream);
-    return launch_fp8_tile(a, large < small, 0, stream);
+    const double step = (p.r == 4 ? 0.95 : p.r == 2 ? 0.8 : 0.6) * (a.d % kFp8Block ? 1.4 : 1.0);
+    const double few = rounds(p.workgroups) * (3 + (nb + 3) / 4 * step);
+    const double r64 = rounds(tiles(64, 128)), small = 3 + nb * std::max(0.65, 0.4 * r64) + 0.6 * r64;
+    const double large = rounds(tiles(256, 256)) * (8 + 1.5 * nb);
+    if (a.t <= kFp8RowsMax || (few <= small && few <= large)) return launch_fp8_rows(a, stream);
+    return launch_fp8_tile(a, large < small, stream);
   }
-  // Few rows a segment: the few-row kernel alone, in several passes where a segment
-  // is longer, as long as there cannot be very many (64 experts of 2816 x 2048: 48
-  // rows a segment 117.6 us alone, 135.5 split; 96 rows 186.2, 165.5).
-  if (a.max_seg_rows <= kFp8RowsMax || (a.max_seg_rows <= 1024 && fp8_usual_rows(a) <= 64))
-    return launch_fp8_rows(a, 0, stream);
-  // two launches that split the segments on the device; armed events: the
-  // start with the first, the stop with the second
-  const ProfileEvents pe = take_profile_events();
-  arm_profile_events({pe.start, nullptr});
-  const int err = launch_fp8_rows(a, kFp8RowsMax, stream);
-  arm_profile_events({nullptr, err ? nullptr : pe.stop});
-  if (err) return err;
-  // large tiles from 256 rows a segment (64 experts of 2816 x 2048: 192 rows 157.8 us
-  // small, 166.3 large; 384 rows 246.6, 233.8; of 4096 x 3584, 512 rows 731, 611)
-  return launch_fp8_tile(a, int64_t(a.m_total) >= int64_t(256) * a.n_seg, kFp8RowsMax, stream);
+  // The few-row kernel up to 3 rows a segment, if none can be long (128 experts of
+  // 3584 x 2048: 1 row 74 us few-row, 83 (64 x 128); 4 rows 116 and 103).  Large tiles
+  // from 80 rows on, if half of the CUs have one (64 experts of 2816 x 2048: 63 rows
+  // 88 us (64 x 128), 87 (256 x 256), 96 rows 103 and 94, 192 rows 151 and 125; 8 of
+  // 704 x 4080 with 150 rows, 24 large tiles: 29 and 43).
+  if (a.max_seg_rows <= kFp8RowsMax && fp8_usual_rows(a) <= 3) return launch_fp8_rows(a, stream);
+  const int64_t tiles = std::max<int64_t>(a.n_seg, a.m_total / 256) * ((int64_t(a.n) + 255) / 256);
+  return launch_fp8_tile(a, int64_t(a.m_total) >= int64_t(80) * a.n_seg && tiles >= 128, stream);
 }
 
 }  // namespace qmm
