@@ -367,7 +367,10 @@ qmm_status qmm_fp8_quant(const qmm_bf16* x, int64_t t, int64_t d, int64_t ldx, u
 /* Y = X·Wᵀ on block-scaled e4m3:
  *   y[t][n] = Σ_b xs[t][b]·ws[n/128][b]·Σ_{k in b} x[t][k]·w[n][k]
  * products and block sums in the matrix cores, the sum over the blocks in fp32,
- * rounded once to bf16.  y: bf16 rows of n at stride ldy (elements, >= n); the
+ * rounded once to bf16.  For t <= 16, and in segments of up to 16 rows of a grouped
+ * call with few rows a segment, the block sums have fp32's precision; otherwise the
+ * matrix cores' e4m3 instruction aligns each 8 neighbouring products to the largest
+ * and cuts what is 2^-13 below it.  y: bf16 rows of n at stride ldy (elements, >= n); the
  * bytes between them are left alone.  No workspace; the order of every sum
  * depends on the shape alone. */
 qmm_status qmm_fp8_gemm(const uint8_t* w, const float* w_scales, int64_t t, int64_t n, int64_t d, const uint8_t* x,
@@ -473,10 +476,11 @@ qmm_status qmm_norm_residual(int64_t t, int64_t d, const qmm_bf16* o, int64_t ld
 /* Per-kernel GPU timing (per-op GPU timestamps, as in the op profiling of
  * "LLM Decode / Prefill 优化案例（Metal）", Step 1).  Arms two caller-owned
  * hipEvent_t handles for the next qmm_gemv / qmm_gemm / qmm_grouped_gemm /
- * qmm_grouped_gemm_swiglu / qmm_moe_combine / qmm_route / qmm_stream_read call
- * on this thread: its kernels are launched with hipExtLaunchKernel so `start`
+ * qmm_grouped_gemm_swiglu / qmm_moe_combine / qmm_route / qmm_stream_read /
+ * qmm_fp8_* / qmm_route_topk / qmm_moe_gather / qmm_norm_residual call on this
+ * thread: its kernels are launched with hipExtLaunchKernel so `start`
  * is stamped by the dispatch of its first kernel and `stop` by that of its last
- * (calls of several kernels: qmm_route, qmm_gemm split along K), and their
+ * (calls of several kernels: qmm_route, qmm_route_topk, qmm_gemm split along K), and their
  * elapsed time is the call's execution time.  Either may be NULL.  The arming
  * is consumed by that next call; a call rejected by validation leaves it armed. */
 qmm_status qmm_profile_next(void* start_event, void* stop_event);
