@@ -105,9 +105,13 @@ inline int64_t topk_chunk(int64_t t) {
   if ((t + c - 1) / c > kTopkMaxChunks) c = round_up((t + kTopkMaxChunks - 1) / kTopkMaxChunks, kTopkChunk);
   return c;
 }
+// The workspace: a chunk's counts by expert, a byte each where they fit, in rows of
+// whole words, else 4 bytes.
+__host__ __device__ constexpr bool topk_bytes(int64_t chunk) { return chunk <= kTopkChunk; }
+__host__ __device__ constexpr int topk_row(int ne) { return (ne + 3) / 4 * 4; }
 inline size_t topk_ws_bytes(int64_t t, int ne) {
   const int64_t c = topk_chunk(t);
-  return t <= c ? 0 : size_t((t + c - 1) / c) * size_t(ne) * 4;
+  return t <= c ? 0 : size_t((t + c - 1) / c) * (topk_bytes(c) ? size_t(topk_row(ne)) : size_t(ne) * 4);
 }
 int launch_topk(const TopkArgs& a, void* stream);
 

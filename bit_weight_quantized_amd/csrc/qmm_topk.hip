@@ -8,18 +8,22 @@
 //   groups ranked by their largest c or the sum of their two largest; the k
 //   largest c of the kept groups; weight p (/ Σ p of the chosen) · scale
 //
-// One workgroup of 16 waves per chunk of tokens, one wave per token: lane i
-// holds experts J·i .. J·i + J-1 as order-preserving integer keys, so the
-// lowest lane and the lowest j among equal keys is the lowest expert.  A round
-// takes the largest key of the wave (DPP, then scalar registers) and the
-// winning lane drops it.
+// One workgroup of 16 waves per chunk of tokens.  Up to 256 experts and k = 16, a
+// row of 16 lanes has a token (four a wave), so that no step leaves the row's DPP:
+// lane i holds experts n·i .. n·i + n-1, n = ceil(experts / 16).  A round takes the
+// largest order-preserving integer key of the row, the lowest expert that has it (a
+// second reduction) and drops it.  More experts: a wave has a token, and scalar
+// instructions find the winner in the comparisons' masks.
+// Bound by instructions: 16384 tokens x 256 experts in 8 groups, k = 8, are 2 us of
+// bytes; a sigmoid that rounds as the formula does is 35 instructions alone.
 //
 // Grouping counts the chunk's tokens per expert in LDS (integer atomics, order
 // free).  One chunk: the same workgroup scans the counts and places its rows.
-// More: the counts go to the workspace, and a second kernel, one workgroup per
-// chunk, adds up every chunk's counts (at most 256 per expert) and places the
-// chunk's rows.  Rows of an expert ascend with the token, found from a bitmap
-// of the chunk's tokens per expert, so nothing depends on timing.
+// More: the counts go to the workspace (a byte each, as a chunk of up to 128 tokens
+// allows), and a second kernel, one workgroup per chunk, adds up every chunk's counts
+// (at most 256 per expert) and places the chunk's rows.  Rows of an expert ascend
+// with the token, found from a bitmap of the chunk's tokens per expert, so nothing
+// depends on timing.
 #include <hip/hip_runtime.h>
 
 #include <math.h>
@@ -32,6 +36,7 @@ namespace qmm {
 namespace {
 
 constexpr int kTkWords = kTopkChunk / 32;        // bitmap words of an expert and pass
+constexpr int kTopkRowMaxK = 16;                 // lane r of a row holds the r-th choice
 static_assert(kRouteMaxExperts == 64 * kTopkWaves, "a thread of the workgroup owns an expert");
 
 // Order-preserving map to an unsigned key; 0 marks an expert that cannot be
@@ -40,6 +45,21 @@ __device__ __forceinline__ uint32_t choice_key(float c) {
   const uint32_t b = __float_as_uint(c) == 0x80000000u ? 0u : __float_as_uint(c);
   const uint32_t flip = uint32_t(int32_t(b) >> 31) | 0x80000000u;
   return c > -INFINITY ? (b ^ flip) : 0u;
+}
+
+// Smallest of the 16 lanes of a row; every lane gets it.
+__device__ __forceinline__ uint32_t umin(uint32_t a, uint32_t b) { return a < b ? a : b; }
+__device__ __forceinline__ uint32_t row_umin(uint32_t v) {
+  v = umin(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0xB1, 0xF, 0xF, false)));
+  v = umin(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x4E, 0xF, 0xF, false)));
+  v = umin(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x141, 0xF, 0xF, false)));
+  return umin(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x140, 0xF, 0xF, false)));
+}
+__device__ __forceinline__ float row_max(float v) {
+  v = fmaxf(v, dpp_f<0xB1>(v));
+  v = fmaxf(v, dpp_f<0x4E>(v));
+  v = fmaxf(v, dpp_f<0x141>(v));
+  return fmaxf(v, dpp_f<0x140>(v));
 }
 
 __device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
@@ -59,10 +79,7 @@ __device__ __forceinline__ float wave_sum(float v) {
 }
 
 __device__ __forceinline__ float wave_max(float v) {
-  v = fmaxf(v, dpp_f<0xB1>(v));
-  v = fmaxf(v, dpp_f<0x4E>(v));
-  v = fmaxf(v, dpp_f<0x141>(v));
-  v = fmaxf(v, dpp_f<0x140>(v));
+  v = row_max(v);
   return fmaxf(fmaxf(readlane_f(v, 0), readlane_f(v, 16)), fmaxf(readlane_f(v, 32), readlane_f(v, 48)));
 }
 
@@ -154,8 +171,235 @@ __device__ __forceinline__ void place_rows(TopkLds<WAVES>& lds, const int32_t* i
   }
 }
 
-// J experts a lane; ONE: all tokens are one chunk, and the workgroup groups
-// them itself.
+// The end of a chunk: its counts to the workspace, or (ONE: it is the only one) the
+// tables themselves.
+template <int WAVES, bool ONE>
+__device__ __forceinline__ void finish(const TopkArgs& a, TopkLds<WAVES>& lds, const int32_t* chosen, int chunk,
+                                       int64_t t0, int64_t t1) {
+  const int tid = threadIdx.x;
+  __syncthreads();                                // counts; the ids of the chunk
+  if constexpr (!ONE) {
+    if (topk_bytes(chunk)) {
+      if (tid < topk_row(a.ne))   // zeros at the end
+        reinterpret_cast<uint8_t*>(a.ws)[int64_t(blockIdx.x) * topk_row(a.ne) + tid] = uint8_t(lds.count[tid]);
+    } else if (tid < a.ne) {
+      a.ws[int64_t(blockIdx.x) * a.ne + tid] = lds.count[tid];
+    }
+  } else {
+    int total;
+    const int at = block_scan<WAVES>(lds.count[tid], lds.wsum, &total);
+    lds.first[tid] = at;
+    if (tid < a.ne) {
+      a.seg_expert[tid] = tid;
+      a.seg_offsets[tid] = at;
+    }
+    if (tid == 0) a.seg_offsets[a.ne] = total;
+    for (int64_t i = total + tid; i < a.t * a.k; i += 64 * WAVES) a.row_index[i] = -1;
+    place_rows(lds, chosen, t0, t1, a.k, a.row_index, a.slot_row);
+  }
+}
+
+// Logits of a row of 16 lanes: J a lane from e0 on; `whole`: the row has 16·J, read
+// at any alignment.
+template <int J, bool BF16>
+__device__ __forceinline__ void load_row(const void* logits, int64_t at, int e0, int n, int ne, bool whole, float* v) {
+  if (whole && J >= 4) {
+    if constexpr (BF16) {
+      typedef uint32_t word2_t __attribute__((ext_vector_type(2), aligned(2)));
+      const uint16_t* p = static_cast<const uint16_t*>(logits) + at + e0;
+#pragma unroll
+      for (int j = 0; j < J / 4; ++j) {
+        const word2_t w = reinterpret_cast<const word2_t*>(p)[j];
+        v[4 * j] = bf16_lo(w[0]);
+        v[4 * j + 1] = bf16_hi(w[0]);
+        v[4 * j + 2] = bf16_lo(w[1]);
+        v[4 * j + 3] = bf16_hi(w[1]);
+      }
+    } else {
+      typedef float float4_at4_t __attribute__((ext_vector_type(4), aligned(4)));
+      const float* p = static_cast<const float*>(logits) + at + e0;
+#pragma unroll
+      for (int j = 0; j < J / 4; ++j) {
+        const float4_at4_t w = reinterpret_cast<const float4_at4_t*>(p)[j];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[4 * j + i] = w[i];
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const float l = logit<BF16>(logits, at + min(e0 + j, ne - 1));
+    v[j] = j < n && e0 + j < ne ? l : -INFINITY;
+  }
+}
+
+// A row of 16 lanes a token, J experts a lane at most.
+template <int WAVES, int J, bool BF16, bool SIGMOID, bool ONE>
+__global__ __launch_bounds__(64 * WAVES) void topk_row_kernel(TopkArgs a, int chunk) {
+  __shared__ TopkLds<WAVES> lds;
+  __shared__ float cs[WAVES][J][64];             // a token's scores, [j][lane]
+  __shared__ __attribute__((aligned(16))) float group_value[WAVES][4][kRouteMaxK];   // at most 64 groups
+  __shared__ uint32_t group_kept[WAVES][4][kRouteMaxK];
+  __shared__ int32_t chosen[ONE ? kTopkChunk * kTopkRowMaxK : 1];
+  const int tid = threadIdx.x;
+  const int lane = tid & 63, rl = lane & 15, rt = lane >> 4;   // lane of the row, row of the wave
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t t0 = int64_t(blockIdx.x) * chunk, t1 = min(a.t, t0 + chunk);
+  const int ne = a.ne, k = a.k, groups = a.groups;
+  const int n = (ne + 15) >> 4, e0 = n * rl;      // the lane's experts
+  const int gs = ne / groups;                     // experts of a group
+  const bool by_logit = !SIGMOID && !a.bias && (groups == 1 || !a.top2);
+  // Where a group is a power of two of whole lanes (as 256 experts in 8 groups: 2) a
+  // lane's experts share its group, and its lanes exchange by DPP; otherwise each
+  // lane goes over the scores of its groups in LDS.
+  const int own = gs % n == 0 ? gs / n : 0;
+  const bool aligned = own == 1 || own == 2 || own == 4 || own == 8 || own == 16;
+  const int own_shift = aligned ? __builtin_ctz(own) : 0;
+  const int g0 = min(e0, ne - 1) / gs, g0_at = min(e0, ne - 1) - g0 * gs;   // the first expert's group, and its place there
+  const bool whole = ne == 16 * J;
+
+  lds.count[tid] = 0;
+  float bias[J];
+#pragma unroll
+  for (int j = 0; j < J; ++j) bias[j] = a.bias ? a.bias[min(e0 + j, ne - 1)] : 0.f;
+  float* value_of = group_value[wave][rt];
+  uint32_t* kept_of = group_kept[wave][rt];
+#pragma unroll
+  for (int i = 0; i < kRouteMaxK / 16; ++i) value_of[16 * i + rl] = -INFINITY;
+  __syncthreads();
+
+  for (int64_t first = t0 + 4 * wave; first < t1; first += 4 * WAVES) {
+    const int64_t tok = first + rt;
+    const bool live = tok < t1;
+    float l[J];
+    uint32_t key[J];
+    int from = e0;
+    asm volatile("" : "+v"(from));                // what hangs on it is not kept from token to token
+    load_row<J, BF16>(a.logits, min(tok, t1 - 1) * a.ld, from, n, ne, whole, l);
+    float top = 0.f, total = 1.f;
+    if constexpr (!SIGMOID) {
+      float m = l[0];
+#pragma unroll
+      for (int j = 1; j < J; ++j) m = fmaxf(m, l[j]);
+      m = row_max(m);
+      top = m > -INFINITY ? m : 0.f;              // nothing left: every e^(l - top) is 0
+      float z = 0.f;
+#pragma unroll
+      for (int j = 0; j < J; ++j) z += expf(l[j] - top);
+      total = sum16(z);
+    }
+    auto prob = [&](float v) { return SIGMOID ? sigmoid(v) : total > 0.f ? expf(v - top) / total : total; };
+    Two two = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const float p = by_logit ? l[j] : prob(l[j]);
+      float c = by_logit ? p : p + bias[j];
+      if (l[j] == -INFINITY) c = -INFINITY;
+      key[j] = choice_key(c);
+      if (key[j] == 0u) c = -INFINITY;            // NaN ranks with the masked
+      l[j] = SIGMOID ? p : l[j];                  // what the weight is made from
+      take(two, c);
+      if (groups > 1 && !aligned) cs[wave][j][lane] = c;
+    }
+    if (groups > 1) {
+      auto worth = [&](const Two& v) { return a.top2 && v.second > -INFINITY ? v.first + v.second : v.first; };
+      // rank among the groups: larger values first, equal ones by index
+      auto kept = [&](float v, int q) {
+        int rank = 0;
+        for (int o = 0; o < groups; o += 4) {
+          const f32x4_t u = *reinterpret_cast<const f32x4_t*>(value_of + o);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) rank += u[i] > v || (u[i] == v && o + i < q) ? 1 : 0;
+        }
+        return rank < a.keep;
+      };
+      if (aligned) {
+        if (own > 1) merge_dpp<0xB1>(two);
+        if (own > 2) merge_dpp<0x4E>(two);
+        if (own > 4) merge_dpp<0x141>(two);
+        if (own > 8) merge_dpp<0x140>(two);
+        const int q = rl >> own_shift;
+        const float v = worth(two);
+        if (q < groups) value_of[q] = v;
+        __builtin_amdgcn_wave_barrier();
+        const bool keep = q < groups && kept(v, q);
+#pragma unroll
+        for (int j = 0; j < J; ++j) key[j] = keep ? key[j] : 0u;
+      } else {
+        __builtin_amdgcn_wave_barrier();
+        for (int q = rl; q < groups; q += 16) {
+          Two best = {-INFINITY, -INFINITY};
+          int at = q * gs / n, j = q * gs - at * n;
+          for (int i = 0; i < gs; ++i) {
+            take(best, cs[wave][j][16 * rt + at]);
+            if (++j == n) {
+              j = 0;
+              ++at;
+            }
+          }
+          value_of[q] = worth(best);
+        }
+        __builtin_amdgcn_wave_barrier();
+        for (int q = rl; q < groups; q += 16) kept_of[q] = kept(value_of[q], q) ? 1u : 0u;
+        __builtin_amdgcn_wave_barrier();
+        int q = g0, i = g0_at;
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          key[j] = kept_of[min(q, groups - 1)] ? key[j] : 0u;
+          if (++i == gs) {
+            i = 0;
+            ++q;
+          }
+        }
+      }
+      __builtin_amdgcn_wave_barrier();
+    }
+    // probabilities (softmax: logits) for the weights of the chosen
+#pragma unroll
+    for (int j = 0; j < J; ++j) cs[wave][j][lane] = l[j];
+
+    // an expert's code, 16·lane + j, has the experts' order
+    uint32_t mine = ~0u;
+    for (int r = 0; r < k; ++r) {
+      uint32_t best = key[0];
+#pragma unroll
+      for (int j = 1; j < J; ++j) best = umax(best, key[j]);
+      const uint32_t m = group_umax<16>(best);
+      if (!__any(m != 0u)) break;                 // nothing left in any row
+      uint32_t at = 255u;
+#pragma unroll
+      for (int j = J - 1; j >= 0; --j) at = key[j] == m ? uint32_t(j) : at;
+      const uint32_t win = row_umin(at + 16u * uint32_t(rl));
+      const uint32_t drop = win - 16u * uint32_t(rl);
+#pragma unroll
+      for (int j = 0; j < J; ++j) key[j] = drop == uint32_t(j) ? 0u : key[j];
+      mine = rl == r && m != 0u ? win : mine;
+    }
+    __builtin_amdgcn_wave_barrier();
+    const int e = mine != ~0u ? int(mine >> 4) * n + int(mine & 15u) : -1;
+    float w = 0.f;
+    if (e >= 0) {
+      w = cs[wave][mine & 15u][16 * rt + int(mine >> 4)];
+      if constexpr (!SIGMOID) w = prob(w);
+    }
+    if (a.renorm) {
+      const float sum = sum16(w);
+      w = sum == 0.f ? 0.f : w / sum;             // a NaN stays one
+    }
+    __builtin_amdgcn_wave_barrier();
+    if (rl < k && live) {
+      a.topk[tok * k + rl] = e;
+      a.weights[tok * k + rl] = w * a.scale;
+      if (e >= 0) atomicAdd(&lds.count[e], 1);
+      if constexpr (ONE) chosen[(tok - t0) * k + rl] = e;
+    }
+  }
+  finish<WAVES, ONE>(a, lds, chosen, chunk, t0, t1);
+}
+
+// A wave a token, J experts a lane; ONE: all tokens are one chunk, and the workgroup
+// groups them itself.
 template <int WAVES, int J, bool BF16, bool SIGMOID, bool ONE>
 __global__ __launch_bounds__(64 * WAVES) void topk_kernel(TopkArgs a, int chunk) {
   __shared__ TopkLds<WAVES> lds;
@@ -312,21 +556,7 @@ __global__ __launch_bounds__(64 * WAVES) void topk_kernel(TopkArgs a, int chunk)
       if constexpr (ONE) chosen[(tok - t0) * k + lane] = mine_e;
     }
   }
-  __syncthreads();                                // counts; the ids of the chunk
-  if constexpr (!ONE) {
-    if (tid < ne) a.ws[int64_t(blockIdx.x) * ne + tid] = lds.count[tid];
-  } else {
-    int total;
-    const int at = block_scan<WAVES>(lds.count[tid], lds.wsum, &total);
-    lds.first[tid] = at;
-    if (tid < ne) {
-      a.seg_expert[tid] = tid;
-      a.seg_offsets[tid] = at;
-    }
-    if (tid == 0) a.seg_offsets[ne] = total;
-    for (int64_t i = total + tid; i < a.t * k; i += 64 * WAVES) a.row_index[i] = -1;
-    place_rows(lds, chosen, t0, t1, k, a.row_index, a.slot_row);
-  }
+  finish<WAVES, ONE>(a, lds, chosen, chunk, t0, t1);
 }
 
 __global__ __launch_bounds__(64 * kTopkWaves) void topk_place_kernel(
@@ -341,23 +571,52 @@ __global__ __launch_bounds__(64 * kTopkWaves) void topk_place_kernel(
   lds.count[tid] = 0;
   lds.first[tid] = 0;
   __syncthreads();
-  const int span = (ne + 63) / 64 * 64, parts = kThreads / span;
-  const int e = tid % span, part = tid / span;
-  if (e < ne && part < parts) {
-    int before = 0, all = 0;
-    for (int c0 = part; c0 < chunks; c0 += 8 * parts) {
-      int v[8];
+  if (topk_bytes(chunk)) {
+    // four experts a thread, in sums of 16 bits (256 chunks of at most 128)
+    const int words = (ne + 3) / 4, parts = kThreads / words;
+    const int e = tid % words, part = tid / words;
+    const uint32_t* row = reinterpret_cast<const uint32_t*>(counts) + e;
+    if (part < parts) {
+      uint32_t before[2] = {0, 0}, all[2] = {0, 0};
+      for (int c0 = part; c0 < chunks; c0 += 16 * parts) {
+        uint32_t v[16];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) v[u] = counts[int64_t(min(c0 + u * parts, chunks - 1)) * ne + e];
+        for (int u = 0; u < 16; ++u) v[u] = row[int64_t(min(c0 + u * parts, chunks - 1)) * words];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const int c = c0 + u * parts;
-        before += c < me ? v[u] : 0;
-        all += c < chunks ? v[u] : 0;
+        for (int u = 0; u < 16; ++u) {
+          const int c = c0 + u * parts;
+          const uint32_t lo = c < chunks ? v[u] & 0x00FF00FFu : 0u, hi = c < chunks ? v[u] >> 8 & 0x00FF00FFu : 0u;
+          all[0] += lo;
+          all[1] += hi;
+          before[0] += c < me ? lo : 0u;
+          before[1] += c < me ? hi : 0u;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        atomicAdd(&lds.count[4 * e + i], int(all[i & 1] >> (8 * (i & 2)) & 0xFFFFu));
+        atomicAdd(&lds.first[4 * e + i], int(before[i & 1] >> (8 * (i & 2)) & 0xFFFFu));
       }
     }
-    atomicAdd(&lds.count[e], all);
-    atomicAdd(&lds.first[e], before);
+  } else {
+    const int span = (ne + 63) / 64 * 64, parts = kThreads / span;
+    const int e = tid % span, part = tid / span;
+    if (e < ne && part < parts) {
+      int before = 0, all = 0;
+      for (int c0 = part; c0 < chunks; c0 += 8 * parts) {
+        int v[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) v[u] = counts[int64_t(min(c0 + u * parts, chunks - 1)) * ne + e];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int c = c0 + u * parts;
+          before += c < me ? v[u] : 0;
+          all += c < chunks ? v[u] : 0;
+        }
+      }
+      atomicAdd(&lds.count[e], all);
+      atomicAdd(&lds.first[e], before);
+    }
   }
   __syncthreads();
   int total;
@@ -376,26 +635,18 @@ __global__ __launch_bounds__(64 * kTopkWaves) void topk_place_kernel(
   place_rows(lds, topk + t0 * k, t0, min(t, t0 + chunk), k, row_index, slot_row);
 }
 
-template <int J, bool BF16, bool SIGMOID>
-int go(const TopkArgs& a, hipStream_t s) {
+// One kernel for one chunk, else the second one places the rows.
+using TopkKernel = void (*)(TopkArgs, int);
+int go(const TopkArgs& a, int waves, TopkKernel one, TopkKernel more, hipStream_t s) {
   const int64_t chunk = topk_chunk(a.t);
   const unsigned chunks = a.t <= chunk ? 1u : unsigned((a.t + chunk - 1) / chunk);   // no tokens: the tables alone
   const ProfileEvents pe = take_profile_events();
   const hipEvent_t ev0 = static_cast<hipEvent_t>(pe.start), ev1 = static_cast<hipEvent_t>(pe.stop);
   if (chunks == 1) {
-    // a few tokens: fewer waves, shorter barriers
-    if constexpr (J <= 4) {
-      if (a.t <= 8) {
-        hipExtLaunchKernelGGL((topk_kernel<4, J, BF16, SIGMOID, true>), dim3(1), dim3(256), 0, s, ev0, ev1, 0, a, int(chunk));
-        return int(hipGetLastError());
-      }
-    }
-    hipExtLaunchKernelGGL((topk_kernel<kTopkWaves, J, BF16, SIGMOID, true>), dim3(1), dim3(64 * kTopkWaves), 0, s, ev0,
-                          ev1, 0, a, int(chunk));
+    hipExtLaunchKernelGGL(one, dim3(1), dim3(64 * waves), 0, s, ev0, ev1, 0, a, int(chunk));
     return int(hipGetLastError());
   }
-  hipExtLaunchKernelGGL((topk_kernel<kTopkWaves, J, BF16, SIGMOID, false>), dim3(chunks), dim3(64 * kTopkWaves), 0, s,
-                        ev0, nullptr, 0, a, int(chunk));
+  hipExtLaunchKernelGGL(more, dim3(chunks), dim3(64 * kTopkWaves), 0, s, ev0, nullptr, 0, a, int(chunk));
   const int err = int(hipGetLastError());
   if (err) return err;
   hipExtLaunchKernelGGL(topk_place_kernel, dim3(chunks), dim3(64 * kTopkWaves), 0, s, nullptr, ev1, 0,
@@ -404,10 +655,25 @@ int go(const TopkArgs& a, hipStream_t s) {
   return int(hipGetLastError());
 }
 
-template <int J>
+template <bool BF16, bool SIGMOID>
 int go(const TopkArgs& a, hipStream_t s) {
-  if (a.sigmoid) return a.bf16 ? go<J, true, true>(a, s) : go<J, false, true>(a, s);
-  return a.bf16 ? go<J, true, false>(a, s) : go<J, false, false>(a, s);
+  constexpr int W = kTopkWaves;
+  if (a.ne <= 256 && a.k <= kTopkRowMaxK) {
+    // 16 tokens at once: fewer waves, shorter barriers
+    const bool few = a.t <= 16;
+    const int waves = few ? 4 : W;
+    if (a.ne <= 64)
+      return go(a, waves, few ? topk_row_kernel<4, 4, BF16, SIGMOID, true> : topk_row_kernel<W, 4, BF16, SIGMOID, true>,
+                topk_row_kernel<W, 4, BF16, SIGMOID, false>, s);
+    if (a.ne <= 128)
+      return go(a, waves, few ? topk_row_kernel<4, 8, BF16, SIGMOID, true> : topk_row_kernel<W, 8, BF16, SIGMOID, true>,
+                topk_row_kernel<W, 8, BF16, SIGMOID, false>, s);
+    return go(a, waves, few ? topk_row_kernel<4, 16, BF16, SIGMOID, true> : topk_row_kernel<W, 16, BF16, SIGMOID, true>,
+              topk_row_kernel<W, 16, BF16, SIGMOID, false>, s);
+  }
+  if (a.ne <= 512)
+    return go(a, W, topk_kernel<W, 8, BF16, SIGMOID, true>, topk_kernel<W, 8, BF16, SIGMOID, false>, s);
+  return go(a, W, topk_kernel<W, 16, BF16, SIGMOID, true>, topk_kernel<W, 16, BF16, SIGMOID, false>, s);
 }
 
 // Weighted sum of the chosen experts' rows, one workgroup per token and 2048
@@ -461,11 +727,8 @@ __global__ __launch_bounds__(256) void gather_kernel(GatherArgs a) {
 
 int launch_topk(const TopkArgs& a, void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (a.ne <= 64) return go<1>(a, s);
-  if (a.ne <= 128) return go<2>(a, s);
-  if (a.ne <= 256) return go<4>(a, s);
-  if (a.ne <= 512) return go<8>(a, s);
-  return go<16>(a, s);
+  if (a.sigmoid) return a.bf16 ? go<true, true>(a, s) : go<false, true>(a, s);
+  return a.bf16 ? go<true, false>(a, s) : go<false, false>(a, s);
 }
 
 int launch_gather(const GatherArgs& a, void* stream) {
