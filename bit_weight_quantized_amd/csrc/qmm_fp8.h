@@ -43,11 +43,15 @@ struct Fp8GemmArgs {
 // reduction axis, and 8·x8 activation rows a pass (the smallest of 1, 2, 4, 8 that
 // holds the rows, in several passes beyond 64).
 //
-// Dense: four waves; r the largest that still gives 160 workgroups, that is work
+// Dense: mostly four waves; r the largest that still gives 160 workgroups, that is work
 // for most of 256 CUs: a larger r reads the activations less often (64 x 13824 x
 // 5120: 20.6 us with r = 4, 27.3 with 2), a smaller one fills the chip (64 x 5120 x
 // 13824: 37.4, 29.2 and 44.0 us with r = 4, 2 and 1; 64 x 4096 x 7168: 21.2, 16.4,
 // 14.3).  Up to 16 rows r = 4 was never faster than 2.
+// Eight waves instead where even r = 1 leaves CUs without a workgroup and every wave
+// still has two blocks (1 x 3584 x 7168: 5.9 us, 7.1 with four; 81 x 525 x 11360: 8.4,
+// 11.6; 20 x 2304 x 7168: 6.2, 6.8, but 32 x 4000 x 4096: 5.7, 5.4; with r = 2 1 x 8000
+// x 8192: 14.0, 11.9), for 32 rows a pass at most, which is what their LDS holds.
 //
 // Grouped: 8 rows a pass and r = 2 (the tile kernel has the longer segments).  Two
 // waves, each with a longer run of blocks, but four where there may be fewer than 512
@@ -60,11 +64,13 @@ struct Fp8RowsShape {
 };
 inline Fp8RowsShape fp8_rows_shape(const Fp8GemmArgs& a) {
   if (a.n_seg > 0) return {2, 1, (int64_t(a.n) + 31) / 32 * std::min(a.n_seg, a.m_total) < 512 ? 4 : 2, 0};
-  const int x8 = a.t <= 8 ? 1 : a.t <= 16 ? 2 : a.t <= 32 ? 4 : 8;
+  int x8 = a.t <= 8 ? 1 : a.t <= 16 ? 2 : a.t <= 32 ? 4 : 8;
   auto workgroups = [&](int r) { return (int64_t(a.n) + 16 * r - 1) / (16 * r) * ((a.t + 8 * x8 - 1) / (8 * x8)); };
   int r = x8 <= 2 ? 2 : 4;
   while (r > 1 && workgroups(r) < 160) r /= 2;
-  return {r, x8, 4, workgroups(r)};
+  if (r > 1 || workgroups(1) > (x8 <= 2 ? 256 : 160) || a.d < 16 * kFp8Block) return {r, x8, 4, workgroups(r)};
+  x8 = std::min(x8, 4);
+  return {1, x8, 8, workgroups(1)};
 }
 // few rows: every weight read once for up to 64 rows
 int launch_fp8_rows(const Fp8GemmArgs& a, void* stream);

@@ -362,6 +362,11 @@ int go(const Fp8GemmArgs& a, hipStream_t s) {
   return int(hipGetLastError());
 }
 
+int dense8(int x8, const Fp8GemmArgs& a, hipStream_t s) {
+  if (x8 == 4) return go<8, 1, 4, false, false>(a, s);
+  return x8 == 1 ? go<8, 1, 1, false, false>(a, s) : go<8, 1, 2, false, false>(a, s);
+}
+
 template <int R>
 int dense(int x8, const Fp8GemmArgs& a, hipStream_t s) {
   if (x8 == 4) return go<4, R, 4, false, false>(a, s);
@@ -380,6 +385,7 @@ int grouped(const Fp8RowsShape& p, const Fp8GemmArgs& a, hipStream_t s) {
 int launch_fp8_rows(const Fp8GemmArgs& a, void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
   const Fp8RowsShape p = fp8_rows_shape(a);
+  if (a.n_seg == 0 && p.waves == 8) return dense8(p.x8, a, s);
   if (a.n_seg == 0) return p.r == 4 ? dense<4>(p.x8, a, s) : p.r == 2 ? dense<2>(p.x8, a, s) : dense<1>(p.x8, a, s);
   return a.glu ? grouped<true>(p, a, s) : grouped<false>(p, a, s);
 }

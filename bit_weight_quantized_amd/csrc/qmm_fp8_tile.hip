@@ -313,7 +313,7 @@ int launch_fp8_product(const Fp8GemmArgs& a, void* stream) {
   if (a.n_seg == 0) {
     // Estimates in us of the three kernels from nb steps and the rounds of workgroups
     // that 256 CUs take: a start and end, and a time for each step, which for the
-    // few-row kernel (four waves share the steps) depends on its weight blocks and on
+    // few-row kernel (its waves share the steps) depends on its weight blocks and on
     // rows that share their cache lines, and of which three 64 x 128 tiles a CU hide
     // a part from each other.  Measured few-row, 64 x 128, 256 x 256: 768 x 1903 x
     // 4240 29.6, 24.8, 51.2; 512 x 4096 x 4096 20.1, 23.8, 43.8; 1024 x 4096 x 4096
@@ -324,7 +324,7 @@ int launch_fp8_product(const Fp8GemmArgs& a, void* stream) {
     const Fp8RowsShape p = fp8_rows_shape(a);
     const int nb = fp8_blocks(a.d);
     const double step = (p.r == 4 ? 0.95 : p.r == 2 ? 0.8 : 0.6) * (a.d % kFp8Block ? 1.4 : 1.0);
-    const double few = rounds(p.workgroups) * (3 + (nb + 3) / 4 * step);
+    const double few = rounds(p.workgroups) * (3 + (nb + p.waves - 1) / p.waves * step);
     const double r64 = rounds(tiles(64, 128)), small = 3 + nb * std::max(0.65, 0.4 * r64) + 0.6 * r64;
     const double large = rounds(tiles(256, 256)) * (8 + 1.5 * nb);
     if (a.t <= kFp8RowsMax || (few <= small && few <= large)) return launch_fp8_rows(a, stream);
