@@ -12,8 +12,10 @@
 // row of 16 lanes has a token (four a wave), so that no step leaves the row's DPP:
 // lane i holds experts n·i .. n·i + n-1, n = ceil(experts / 16).  A round takes the
 // largest order-preserving integer key of the row, the lowest expert that has it (a
-// second reduction) and drops it.  More experts: a wave has a token, and scalar
-// instructions find the winner in the comparisons' masks.
+// second reduction) and drops it; 129 to 256 experts take a sort of each lane's 8
+// largest and merges across the row instead where there are 5 to 8 rounds.  More
+// experts: a wave has a token, and scalar instructions find the winner in the
+// comparisons' masks.
 // Bound by instructions: 16384 tokens x 256 experts in 8 groups, k = 8, are 2 us of
 // bytes; a sigmoid that rounds as the formula does is 35 instructions alone.
 //
@@ -37,6 +39,7 @@ namespace {
 
 constexpr int kTkWords = kTopkChunk / 32;        // bitmap words of an expert and pass
 constexpr int kTopkRowMaxK = 16;                 // lane r of a row holds the r-th choice
+constexpr int kTopkRounds = 4;                   // more rounds of 84 instructions cost more than the sort's 360
 static_assert(kRouteMaxExperts == 64 * kTopkWaves, "a thread of the workgroup owns an expert");
 
 // Order-preserving map to an unsigned key; 0 marks an expert that cannot be
@@ -234,6 +237,55 @@ __device__ __forceinline__ void load_row(const void* logits, int64_t at, int e0,
   }
 }
 
+// Sorting of keys that carry their expert: the 62 bits (key, 255 - code) as a positive
+// double, whose order is theirs (the exponent stays below that of infinity), since a
+// 64-bit maximum is one instruction on doubles.  In asm: fmax would quiet NaNs first.
+__device__ __forceinline__ double wide_key(uint32_t key, uint32_t code) {
+  return __hiloint2double(int(key >> 2), int(key << 30 | (255u - code)));
+}
+__device__ __forceinline__ double wide_max(double a, double b) {
+  double r;
+  asm("v_max_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+  return r;
+}
+__device__ __forceinline__ double wide_min(double a, double b) {
+  double r;
+  asm("v_min_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+  return r;
+}
+__device__ __forceinline__ void wide_order(double& a, double& b) {   // the larger first
+  const double hi = wide_max(a, b);
+  b = wide_min(a, b);
+  a = hi;
+}
+// 8 values that rise and then fall (or the reverse), largest first
+__device__ __forceinline__ void wide_merge(double* v) {
+#pragma unroll
+  for (int d = 4; d >= 1; d >>= 1)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (!(i & d)) wide_order(v[i], v[i + d]);
+}
+// 8 values, largest first: pairs, then merges of 2 and 4
+__device__ __forceinline__ void wide_sort(double* v) {
+  constexpr int pair[19][2] = {{0, 1}, {2, 3}, {4, 5}, {6, 7}, {0, 2}, {1, 3}, {4, 6}, {5, 7}, {1, 2}, {5, 6},
+                               {0, 4}, {1, 5}, {2, 6}, {3, 7}, {2, 4}, {3, 5}, {1, 2}, {3, 4}, {5, 6}};
+#pragma unroll
+  for (int i = 0; i < 19; ++i) wide_order(v[pair[i][0]], v[pair[i][1]]);
+}
+// the 8 largest of this lane's and another's, both sorted
+template <int CTRL>
+__device__ __forceinline__ void wide_join(double* v) {
+  double o[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    o[i] = __hiloint2double(__builtin_amdgcn_update_dpp(0, __double2hiint(v[i]), CTRL, 0xF, 0xF, false),
+                            __builtin_amdgcn_update_dpp(0, __double2loint(v[i]), CTRL, 0xF, 0xF, false));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = wide_max(v[i], o[7 - i]);
+  wide_merge(v);
+}
+
 // A row of 16 lanes a token, J experts a lane at most.
 template <int WAVES, int J, bool BF16, bool SIGMOID, bool ONE>
 __global__ __launch_bounds__(64 * WAVES) void topk_row_kernel(TopkArgs a, int chunk) {
@@ -361,7 +413,27 @@ __global__ __launch_bounds__(64 * WAVES) void topk_row_kernel(TopkArgs a, int ch
 
     // an expert's code, 16·lane + j, has the experts' order
     uint32_t mine = ~0u;
-    for (int r = 0; r < k; ++r) {
+    const bool sorted = J == 16 && k > kTopkRounds && k <= 8;
+    if (J == 16 && sorted) {
+      double v[J];
+#pragma unroll
+      for (int j = 0; j < J; ++j) v[j] = wide_key(key[j], uint32_t(16 * rl + j));
+      wide_sort(v);
+      wide_sort(v + J / 2);
+#pragma unroll
+      for (int i = 0; i < J / 2; ++i) v[i] = wide_max(v[i], v[J - 1 - i]);
+      wide_merge(v);
+      wide_join<0xB1>(v);
+      wide_join<0x4E>(v);
+      wide_join<0x141>(v);
+      wide_join<0x140>(v);
+      double pick = v[0];
+#pragma unroll
+      for (int i = 1; i < J / 2; ++i) pick = rl == i ? v[i] : pick;
+      const uint32_t lo = uint32_t(__double2loint(pick));
+      if (rl < k && (__double2hiint(pick) != 0 || lo >> 30 != 0)) mine = 255u - (lo & 255u);
+    }
+    for (int r = sorted ? k : 0; r < k; ++r) {
       uint32_t best = key[0];
 #pragma unroll
       for (int j = 1; j < J; ++j) best = umax(best, key[j]);
