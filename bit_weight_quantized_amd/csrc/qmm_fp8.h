@@ -99,14 +99,15 @@ struct TopkArgs {
   int32_t* slot_row;    // [t][k]
   int32_t* ws;          // counts [chunks][ne], or NULL for one chunk
 };
-// Tokens of one workgroup: 16 waves, up to 8 tokens each, and no more than 256
-// chunks, one for each CU (the second kernel adds every chunk's counts up itself).
+// Tokens of one workgroup: up to kTopkChunk in one (no workspace); else 16 or more,
+// up to kTopkMaxChunks chunks, one for each CU (the second kernel adds every chunk's
+// counts up itself).
 constexpr int kTopkWaves = 16;
 constexpr int kTopkChunk = 128;
 constexpr int64_t kTopkMaxChunks = 256;
-inline int64_t topk_chunk(int64_t t) {
+inline int64_t topk_chunk(int64_t t, int ne) {
   if (t <= kTopkChunk) return kTopkChunk;
-  int64_t c = 2 * kTopkWaves;
+  int64_t c = ne > 1 ? 16 : 32;   // a single expert's count takes a whole word
   while (c < kTopkChunk && (t + c - 1) / c > kTopkMaxChunks) c *= 2;
   if ((t + c - 1) / c > kTopkMaxChunks) c = round_up((t + kTopkMaxChunks - 1) / kTopkMaxChunks, kTopkChunk);
   return c;
@@ -116,7 +117,7 @@ inline int64_t topk_chunk(int64_t t) {
 __host__ __device__ constexpr bool topk_bytes(int64_t chunk) { return chunk <= kTopkChunk; }
 __host__ __device__ constexpr int topk_row(int ne) { return (ne + 3) / 4 * 4; }
 inline size_t topk_ws_bytes(int64_t t, int ne) {
-  const int64_t c = topk_chunk(t);
+  const int64_t c = topk_chunk(t, ne);
   return t <= c ? 0 : size_t((t + c - 1) / c) * (topk_bytes(c) ? size_t(topk_row(ne)) : size_t(ne) * 4);
 }
 int launch_topk(const TopkArgs& a, void* stream);

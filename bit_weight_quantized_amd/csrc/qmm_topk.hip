@@ -182,9 +182,10 @@ __device__ __forceinline__ void finish(const TopkArgs& a, TopkLds<WAVES>& lds, c
   const int tid = threadIdx.x;
   __syncthreads();                                // counts; the ids of the chunk
   if constexpr (!ONE) {
+    if (a.t <= kTopkChunk) return;                // counted from the ids
     if (topk_bytes(chunk)) {
-      if (tid < topk_row(a.ne))   // zeros at the end
-        reinterpret_cast<uint8_t*>(a.ws)[int64_t(blockIdx.x) * topk_row(a.ne) + tid] = uint8_t(lds.count[tid]);
+      for (int i = tid; i < topk_row(a.ne); i += 64 * WAVES)   // zeros at the end
+        reinterpret_cast<uint8_t*>(a.ws)[int64_t(blockIdx.x) * topk_row(a.ne) + i] = uint8_t(lds.count[i]);
     } else if (tid < a.ne) {
       a.ws[int64_t(blockIdx.x) * a.ne + tid] = lds.count[tid];
     }
@@ -643,7 +644,10 @@ __global__ __launch_bounds__(64 * kTopkWaves) void topk_place_kernel(
   lds.count[tid] = 0;
   lds.first[tid] = 0;
   __syncthreads();
-  if (topk_bytes(chunk)) {
+  if (!counts) {
+    for (int i = tid; i < int(t) * k; i += kThreads)
+      if (topk[i] >= 0) atomicAdd(&lds.count[topk[i]], 1);
+  } else if (topk_bytes(chunk)) {
     // four experts a thread, in sums of 16 bits (256 chunks of at most 128)
     const int words = (ne + 3) / 4, parts = kThreads / words;
     const int e = tid % words, part = tid / words;
@@ -707,45 +711,66 @@ __global__ __launch_bounds__(64 * kTopkWaves) void topk_place_kernel(
   place_rows(lds, topk + t0 * k, t0, min(t, t0 + chunk), k, row_index, slot_row);
 }
 
-// One kernel for one chunk, else the second one places the rows.
+// `one` (with its waves) for a single chunk.  Otherwise `more` for every chunk, and a
+// second kernel places the rows; up to kTopkChunk tokens it counts the ids itself.
 using TopkKernel = void (*)(TopkArgs, int);
-int go(const TopkArgs& a, int waves, TopkKernel one, TopkKernel more, hipStream_t s) {
-  const int64_t chunk = topk_chunk(a.t);
+struct TopkLaunch {
+  TopkKernel kernel;
+  int waves;
+};
+int go(const TopkArgs& a, TopkLaunch one, TopkLaunch more, int64_t chunk, hipStream_t s) {
   const unsigned chunks = a.t <= chunk ? 1u : unsigned((a.t + chunk - 1) / chunk);   // no tokens: the tables alone
   const ProfileEvents pe = take_profile_events();
   const hipEvent_t ev0 = static_cast<hipEvent_t>(pe.start), ev1 = static_cast<hipEvent_t>(pe.stop);
   if (chunks == 1) {
-    hipExtLaunchKernelGGL(one, dim3(1), dim3(64 * waves), 0, s, ev0, ev1, 0, a, int(chunk));
+    hipExtLaunchKernelGGL(one.kernel, dim3(1), dim3(64 * one.waves), 0, s, ev0, ev1, 0, a, int(chunk));
     return int(hipGetLastError());
   }
-  hipExtLaunchKernelGGL(more, dim3(chunks), dim3(64 * kTopkWaves), 0, s, ev0, nullptr, 0, a, int(chunk));
+  hipExtLaunchKernelGGL(more.kernel, dim3(chunks), dim3(64 * more.waves), 0, s, ev0, nullptr, 0, a, int(chunk));
   const int err = int(hipGetLastError());
   if (err) return err;
-  hipExtLaunchKernelGGL(topk_place_kernel, dim3(chunks), dim3(64 * kTopkWaves), 0, s, nullptr, ev1, 0,
-                        static_cast<const int32_t*>(a.topk), a.t, a.ne, a.k, int(chunk),
-                        static_cast<const int32_t*>(a.ws), a.seg_expert, a.seg_offsets, a.row_index, a.slot_row);
+  const bool count = a.t <= kTopkChunk;
+  hipExtLaunchKernelGGL(topk_place_kernel, dim3(count ? 1u : chunks), dim3(64 * kTopkWaves), 0, s, nullptr, ev1, 0,
+                        static_cast<const int32_t*>(a.topk), a.t, a.ne, a.k, int(count ? kTopkChunk : chunk),
+                        static_cast<const int32_t*>(count ? nullptr : a.ws), a.seg_expert, a.seg_offsets, a.row_index,
+                        a.slot_row);
   return int(hipGetLastError());
+}
+
+// J experts a lane of a row.  Chunks of 16 tokens take four waves (256 experts, 32
+// tokens: 11 us, 15 with sixteen), longer ones sixteen.
+template <int J, bool BF16, bool SIGMOID>
+int go_row(const TopkArgs& a, int64_t chunk, hipStream_t s) {
+  constexpr int W = kTopkWaves;
+  const TopkLaunch one = a.t <= 16 ? TopkLaunch{topk_row_kernel<4, J, BF16, SIGMOID, true>, 4}
+                                   : TopkLaunch{topk_row_kernel<W, J, BF16, SIGMOID, true>, W};
+  const TopkLaunch more = chunk <= 16 ? TopkLaunch{topk_row_kernel<4, J, BF16, SIGMOID, false>, 4}
+                                      : TopkLaunch{topk_row_kernel<W, J, BF16, SIGMOID, false>, W};
+  return go(a, one, more, chunk, s);
 }
 
 template <bool BF16, bool SIGMOID>
 int go(const TopkArgs& a, hipStream_t s) {
   constexpr int W = kTopkWaves;
+  int64_t chunk = topk_chunk(a.t, a.ne);
   if (a.ne <= 256 && a.k <= kTopkRowMaxK) {
-    // 16 tokens at once: fewer waves, shorter barriers
-    const bool few = a.t <= 16;
-    const int waves = few ? 4 : W;
-    if (a.ne <= 64)
-      return go(a, waves, few ? topk_row_kernel<4, 4, BF16, SIGMOID, true> : topk_row_kernel<W, 4, BF16, SIGMOID, true>,
-                topk_row_kernel<W, 4, BF16, SIGMOID, false>, s);
-    if (a.ne <= 128)
-      return go(a, waves, few ? topk_row_kernel<4, 8, BF16, SIGMOID, true> : topk_row_kernel<W, 8, BF16, SIGMOID, true>,
-                topk_row_kernel<W, 8, BF16, SIGMOID, false>, s);
-    return go(a, waves, few ? topk_row_kernel<4, 16, BF16, SIGMOID, true> : topk_row_kernel<W, 16, BF16, SIGMOID, true>,
-              topk_row_kernel<W, 16, BF16, SIGMOID, false>, s);
+    // Few tokens of many experts: a wave each (256 experts, 1 token: 5.8 us, 7.6 with
+    // rows; 8 tokens: 8.9, 7.7).
+    if (a.ne > 128 && a.t <= 4) {
+      const TopkLaunch wave{topk_kernel<4, 4, BF16, SIGMOID, true>, 4};
+      return go(a, wave, wave, chunk, s);
+    }
+    // One workgroup for up to 128 tokens, or more of them and a second launch where
+    // its passes take longer than that (256 experts, 32 tokens: 15.1 us in one, 10.6 in
+    // two, 128 tokens 26.9 and 11.1; 60 experts, 128 tokens: 9.6, 9.5).
+    if (a.t <= kTopkChunk && a.t * a.ne >= 8192) chunk = 16;
+    if (a.ne <= 64) return go_row<4, BF16, SIGMOID>(a, chunk, s);
+    if (a.ne <= 128) return go_row<8, BF16, SIGMOID>(a, chunk, s);
+    return go_row<16, BF16, SIGMOID>(a, chunk, s);
   }
   if (a.ne <= 512)
-    return go(a, W, topk_kernel<W, 8, BF16, SIGMOID, true>, topk_kernel<W, 8, BF16, SIGMOID, false>, s);
-  return go(a, W, topk_kernel<W, 16, BF16, SIGMOID, true>, topk_kernel<W, 16, BF16, SIGMOID, false>, s);
+    return go(a, {topk_kernel<W, 8, BF16, SIGMOID, true>, W}, {topk_kernel<W, 8, BF16, SIGMOID, false>, W}, chunk, s);
+  return go(a, {topk_kernel<W, 16, BF16, SIGMOID, true>, W}, {topk_kernel<W, 16, BF16, SIGMOID, false>, W}, chunk, s);
 }
 
 // Weighted sum of the chosen experts' rows, one workgroup per token and 2048

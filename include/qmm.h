@@ -433,7 +433,7 @@ size_t qmm_route_topk_workspace_bytes(int64_t t, int32_t n_experts);
  *   slot_row int32[t][k]: the grouped row of each slot, -1 in slots of -1
  *   ws      qmm_route_topk_workspace_bytes(t, n_experts) bytes, 4-byte aligned
  * Limits: t·k < 2^30; n_experts <= 1024; k <= min(64, n_experts); n_groups <= 64,
- * dividing n_experts.  One launch up to 128 tokens, else two. */
+ * dividing n_experts.  One launch, or two (always beyond 128 tokens). */
 qmm_status qmm_route_topk(const void* logits, qmm_dtype dtype, int64_t t, int32_t n_experts, int64_t ld,
                           qmm_score score, const float* bias, int32_t n_groups, int32_t keep_groups,
                           qmm_group_score group_score, int32_t k, int32_t renorm, float scale, int32_t* topk,
