@@ -19,6 +19,10 @@
 // largest and cuts what lies 13 binary places below it (measured).  Few rows
 // feed the next layer's rounding directly and have the time; with more rows the
 // conversions would cost more than the reads.
+//
+// Measured: 1 x 13824 x 5120 12.6 us (5.6 TB/s), 37 x 5120 x 13824 16.5 us (4.3), 8
+// experts of 128, 4 tokens, 4096 x 3584 60 us (6.4; all with a part of the weights in
+// the Infinity Cache).
 #include <hip/hip_runtime.h>
 
 #include "qmm_fp8.h"

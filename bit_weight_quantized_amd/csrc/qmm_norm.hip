@@ -9,7 +9,8 @@
 // r are read once and v and h are written once: bound by memory for many rows,
 // by the two sums over the row for a few.  Everything between the loads and the
 // stores is fp32; h is made from v before v is rounded for the store, and the
-// e4m3 codes from h before h is rounded.
+// e4m3 codes from h before h is rounded.  8192 x 5120 with gate and both outputs: 77 to
+// 80 us (74 us for its bytes at the rate of a copy); 1 x 5120: 4.5 us.
 #include <hip/hip_runtime.h>
 
 #include "qmm_fp8.h"
