@@ -299,7 +299,7 @@ int go(const Fp8GemmArgs& a, hipStream_t s) {
   const int64_t tiles_t = GROUPED ? int64_t(a.m_total) / T::kT + std::min(a.n_seg, a.m_total)
                                   : (a.t + T::kT - 1) / T::kT;
   if (tiles_t == 0) return 0;
-  if (tiles_n * tiles_t >= (int64_t(1) << 22)) return int(hipErrorInvalidValue);
+  if (tiles_n * tiles_t * 64 * T::kWaves >= (int64_t(1) << 32)) return int(hipErrorInvalidValue);   // the grid's limit
   const Fp8TileArgs k{a.w, a.ws, a.n, a.d, fp8_blocks(a.d), a.x, a.xs, a.t, a.y, a.ldy, int(tiles_n), a.row_index,
                       a.seg_expert, a.seg_offsets, a.n_experts, a.n_seg, a.m_total, int(a.t_x)};
   launch_kernel_lds(kernel, dim3(unsigned(tiles_n * tiles_t)), dim3(64 * T::kWaves), bytes, s, k);

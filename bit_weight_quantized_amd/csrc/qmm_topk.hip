@@ -755,6 +755,11 @@ template <bool BF16, bool SIGMOID>
 int go(const TopkArgs& a, hipStream_t s) {
   constexpr int W = kTopkWaves;
   int64_t chunk = topk_chunk(a.t, a.ne);
+  // One workgroup for up to 128 tokens, or more of them and a second launch where
+  // its passes take longer than that (256 experts, 32 tokens: 15.1 us in one, 10.6 in
+  // two, 128 tokens 26.9 and 11.1; 896 experts, 75 tokens 64 and 15; 60 experts, 128
+  // tokens 9.6 and 9.5).
+  if (a.t <= kTopkChunk && a.t * a.ne >= 8192) chunk = 16;
   if (a.ne <= 256 && a.k <= kTopkRowMaxK) {
     // Few tokens of many experts: a wave each (256 experts, 1 token: 5.8 us, 7.6 with
     // rows; 8 tokens: 8.9, 7.7).
@@ -762,10 +767,6 @@ int go(const TopkArgs& a, hipStream_t s) {
       const TopkLaunch wave{topk_kernel<4, 4, BF16, SIGMOID, true>, 4};
       return go(a, wave, wave, chunk, s);
     }
-    // One workgroup for up to 128 tokens, or more of them and a second launch where
-    // its passes take longer than that (256 experts, 32 tokens: 15.1 us in one, 10.6 in
-    // two, 128 tokens 26.9 and 11.1; 60 experts, 128 tokens: 9.6, 9.5).
-    if (a.t <= kTopkChunk && a.t * a.ne >= 8192) chunk = 16;
     if (a.ne <= 64) return go_row<4, BF16, SIGMOID>(a, chunk, s);
     if (a.ne <= 128) return go_row<8, BF16, SIGMOID>(a, chunk, s);
     return go_row<16, BF16, SIGMOID>(a, chunk, s);
