@@ -9,8 +9,9 @@
 // r are read once and v and h are written once: bound by memory for many rows,
 // by the two sums over the row for a few.  Everything between the loads and the
 // stores is fp32; h is made from v before v is rounded for the store, and the
-// e4m3 codes from h before h is rounded.  8192 x 5120 with gate and both outputs: 77 to
-// 80 us (74 us for its bytes at the rate of a copy); 1 x 5120: 4.5 us.
+// e4m3 codes from h before h is rounded.  8192 x 5120 with gate and both outputs: 76.7 us
+// (74 us for its bytes at the rate of a copy); 1 x 5120: 4.5 us.  At most 128 registers,
+// for four waves on a SIMD (1000 x 13824: 26.7 us, 32.9 with the 130 of three waves).
 #include <hip/hip_runtime.h>
 
 #include "qmm_fp8.h"
@@ -38,7 +39,7 @@ __device__ __forceinline__ u32x4_t narrow(const F8& v) {
   u32x4_t r;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    r[i] = uint32_t(f32_to_bf16(v.f[2 * i])) | uint32_t(f32_to_bf16(v.f[2 * i + 1])) << 16;
+    r[i] = pack_bf16x2(v.f[2 * i], v.f[2 * i + 1]);
   return r;
 }
 
@@ -74,7 +75,7 @@ __device__ __forceinline__ float block_sum(float v, float* lds) {
 // load of the row is issued before the first sum, so a row waits for memory once
 // (beyond, the registers do not hold them).
 template <int WAVES, int V, bool RF32>
-__global__ __launch_bounds__(64 * WAVES) void norm_kernel(NormArgs a) {
+__global__ __launch_bounds__(64 * WAVES, 4) void norm_kernel(NormArgs a) {
   __shared__ float sums[2][WAVES];
   constexpr bool kEarly = WAVES * V <= 32;
   const int64_t row = blockIdx.x;
@@ -198,7 +199,7 @@ int launch_norm_residual(const NormArgs& a, void* stream) {
   // Waves by width: eight, with as few groups a lane as hold the row (8192 rows of
   // 7168: 104.6 us, 111.4 with four waves, 114.7 with sixteen), but four where
   // eight would leave half the lanes without work (8192 of 5120: 79.4, 83.7 with
-  // eight, 91.4 with sixteen), and sixteen for few rows, which wait for memory once
+  // eight, 91.4 with sixteen, all with conversions to bf16 in software), and sixteen for few rows, which wait for memory once
   // whatever they hold (64 of 5120: 4.8 us, 6.1 with four).
   const int n8 = a.d / 8;
   if (n8 <= 64) return go<1, 1>(a, s);

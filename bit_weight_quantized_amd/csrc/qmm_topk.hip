@@ -819,8 +819,7 @@ __global__ __launch_bounds__(256) void gather_kernel(GatherArgs a) {
   u32x4_t o;
 #pragma unroll
   for (int q = 0; q < 4; ++q)
-    o[q] = bad ? 0x7FC07FC0u
-               : uint32_t(f32_to_bf16(acc[2 * q])) | uint32_t(f32_to_bf16(acc[2 * q + 1])) << 16;
+    o[q] = bad ? 0x7FC07FC0u : pack_bf16x2(acc[2 * q], acc[2 * q + 1]);
   *reinterpret_cast<u32x4_t*>(a.out + tok * a.d + 8 * c8) = o;
 }
 
