@@ -146,8 +146,8 @@ __global__ __launch_bounds__(64 * WT * WN) void fp8_tile_kernel(Fp8TileArgs A) {
   };
 
   // ---- operands
-  const float* ws0 = P.ws + int64_t((n0 + (GLU ? 8 : 16) * WS * wn) / kFp8Block) * nb;
-  const float* ws1 = P.ws + int64_t(P.sb + (n0 + 8 * WS * wn) / kFp8Block) * nb;
+  const float* ws0 = P.ws + int64_t(fp8_scale_row(n0 + (GLU ? 8 : 16) * WS * wn, nout)) * nb;
+  const float* ws1 = P.ws + int64_t(P.sb + fp8_scale_row(n0 + 8 * WS * wn, nout)) * nb;
   const int o0 = 16 * (g ^ (col & 7));
   f32x4_t acc[TS][WS];
 #pragma unroll
