@@ -15,7 +15,7 @@ inline int fp8_blocks(int64_t d) { return int((d + kFp8Block - 1) / kFp8Block); 
 // Scale row of a weight row (of one half with the activation): rows past the matrix,
 // which the last tile of a matrix has, take the last one, since ceil(n / 128) is all
 // there are.
-__host__ __device__ constexpr int fp8_scale_row(int row, int n) { return row / kFp8Block; }
+__host__ __device__ constexpr int fp8_scale_row(int row, int n) { return (row < n ? row : n - 1) / kFp8Block; }
 
 struct Fp8QuantArgs {
   const uint16_t* x;   // [t][ldx] bf16
