@@ -17,6 +17,24 @@ inline int fp8_blocks(int64_t d) { return int((d + kFp8Block - 1) / kFp8Block); 
 // there are.
 __host__ __device__ constexpr int fp8_scale_row(int row, int n) { return (row < n ? row : n - 1) / kFp8Block; }
 
+// Offsets of the buffer -> LDS copies.  Only the lane's offset is taken to be held
+// against the buffer's size, never the scalar one, and nothing is taken from how the
+// machine forms their sum: a copy that may not read everything behind its lane offset
+// has all of its offset there, and one from an empty buffer no scalar offset.
+constexpr uint32_t kOOB8 = 0x80000000u;   // past every range: reads zero
+// activation scales of block b and the three after it, of the row at `row` (or kOOB8)
+__host__ __device__ constexpr uint32_t fp8_scales_at(uint32_t row, int b) {
+  return (row + 4u * uint32_t(b)) | (row & kOOB8);
+}
+// scalar offset of block b's codes; past the share that ends at b_end the buffer is empty
+__host__ __device__ constexpr uint32_t fp8_block_at(int b, int b_end) {
+  return b < b_end ? uint32_t(kFp8Block) * uint32_t(b) : 0u;
+}
+// set in the lane offset of the 16 codes `chunk` bytes into block b where d ends before
+__host__ __device__ constexpr uint32_t fp8_past(int chunk, int b, int d) {
+  return kFp8Block * b + chunk < d ? 0u : kOOB8;
+}
+
 struct Fp8QuantArgs {
   const uint16_t* x;   // [t][ldx] bf16
   int64_t t, ldx;

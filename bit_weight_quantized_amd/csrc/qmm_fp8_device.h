@@ -8,8 +8,6 @@ namespace qmm {
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 
-constexpr uint32_t kOOB8 = 0x80000000u;   // buffer offset past every range: reads zero
-
 // Smallest block maximum a scale is made from: keeps m / 448 and 448 / m
 // normal fp32 numbers, and gives a block of zeros a scale like any other.
 constexpr float kFp8Floor = 0x1p-96f;

@@ -190,18 +190,17 @@ __global__ __launch_bounds__(64 * WAVES, 2) void fp8_rows_kernel(
         const int src = 64 * i + lane < kRows ? source(64 * i + lane) : -1;
         soff[i] = src >= 0 ? uint32_t(src) * uint32_t(nb) * 4u : kOOB8;
       }
-      // Copy `i` of block b into a stage.  The block's place in a row is the scalar
-      // offset, so the lanes' offsets stay as they are; past the wave's share the
-      // buffers are empty (zeros, no reads, the same count of copies), and in a short
-      // last block the chunks past d are out of range.
+      // Copy `i` of block b into a stage.  A code's block is the scalar offset, so the
+      // lanes' offsets stay as they are; past the wave's share the buffers are empty
+      // (zeros, no reads, the same count of copies), and in a short last block the
+      // chunks past d are out of range.
       struct Cursor {
         bool in;
         uint32_t at, k, past;
         uint32_t chunk;   // where the scales of its four blocks are
       };
       auto cursor = [&](int b, int stage) {
-        return Cursor{b < b_end, ring_at + uint32_t(stage * T::kStage), uint32_t(kFp8Block * b),
-                      kFp8Block * b + cchunk < d ? 0u : kOOB8,
+        return Cursor{b < b_end, ring_at + uint32_t(stage * T::kStage), fp8_block_at(b, b_end), fp8_past(cchunk, b, d),
                       uint32_t(D * T::kStage + ((b - b_begin) >> 2) % T::kChunks * T::kChunk)};
       };
       auto copy = [&](const Cursor& c, int i) {
@@ -213,12 +212,13 @@ __global__ __launch_bounds__(64 * WAVES, 2) void fp8_rows_kernel(
                              c.at + T::kX + 1024u * (i - 2 * R));
       };
       // The scales of four blocks at once, before the first of them (rows lie far
-      // apart: a copy costs a cache line for each row, whatever it takes of it).
-      auto copy_scales = [&](const Cursor& c) {
+      // apart: a copy costs a cache line for each row, whatever it takes of it).  The
+      // last row may have fewer left: what is past the buffer reads zero.
+      auto copy_scales = [&](const Cursor& c, int b) {
 #pragma unroll
         for (int i = 0; i < T::kSc; ++i)
-          copy16_to_lds_from(make_rsrc(sp, c.in ? x_rows * uint32_t(nb) * 4u : 0u), soff[i], c.k / 32u,
-                             ring_at + c.chunk + 1024u * i);
+          copy16_to_lds(make_rsrc(sp, c.in ? x_rows * uint32_t(nb) * 4u : 0u), fp8_scales_at(soff[i], b),
+                        ring_at + c.chunk + 1024u * i);
       };
 
       f32x4_t acc[R][C];
@@ -230,7 +230,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void fp8_rows_kernel(
 #pragma unroll
       for (int i = 0; i < D; ++i) {
         const Cursor c = cursor(b_begin + i, i);
-        if (i == 0) copy_scales(c);
+        if (i == 0) copy_scales(c, b_begin);
 #pragma unroll
         for (int k = 0; k < T::kOps; ++k) copy(c, k);
       }
@@ -263,7 +263,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void fp8_rows_kernel(
         wait_reads();                       // ... and is in registers: its stage is free
         const Cursor nx = cursor(b + D, stage);
         stage = stage + 1 == D ? 0 : stage + 1;
-        if (((b + D - b_begin) & 3) == 0) copy_scales(nx);
+        if (((b + D - b_begin) & 3) == 0) copy_scales(nx, b + D);
         if constexpr (T::kExact) {
 #pragma unroll
           for (int k = 0; k < T::kOps; ++k) copy(nx, k);

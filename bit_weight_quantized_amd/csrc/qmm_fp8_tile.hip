@@ -141,7 +141,7 @@ __global__ __launch_bounds__(64 * WT * WN) void fp8_tile_kernel(Fp8TileArgs A) {
   // costs a cache line for each row, whatever it takes of it)
   auto copy_scales = [&](int b) {
     if ((b & 3) == 0 && wave < T::kT / 64)
-      copy16_to_lds(src.s, (soff + 4u * uint32_t(b)) | (soff & kOOB8),
+      copy16_to_lds(src.s, fp8_scales_at(soff, b),
                     base + 2u * T::kStage + uint32_t(b >> 2 & 1) * T::kScales + 1024u * uint32_t(wave));
   };
 

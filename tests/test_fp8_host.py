@@ -30,3 +30,7 @@ def driver(tmp_path_factory):
 
 def test_no_wave_reads_past_the_weight_scales(driver):
     driver("scale_rows")
+
+
+def test_few_row_copies_stay_inside_their_buffers(driver):
+    driver("rows_copies")
