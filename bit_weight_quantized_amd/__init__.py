@@ -131,8 +131,10 @@ def load():
 def _ptr(v):
     try:
         return v.data_ptr()
-    except AttributeError:   # None or an address
-        return v
+    except AttributeError:
+        if v is None or isinstance(v, int):   # an address
+            return v
+        raise   # ctypes would pass bytes and str on as addresses of host memory
 
 
 def _nbytes(v):
