@@ -155,7 +155,10 @@ def _stream(s):
             import torch
             if not torch.cuda.is_available():
                 return None
-            _raw_stream = (torch._C._cuda_getCurrentRawStream, torch.cuda.current_device)
+            # the handle without a Stream object around it, where this torch has that
+            handle = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+            _raw_stream = (handle or (lambda device: torch.cuda.current_stream(device).cuda_stream),
+                           torch.cuda.current_device)
         handle, device = _raw_stream
         return handle(device())
     if isinstance(s, int):

@@ -30,3 +30,19 @@ def test_only_tensors_addresses_and_none_are_pointers(wrong):
                                                0.0, 1e-6, P, 64, None, None, stream=0)):
         with pytest.raises(AttributeError):
             call()
+
+
+def test_current_stream_without_the_private_lookup(monkeypatch):
+    """A torch without its private function for the raw handle: the public one serves."""
+    torch = pytest.importorskip("torch")
+
+    class Stream:
+        cuda_stream = 77
+
+    monkeypatch.setattr(qmm, "_raw_stream", None)
+    monkeypatch.setattr(torch.cuda, "is_available", lambda: True)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Stream() if device == 3 else None)
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    assert qmm._stream(None) == 77
+    assert qmm._stream(0) == 0 and qmm._stream(Stream()) == 77
