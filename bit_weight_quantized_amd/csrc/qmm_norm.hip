@@ -75,10 +75,10 @@ __device__ __forceinline__ float block_sum(float v, float* lds) {
 // load of the row is issued before the first sum, so a row waits for memory once
 // (beyond, the registers do not hold them).
 template <int WAVES, int V, bool RF32>
-__global__ __launch_bounds__(64 * WAVES, 4) void norm_kernel(NormArgs a) {
+__global__ __launch_bounds__(64 * WAVES, 4) void norm_kernel(NormArgs a, int64_t first) {
   __shared__ float sums[2][WAVES];
   constexpr bool kEarly = WAVES * V <= 32;
-  const int64_t row = blockIdx.x;
+  const int64_t row = first + blockIdx.x;
   const int n8 = a.d >> 3;
   const float inv_d = 1.0f / float(a.d);
   const u32x4_t zero = {0, 0, 0, 0};
@@ -185,11 +185,7 @@ __global__ __launch_bounds__(64 * WAVES, 4) void norm_kernel(NormArgs a) {
 
 template <int WAVES, int V>
 int go(const NormArgs& a, hipStream_t s) {
-  if (a.r_f32)
-    launch_kernel(norm_kernel<WAVES, V, true>, dim3(unsigned(a.t)), dim3(64 * WAVES), s, a);
-  else
-    launch_kernel(norm_kernel<WAVES, V, false>, dim3(unsigned(a.t)), dim3(64 * WAVES), s, a);
-  return int(hipGetLastError());
+  return launch_rows(a.r_f32 ? norm_kernel<WAVES, V, true> : norm_kernel<WAVES, V, false>, a, a.t, 1, 64 * WAVES, s);
 }
 
 }  // namespace

@@ -781,8 +781,8 @@ int go(const TopkArgs& a, hipStream_t s) {
 // rounded once.  Bound by the reads of o; the rows are known before the first
 // load, so all of a token's loads are in flight together (8 slots at a time).  4096
 // tokens, 8 slots of 3584: 44 us (6.0 TB/s).
-__global__ __launch_bounds__(256) void gather_kernel(GatherArgs a) {
-  const int64_t tok = blockIdx.x;
+__global__ __launch_bounds__(256) void gather_kernel(GatherArgs a, int64_t first) {
+  const int64_t tok = first + blockIdx.x;
   const int c8 = blockIdx.y * 256 + threadIdx.x;
   if (c8 >= a.d / 8) return;
   const int32_t* rows = a.slot_row + tok * a.k;
@@ -832,9 +832,7 @@ int launch_topk(const TopkArgs& a, void* stream) {
 }
 
 int launch_gather(const GatherArgs& a, void* stream) {
-  launch_kernel(gather_kernel, dim3(unsigned(a.t), unsigned((a.d / 8 + 255) / 256)), dim3(256),
-                static_cast<hipStream_t>(stream), a);
-  return int(hipGetLastError());
+  return launch_rows(gather_kernel, a, a.t, unsigned((a.d / 8 + 255) / 256), 256, static_cast<hipStream_t>(stream));
 }
 
 }  // namespace qmm

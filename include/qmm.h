@@ -432,7 +432,7 @@ size_t qmm_route_topk_workspace_bytes(int64_t t, int32_t n_experts);
  *           ascending, and row_index is -1 past seg_offsets[n_experts]
  *   slot_row int32[t][k]: the grouped row of each slot, -1 in slots of -1
  *   ws      qmm_route_topk_workspace_bytes(t, n_experts) bytes, 4-byte aligned
- * Limits: t·k < 2^30; n_experts <= 1024; k <= min(64, n_experts); n_groups <= 64,
+ * Limits: t <= 2^24, t·k < 2^30; n_experts <= 1024; k <= min(64, n_experts); n_groups <= 64,
  * dividing n_experts.  One launch, or two (always beyond 128 tokens). */
 qmm_status qmm_route_topk(const void* logits, qmm_dtype dtype, int64_t t, int32_t n_experts, int64_t ld,
                           qmm_score score, const float* bias, int32_t n_groups, int32_t keep_groups,
@@ -446,7 +446,7 @@ qmm_status qmm_route_topk(const void* logits, qmm_dtype dtype, int64_t t, int32_
  *   o bf16[m_total][d]; slot_row int32[t][k], weights fp32[t][k] (qmm_route_topk);
  *   shared bf16[t][d] or NULL; out bf16[t][d] (may be shared).  A slot below 0 adds
  *   nothing; one at m_total or above makes the token NaN.
- * Limits: k <= 64, d a multiple of 8 in [8, 65536], t·k < 2^30; o, shared and out
+ * Limits: t <= 2^24, k <= 64, d a multiple of 8 in [8, 65536], t·k < 2^30; o, shared and out
  * 16-byte aligned. */
 qmm_status qmm_moe_gather(const qmm_bf16* o, int32_t m_total, int64_t d, int64_t t, int32_t k, const int32_t* slot_row,
                           const float* weights, const qmm_bf16* shared, qmm_bf16* out, void* stream);
