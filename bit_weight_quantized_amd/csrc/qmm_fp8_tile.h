@@ -42,6 +42,7 @@ struct Fp8Place {
   int64_t m0, m_end;
   int n0;
   bool bad_expert;
+  bool starts;            // the first rows of its segment
   const uint8_t* w;
   const float* ws;
   int sb;                 // scale rows of the gate half
@@ -73,16 +74,18 @@ struct Fp8Tiles {
     all = __builtin_amdgcn_readlane(incl, 63);
   }
 
-  // The tt-th tile, if it is one of these: its segment's number from s0, rows [lo, hi).
-  __device__ __forceinline__ int find(int tt, int& lo, int& hi) const {
+  // The tt-th tile, if it is one of these: its segment's number from s0, rows [lo, hi),
+  // and whether they are the segment's first.
+  __device__ __forceinline__ int find(int tt, int& lo, int& hi, bool& starts) const {
     const uint64_t who = __ballot(tt >= first && tt < first + sum);
     if (!who) return -1;
-    int s = -1, b = 0, e = 0, f = first;
+    int s = -1, b = 0, e = 0, f = first, nth = 0;
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       if (s < 0 && tt >= f && tt < f + tiles[u]) {
         s = 4 * int(threadIdx.x & 63) + u;
-        b = at[u] + (tt - f) * kT;
+        nth = tt - f;
+        b = at[u] + nth * kT;
         e = min(b + kT, at[u + 1]);
       }
       f += tiles[u];
@@ -90,6 +93,7 @@ struct Fp8Tiles {
     const int src = __builtin_ctzll(who);
     lo = __builtin_amdgcn_readlane(b, src);
     hi = __builtin_amdgcn_readlane(e, src);
+    starts = __builtin_amdgcn_readlane(nth, src) == 0;
     return __builtin_amdgcn_readlane(s, src);
   }
 };
@@ -125,6 +129,7 @@ __device__ __forceinline__ bool fp8_place(const Fp8TileArgs& a, Fp8Place& p) {
   const int tn = 8 * strip + in_strip - tt * width;
   p.n0 = tn * kOut;
   p.bad_expert = false;
+  p.starts = false;
   p.w = a.w;
   p.ws = a.ws;
   p.sb = GLU ? (nout + kFp8Block - 1) / kFp8Block : 0;
@@ -136,7 +141,7 @@ __device__ __forceinline__ bool fp8_place(const Fp8TileArgs& a, Fp8Place& p) {
   for (int s0 = 0; s0 < a.n_seg; s0 += 256) {
     if (a.n_seg > 256) some.scan(a, s0);
     int lo, hi;
-    const int s = some.find(tt, lo, hi);
+    const int s = some.find(tt, lo, hi, p.starts);
     if (s >= 0) {
       p.m0 = lo;
       p.m_end = hi;

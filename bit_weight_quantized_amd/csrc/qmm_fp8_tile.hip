@@ -178,9 +178,9 @@ __global__ __launch_bounds__(64 * WT * WN) void fp8_tile_kernel(Fp8TileArgs A) {
   // block sums and their multiply-adds, kAhead matrix instructions apart: the
   // order is fixed, since the scheduler would start all the block sums first and
   // keep them in registers that the accumulators need
-  auto multiply = [&](auto half, auto blocks, float w0, float w1) {
+  auto multiply = [&](auto half, auto blocks, auto exact, float w0, float w1) {
     constexpr int h = decltype(half)::value, kAhead = 4, N = decltype(blocks)::value * WS;
-    constexpr bool kExact = GROUPED && decltype(blocks)::value * WT == 1;   // 16 rows at most
+    constexpr bool kExact = decltype(exact)::value;
     f32x4_t p[kAhead + 1];
 #pragma unroll
     for (int m = 0; m < (N ? N + kAhead : 0); ++m) {
@@ -208,7 +208,7 @@ __global__ __launch_bounds__(64 * WT * WN) void fp8_tile_kernel(Fp8TileArgs A) {
   phase_end();
   if (behind) phase_end();
   // The steps, with `first` and `second` live activation blocks of a half.
-  auto steps = [&](auto first, auto second) {
+  auto steps = [&](auto first, auto second, auto exact) {
     float w0 = scalar_load(ws0, 0), w1 = GLU ? scalar_load(ws1, 0) : 0.f;
     for (int b = 0; b < nb; ++b) {
       st = lds + (b & 1) * T::kStage;
@@ -225,7 +225,7 @@ __global__ __launch_bounds__(64 * WT * WN) void fp8_tile_kernel(Fp8TileArgs A) {
       if (b % 4 == 3 && wave < T::kT / 64) wait_copies<T::kAfter + 1>();
       else wait_copies<T::kAfter>();
       phase_end();
-      multiply(std::integral_constant<int, 0>{}, first, w0, w1);
+      multiply(std::integral_constant<int, 0>{}, first, exact, w0, w1);
       phase_end();
       __builtin_amdgcn_s_setprio(1);
       read_x(std::integral_constant<int, 1>{}, second);
@@ -238,7 +238,7 @@ __global__ __launch_bounds__(64 * WT * WN) void fp8_tile_kernel(Fp8TileArgs A) {
       if (b % 4 == 2 && wave < T::kT / 64) wait_copies<T::kAfter + 1>();
       else wait_copies<T::kAfter>();
       phase_end();
-      multiply(std::integral_constant<int, 1>{}, second, w0, w1);
+      multiply(std::integral_constant<int, 1>{}, second, exact, w0, w1);
       phase_end();
       w0 = w0n;
       w1 = w1n;
@@ -246,14 +246,20 @@ __global__ __launch_bounds__(64 * WT * WN) void fp8_tile_kernel(Fp8TileArgs A) {
   };
   // A tile with few live rows leaves out the block sums of dead ones, a quarter of
   // the tile at a time: the waves' blocks alternate, so all waves have less to do.
+  // Segments of up to 16 rows have block sums in fp32, the last rows of a longer one
+  // have them as its other rows do: a row's result depends on the rows that its
+  // segment has, not on its place among them.
   const int rows = int(P.m_end - P.m0);
   using None = std::integral_constant<int, 0>;
   using Part = std::integral_constant<int, H / 2>;
   using Whole = std::integral_constant<int, H>;
-  if (rows > T::kT / 4 * 3) steps(Whole{}, Whole{});
-  else if (rows > T::kT / 2) steps(Whole{}, Part{});
-  else if (rows > T::kT / 4) steps(Whole{}, None{});
-  else steps(Part{}, None{});
+  constexpr bool kShort = GROUPED && T::kT == 64;       // a quarter is 16 rows
+  const std::false_type fast{};
+  if (rows > T::kT / 4 * 3) steps(Whole{}, Whole{}, fast);
+  else if (rows > T::kT / 2) steps(Whole{}, Part{}, fast);
+  else if (rows > T::kT / 4) steps(Whole{}, None{}, fast);
+  else if (kShort && P.starts) steps(Part{}, None{}, std::integral_constant<bool, kShort>{});
+  else steps(Part{}, None{}, fast);
   if (!behind) phase_end();                             // the groups' barrier counts match
   wait_copies<0>();
   phase_end();
