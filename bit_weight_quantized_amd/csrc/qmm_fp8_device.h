@@ -53,9 +53,11 @@ __device__ __forceinline__ float scalar_load(const float* p, int i) {
 
 __device__ __forceinline__ float silu(float v) { return v / (1.0f + expf(-v)); }
 
-// The same from the hardware's exponential and reciprocal (a few 2^-23 of its
-// value, less than the sums it is taken of), for tiles of many values: the
-// precise form is 35 instructions a value.
+// The same from the hardware's exponential and reciprocal, for tiles of many values:
+// the precise form is 35 instructions a value.  The product with log2(e) is rounded
+// before the exponential, so e^-v is off by 1.22·|v|·2^-24 of its value and what
+// follows by a few 2^-24 more: 2^-18 of silu at v = -40, 2^-9 of what the rounding to
+// bf16 takes.  Below v = -87, where silu is under 2^-119, either form may give zero.
 __device__ __forceinline__ float quick_silu(float v) {
   return v * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * -1.44269504f));
 }

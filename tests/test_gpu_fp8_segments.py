@@ -56,3 +56,27 @@ def test_short_segments_have_sums_in_fp32(length):
     mag = np.abs(fp8.dequant_rows(x[src], xs[src])) @ np.abs(fp8.dequant_matrix(w, ws)).T
     rest = (128 + 2 + fp8.blocks(d) + 16) * 2.0 ** -23 * mag
     assert np.all(np.abs(y - ref) <= fp8.gemm_tolerance(ref, rest))
+
+
+# segments of one row take the few-row kernel, one of 4096 rows 64 x 128 tiles, and of
+# 32768 rows 256 x 256 tiles
+@pytest.mark.parametrize("segments_,repeat", [(4096, 1), (1, 1), (1, 8)])
+def test_activation_over_its_whole_range(segments_, repeat):
+    """silu(g)·g for g from -110 to 110: gate and up are the rows' scales exactly.
+    Off by e^-g's (1.22·|g| + 3)·2^-24 at most, a sum, a reciprocal and two products of
+    a few 2^-24, and the rounding to bf16; below 2^-126 the exponential may be zero."""
+    say("silu", segments_, repeat)
+    g = np.linspace(-110.0, 110.0, 4096).astype(np.float32)
+    m, d, nh = 4096 * repeat, 16, 16
+    x, w = np.zeros((4096, d), np.uint8), np.zeros((1, 2 * nh, d), np.uint8)
+    x[:, 0], w[:, :, 0] = 0x38, 0x38                           # 1.0
+    offs = np.linspace(0, m, segments_ + 1).astype(np.int32)
+    h = guarded((m, nh), float("nan"), torch.bfloat16)
+    qmm.qmm_fp8_grouped_gemm_swiglu(dev(w), dev(np.ones((1, 2, 1), np.float32)), 1, 2 * nh, d, dev(x), dev(g[:, None]), 4096,
+                                    dev((np.arange(m) % 4096).astype(np.int32)), dev(np.zeros(segments_, np.int32)),
+                                    dev(offs), segments_, m, m // segments_, h)
+    h = as_f64(h.view(torch.int16))
+    v = np.tile(g.astype(np.float64), repeat)[:, None]
+    ref = fp8.silu(v) * v
+    tol = np.abs(ref) * (2.0 ** -8 + (1.3 * np.abs(v) + 8) * 2.0 ** -23) + 2.0 ** -125 * v * v + 2.0 ** -133
+    assert np.all(np.abs(h - ref) <= tol)
