@@ -98,7 +98,38 @@ inline Fp8RowsShape fp8_rows_shape(const Fp8GemmArgs& a) {
 int launch_fp8_rows(const Fp8GemmArgs& a, void* stream);
 // many rows: LDS tiles of 256 x 256 (large) or 64 x 128
 int launch_fp8_tile(const Fp8GemmArgs& a, bool large, void* stream);
-// the choice between them
+// the choice between them, and its launch
+enum class Fp8Kernel { kRows, kTile64, kTile256 };
+inline Fp8Kernel fp8_kernel(const Fp8GemmArgs& a) {
+  if (a.n_seg == 0) {
+    // Estimates in us of the three kernels from nb steps and the rounds of workgroups
+    // that 256 CUs take: a start and end, and a time for each step, which for the
+    // few-row kernel (its waves share the steps) depends on its weight blocks and on
+    // rows that share their cache lines, and of which three 64 x 128 tiles a CU hide
+    // a part from each other.  Measured few-row, 64 x 128, 256 x 256: 768 x 1903 x
+    // 4240 29.6, 24.8, 51.2; 512 x 4096 x 4096 20.1, 23.8, 43.8; 1024 x 4096 x 4096
+    // 40.0, 29.3, 45.8; 1052 x 10215 x 1296 63.4, 32.7, 26.8; 129 x 5619 x 4352 19.6,
+    // 24.4, 42.2.
+    auto rounds = [](int64_t workgroups) { return double((workgroups + 255) / 256); };
+    auto tiles = [&](int rows, int cols) { return ((a.t + rows - 1) / rows) * ((int64_t(a.n) + cols - 1) / cols); };
+    const Fp8RowsShape p = fp8_rows_shape(a);
+    const int nb = fp8_blocks(a.d);
+    const double step = (p.r == 4 ? 0.95 : p.r == 2 ? 0.8 : 0.6) * (a.d % kFp8Block ? 1.4 : 1.0);
+    const double few = rounds(p.workgroups) * (3 + (nb + p.waves - 1) / p.waves * step);
+    const double r64 = rounds(tiles(64, 128)), small = 3 + nb * std::max(0.65, 0.4 * r64) + 0.6 * r64;
+    const double large = rounds(tiles(256, 256)) * (8 + 1.5 * nb);
+    if (a.t <= kFp8RowsMax || (few <= small && few <= large)) return Fp8Kernel::kRows;
+    return large < small ? Fp8Kernel::kTile256 : Fp8Kernel::kTile64;
+  }
+  // The few-row kernel up to 3 rows a segment, if none can be long (128 experts of
+  // 3584 x 2048: 1 row 74 us few-row, 83 (64 x 128); 4 rows 116 and 103).  Large tiles
+  // from 80 rows on, if half of the CUs have one (64 experts of 2816 x 2048: 63 rows
+  // 88 us (64 x 128), 87 (256 x 256), 96 rows 103 and 94, 192 rows 151 and 125; 8 of
+  // 704 x 4080 with 150 rows, 24 large tiles: 29 and 43).
+  if (a.max_seg_rows <= kFp8RowsMax && fp8_usual_rows(a) <= 3) return Fp8Kernel::kRows;
+  const int64_t tiles = std::max<int64_t>(a.n_seg, a.m_total / 256) * ((int64_t(a.n) + 255) / 256);
+  return int64_t(a.m_total) >= int64_t(80) * a.n_seg && tiles >= 128 ? Fp8Kernel::kTile256 : Fp8Kernel::kTile64;
+}
 int launch_fp8_product(const Fp8GemmArgs& a, void* stream);
 
 struct TopkArgs {
@@ -176,6 +207,28 @@ struct NormArgs {
   uint8_t* q;               // [t][d] or NULL
   float* q_scales;          // [t][blocks]
 };
+// Waves of a row's workgroup and groups of 8 elements a lane, by width: eight waves,
+// with as few groups a lane as hold the row (8192 rows of 7168: 104.6 us, 111.4 with
+// four waves, 114.7 with sixteen), but four where eight would leave half the lanes
+// without work (8192 of 5120: 79.4, 83.7 with eight, 91.4 with sixteen, all with
+// conversions to bf16 in software), and sixteen for few rows, which wait for memory
+// once whatever they hold (64 of 5120: 4.8 us, 6.1 with four).
+struct NormShape {
+  int waves, groups;
+};
+inline NormShape norm_shape(int64_t t, int d) {
+  const int n8 = d / 8;
+  if (n8 <= 64) return {1, 1};
+  if (n8 <= 256) return {4, 1};
+  if (n8 <= 512) return {8, 1};
+  if (t <= 256 && n8 <= 1024) return {16, 1};
+  if (n8 <= 768) return {4, 3};
+  if (n8 <= 1024) return {8, 2};
+  if (n8 <= 1536) return {8, 3};
+  if (n8 <= 2048) return {8, 4};
+  if (n8 <= 4096) return {16, 4};
+  return {16, 8};
+}
 int launch_norm_residual(const NormArgs& a, void* stream);
 
 }  // namespace qmm

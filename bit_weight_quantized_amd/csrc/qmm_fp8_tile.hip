@@ -326,34 +326,8 @@ int launch_fp8_tile(const Fp8GemmArgs& a, bool large, void* stream) {
 }
 
 int launch_fp8_product(const Fp8GemmArgs& a, void* stream) {
-  if (a.n_seg == 0) {
-    // Estimates in us of the three kernels from nb steps and the rounds of workgroups
-    // that 256 CUs take: a start and end, and a time for each step, which for the
-    // few-row kernel (its waves share the steps) depends on its weight blocks and on
-    // rows that share their cache lines, and of which three 64 x 128 tiles a CU hide
-    // a part from each other.  Measured few-row, 64 x 128, 256 x 256: 768 x 1903 x
-    // 4240 29.6, 24.8, 51.2; 512 x 4096 x 4096 20.1, 23.8, 43.8; 1024 x 4096 x 4096
-    // 40.0, 29.3, 45.8; 1052 x 10215 x 1296 63.4, 32.7, 26.8; 129 x 5619 x 4352 19.6,
-    // 24.4, 42.2.
-    auto rounds = [](int64_t workgroups) { return double((workgroups + 255) / 256); };
-    auto tiles = [&](int rows, int cols) { return ((a.t + rows - 1) / rows) * ((int64_t(a.n) + cols - 1) / cols); };
-    const Fp8RowsShape p = fp8_rows_shape(a);
-    const int nb = fp8_blocks(a.d);
-    const double step = (p.r == 4 ? 0.95 : p.r == 2 ? 0.8 : 0.6) * (a.d % kFp8Block ? 1.4 : 1.0);
-    const double few = rounds(p.workgroups) * (3 + (nb + p.waves - 1) / p.waves * step);
-    const double r64 = rounds(tiles(64, 128)), small = 3 + nb * std::max(0.65, 0.4 * r64) + 0.6 * r64;
-    const double large = rounds(tiles(256, 256)) * (8 + 1.5 * nb);
-    if (a.t <= kFp8RowsMax || (few <= small && few <= large)) return launch_fp8_rows(a, stream);
-    return launch_fp8_tile(a, large < small, stream);
-  }
-  // The few-row kernel up to 3 rows a segment, if none can be long (128 experts of
-  // 3584 x 2048: 1 row 74 us few-row, 83 (64 x 128); 4 rows 116 and 103).  Large tiles
-  // from 80 rows on, if half of the CUs have one (64 experts of 2816 x 2048: 63 rows
-  // 88 us (64 x 128), 87 (256 x 256), 96 rows 103 and 94, 192 rows 151 and 125; 8 of
-  // 704 x 4080 with 150 rows, 24 large tiles: 29 and 43).
-  if (a.max_seg_rows <= kFp8RowsMax && fp8_usual_rows(a) <= 3) return launch_fp8_rows(a, stream);
-  const int64_t tiles = std::max<int64_t>(a.n_seg, a.m_total / 256) * ((int64_t(a.n) + 255) / 256);
-  return launch_fp8_tile(a, int64_t(a.m_total) >= int64_t(80) * a.n_seg && tiles >= 128, stream);
+  const Fp8Kernel k = fp8_kernel(a);
+  return k == Fp8Kernel::kRows ? launch_fp8_rows(a, stream) : launch_fp8_tile(a, k == Fp8Kernel::kTile256, stream);
 }
 
 }  // namespace qmm

@@ -192,22 +192,20 @@ int go(const NormArgs& a, hipStream_t s) {
 
 int launch_norm_residual(const NormArgs& a, void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
-  // Waves by width: eight, with as few groups a lane as hold the row (8192 rows of
-  // 7168: 104.6 us, 111.4 with four waves, 114.7 with sixteen), but four where
-  // eight would leave half the lanes without work (8192 of 5120: 79.4, 83.7 with
-  // eight, 91.4 with sixteen, all with conversions to bf16 in software), and sixteen for few rows, which wait for memory once
-  // whatever they hold (64 of 5120: 4.8 us, 6.1 with four).
-  const int n8 = a.d / 8;
-  if (n8 <= 64) return go<1, 1>(a, s);
-  if (n8 <= 256) return go<4, 1>(a, s);
-  if (n8 <= 512) return go<8, 1>(a, s);
-  if (a.t <= 256 && n8 <= 1024) return go<16, 1>(a, s);
-  if (n8 <= 768) return go<4, 3>(a, s);
-  if (n8 <= 1024) return go<8, 2>(a, s);
-  if (n8 <= 1536) return go<8, 3>(a, s);
-  if (n8 <= 2048) return go<8, 4>(a, s);
-  if (n8 <= 4096) return go<16, 4>(a, s);
-  return go<16, 8>(a, s);
+  const NormShape p = norm_shape(a.t, a.d);
+  switch (100 * p.groups + p.waves) {
+    case 101: return go<1, 1>(a, s);
+    case 104: return go<4, 1>(a, s);
+    case 108: return go<8, 1>(a, s);
+    case 116: return go<16, 1>(a, s);
+    case 304: return go<4, 3>(a, s);
+    case 208: return go<8, 2>(a, s);
+    case 308: return go<8, 3>(a, s);
+    case 408: return go<8, 4>(a, s);
+    case 416: return go<16, 4>(a, s);
+    case 816: return go<16, 8>(a, s);
+  }
+  return int(hipErrorInvalidValue);
 }
 
 }  // namespace qmm

@@ -84,11 +84,44 @@ int rows_copies() {
   return 0;
 }
 
+// The kernel that a call takes, for "dense t n d", "grouped n d n_seg m_total
+// max_seg_rows" and "norm t d" lines on stdin.
+int kernels() {
+  char what[16];
+  while (scanf("%15s", what) == 1) {
+    qmm::Fp8GemmArgs a{};
+    long long t = 0;
+    if (!strcmp(what, "norm")) {
+      int d = 0;
+      if (scanf("%lld %d", &t, &d) != 2) return 2;
+      const qmm::NormShape p = qmm::norm_shape(t, d);
+      printf("norm %d %d\n", p.waves, p.groups);
+      continue;
+    }
+    if (!strcmp(what, "dense")) {
+      if (scanf("%lld %d %d", &t, &a.n, &a.d) != 3) return 2;
+      a.t = t;
+    } else {
+      if (scanf("%d %d %d %d %d", &a.n, &a.d, &a.n_seg, &a.m_total, &a.max_seg_rows) != 5) return 2;
+      a.t = a.m_total;
+      a.max_seg_rows = std::min(a.max_seg_rows, a.m_total);
+    }
+    const qmm::Fp8Kernel k = qmm::fp8_kernel(a);
+    const qmm::Fp8RowsShape p = qmm::fp8_rows_shape(a);
+    if (k == qmm::Fp8Kernel::kRows)
+      printf("rows %d %d %d\n", p.waves, p.r, p.x8);
+    else
+      printf("tile %d\n", k == qmm::Fp8Kernel::kTile64 ? 64 : 256);
+  }
+  return 0;
+}
+
 }  // namespace
 
 int main(int argc, char** argv) {
   if (argc > 1 && !strcmp(argv[1], "scale_rows")) return scale_rows();
   if (argc > 1 && !strcmp(argv[1], "rows_copies")) return rows_copies();
+  if (argc > 1 && !strcmp(argv[1], "kernels")) return kernels();
   printf("no such check\n");
   return 2;
 }

@@ -1,10 +1,12 @@
-"""Host checks of the block-scaled e4m3 path's address functions (CPU only:
-g++ compiles tests/fp8_host_driver.cpp against the ROCm headers)."""
+"""Host checks of the block-scaled e4m3 path's address functions and of its choice of
+kernels (CPU only: g++ compiles tests/fp8_host_driver.cpp against the ROCm headers)."""
 import os
 import shutil
 import subprocess
 
 import pytest
+
+import fp8_shapes as S
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
@@ -21,8 +23,8 @@ def driver(tmp_path_factory):
                        capture_output=True, text=True)
     assert r.returncode == 0, r.stderr[-3000:]
 
-    def run(*args):
-        r = subprocess.run([str(exe), *map(str, args)], capture_output=True, text=True, timeout=120)
+    def run(*args, text=""):
+        r = subprocess.run([str(exe), *map(str, args)], input=text, capture_output=True, text=True, timeout=120)
         assert r.returncode == 0, r.stdout[-2000:] + r.stderr[-2000:]
         return r.stdout
     return run
@@ -34,3 +36,36 @@ def test_no_wave_reads_past_the_weight_scales(driver):
 
 def test_few_row_copies_stay_inside_their_buffers(driver):
     driver("rows_copies")
+
+
+def ask(driver, lines):
+    out = driver("kernels", text="\n".join(lines) + "\n").splitlines()
+    assert len(out) == len(lines)
+    return out
+
+
+def test_every_product_kernel_has_a_shape(driver):
+    """The shapes that the GPU tests run for each kernel still choose it, and the
+    few-row variants are all those that the source compiles."""
+    got = ask(driver, [f"dense {t} {n} {d}" for t, n, d in S.DENSE_ROWS.values()])
+    assert got == [f"rows {w} {r} {x}" for w, r, x in S.DENSE_ROWS]
+    assert set(ask(driver, [f"dense {t} {n} {d}" for t, n, d in S.DENSE_64])) == {"tile 64"}
+    assert set(ask(driver, [f"dense {t} {n} {d}" for t, n, d in S.DENSE_256])) == {"tile 256"}
+
+    def grouped(n, d, lengths):
+        return f"grouped {n} {d} {len(lengths)} {sum(lengths)} {max(lengths)}"
+    assert ask(driver, [grouped(*s) for s in S.GROUPED_ROWS.values()]) == [f"rows {w} {r} {x}" for w, r, x in S.GROUPED_ROWS]
+    assert set(ask(driver, [grouped(*s) for s in S.GROUPED_64])) == {"tile 64"}
+    assert set(ask(driver, [grouped(*s) for s in S.GROUPED_256])) == {"tile 256"}
+    # every variant that any number of rows and columns can reach
+    lines = [f"dense {t} {n} {d}" for t in (1, 8, 9, 16, 17, 32, 33, 64, 65, 100, 200, 600)
+             for n in (1, 300, 2570, 5130, 10200, 40000) for d in (16, 272, 1040, 2064, 8192)]
+    reached = {x for x in ask(driver, lines) if x.startswith("rows")}
+    assert reached == {f"rows {w} {r} {x}" for w, r, x in S.DENSE_ROWS}
+
+
+def test_every_norm_kernel_has_a_shape(driver):
+    got = ask(driver, [f"norm {t} {d}" for t, d in S.NORMS.values()])
+    assert got == [f"norm {w} {g}" for w, g in S.NORMS]
+    reached = set(ask(driver, [f"norm {t} {d}" for t in (1, 256, 257, 9000) for d in range(8, 65537, 8 * 61)]))
+    assert reached == set(got)
