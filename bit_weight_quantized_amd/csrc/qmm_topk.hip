@@ -300,7 +300,7 @@ __global__ __launch_bounds__(64 * WAVES) void topk_row_kernel(TopkArgs a, int ch
   const int tid = threadIdx.x;
   const int lane = tid & 63, rl = lane & 15, rt = lane >> 4;   // lane of the row, row of the wave
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int64_t t0 = int64_t(blockIdx.x) * chunk, t1 = min(a.t, t0 + chunk);
+  const int t0 = int(blockIdx.x) * chunk, t1 = min(int(a.t), t0 + chunk);   // at most 2^24 tokens
   const int ne = a.ne, k = a.k, groups = a.groups;
   const int n = (ne + 15) >> 4, e0 = n * rl;      // the lane's experts
   const int gs = ne / groups;                     // experts of a group
@@ -324,14 +324,14 @@ __global__ __launch_bounds__(64 * WAVES) void topk_row_kernel(TopkArgs a, int ch
   for (int i = 0; i < kRouteMaxK / 16; ++i) value_of[16 * i + rl] = -INFINITY;
   __syncthreads();
 
-  for (int64_t first = t0 + 4 * wave; first < t1; first += 4 * WAVES) {
-    const int64_t tok = first + rt;
+  for (int first = t0 + 4 * wave; first < t1; first += 4 * WAVES) {
+    const int tok = first + rt;
     const bool live = tok < t1;
     float l[J];
     uint32_t key[J];
     int from = e0;
     asm volatile("" : "+v"(from));                // what hangs on it is not kept from token to token
-    load_row<J, BF16>(a.logits, min(tok, t1 - 1) * a.ld, from, n, ne, whole, l);
+    load_row<J, BF16>(a.logits, int64_t(min(tok, t1 - 1)) * a.ld, from, n, ne, whole, l);
     float top = 0.f, total = 1.f;
     if constexpr (!SIGMOID) {
       float m = l[0];
@@ -464,7 +464,7 @@ __global__ __launch_bounds__(64 * WAVES) void topk_row_kernel(TopkArgs a, int ch
     }
     __builtin_amdgcn_wave_barrier();
     if (rl < k && live) {
-      a.topk[tok * k + rl] = e;
+      a.topk[tok * k + rl] = e;   // t·k is below 2^30
       a.weights[tok * k + rl] = w * a.scale;
       if (e >= 0) atomicAdd(&lds.count[e], 1);
       if constexpr (ONE) chosen[(tok - t0) * k + rl] = e;
