@@ -130,8 +130,6 @@ qmm::ProfileEvents qmm::take_profile_events() {
   return pe;
 }
 
-void qmm::arm_profile_events(ProfileEvents pe) { g_profile = pe; }
-
 qmm_status qmm::api_fail(qmm_status s, const char* what) { return fail(s, what); }
 qmm_status qmm::api_hip_fail(int err, const char* where) { return hip_fail(err, where); }
 

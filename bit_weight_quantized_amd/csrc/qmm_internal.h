@@ -150,7 +150,6 @@ struct ProfileEvents {
   void* stop;
 };
 ProfileEvents take_profile_events();
-void arm_profile_events(ProfileEvents pe);   // for a call's next launch
 
 // Error text of the calling thread (qmm_last_error); both return the status.
 qmm_status api_fail(qmm_status s, const char* what);
