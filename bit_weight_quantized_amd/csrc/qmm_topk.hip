@@ -261,7 +261,7 @@ __device__ __forceinline__ void wide_order(double& a, double& b) {   // the larg
   b = wide_min(a, b);
   a = hi;
 }
-// 8 values that rise and then fall (or the reverse), largest first
+// 8 values that rise and then fall (or the reverse), largest first: Batcher's bitonic merge
 __device__ __forceinline__ void wide_merge(double* v) {
 #pragma unroll
   for (int d = 4; d >= 1; d >>= 1)
@@ -269,7 +269,8 @@ __device__ __forceinline__ void wide_merge(double* v) {
     for (int i = 0; i < 8; ++i)
       if (!(i & d)) wide_order(v[i], v[i + d]);
 }
-// 8 values, largest first: pairs, then merges of 2 and 4
+// 8 values, largest first: Batcher's odd-even merge network (pairs, then merges of 2
+// and 4)
 __device__ __forceinline__ void wide_sort(double* v) {
   constexpr int pair[19][2] = {{0, 1}, {2, 3}, {4, 5}, {6, 7}, {0, 2}, {1, 3}, {4, 6}, {5, 7}, {1, 2}, {5, 6},
                                {0, 4}, {1, 5}, {2, 6}, {3, 7}, {2, 4}, {3, 5}, {1, 2}, {3, 4}, {5, 6}};

@@ -415,7 +415,8 @@ size_t qmm_route_topk_workspace_bytes(int64_t t, int32_t n_experts);
  *   logits  [t] rows of n_experts at stride ld, bf16 or fp32 (dtype).  A logit of
  *           -inf masks its expert for that token: never chosen, probability 0.
  *           NaN logits are never chosen either; under softmax they make the
- *           token's weights NaN
+ *           token's weights NaN, and where c is made from p (a bias, or groups by
+ *           their two largest) its choices -1
  *   p       softmax over the row or 1/(1 + e^-l), fp32
  *   c       p + bias (fp32[n_experts], or NULL).  Under softmax without a bias,
  *           unless groups go by their two largest, c is the logit itself: the
