@@ -129,10 +129,12 @@ def load():
 
 
 def _ptr(v):
+    if v is None or type(v) is int:   # an address
+        return v
     try:
         return v.data_ptr()
     except AttributeError:
-        if v is None or isinstance(v, int):   # an address
+        if isinstance(v, int):
             return v
         raise   # ctypes would pass bytes and str on as addresses of host memory
 

@@ -32,6 +32,24 @@ def test_only_tensors_addresses_and_none_are_pointers(wrong):
             call()
 
 
+def test_addresses_and_none_raise_nothing_inside(monkeypatch):
+    """An address is looked at by its type, not by a failed attribute: 0.09 us, not 0.39."""
+    import enum
+
+    class Address(enum.IntEnum):
+        A = P
+
+    import sys
+    events = []
+    sys.settrace(lambda frame, event, arg: (events.append(event), lambda f, e, a: events.append(e))[1])
+    try:
+        got = [qmm._ptr(v) for v in (None, 0, P)]
+    finally:
+        sys.settrace(None)
+    assert got == [None, 0, P] and "exception" not in events
+    assert qmm._ptr(Address.A) == P
+
+
 def test_current_stream_without_the_private_lookup(monkeypatch):
     """A torch without its private function for the raw handle: the public one serves."""
     torch = pytest.importorskip("torch")
