@@ -65,11 +65,12 @@ struct Fp8GemmArgs {
 // reduction axis, and 8·x8 activation rows a pass (the smallest of 1, 2, 4, 8 that
 // holds the rows, in several passes beyond 64).
 //
-// Dense: mostly four waves; r the largest that still gives 160 workgroups, that is work
-// for most of 256 CUs: a larger r reads the activations less often (64 x 13824 x
-// 5120: 20.6 us with r = 4, 27.3 with 2), a smaller one fills the chip (64 x 5120 x
-// 13824: 37.4, 29.2 and 44.0 us with r = 4, 2 and 1; 64 x 4096 x 7168: 21.2, 16.4,
-// 14.3).  Up to 16 rows r = 4 was never faster than 2.
+// Dense: mostly four waves; r the largest that gives more than 128 workgroups: a larger
+// r reads the activations less often (64 x 13824 x 5120: 15.6 us with r = 4, 19.6 with
+// 2), a smaller one fills 256 CUs (64 x 4096 x 7168: 9.8 us with r = 1, 11.0 with 2, 14.0
+// with 4), but half of r at more than 128 workgroups is a second round of the CUs (64 x
+// 4352 x 7168: r = 2 11.1, r = 1 17.6; 64 x 9216 x 4096: r = 4 10.8, r = 2 14.2; 1 x 4224
+// x 13824: r = 2 13.3, r = 1 14.0).  Up to 16 rows r = 4 was never faster than 2.
 // Eight waves instead where even r = 1 leaves CUs without a workgroup and every wave
 // still has two blocks (1 x 3584 x 7168: 5.9 us, 7.1 with four; 81 x 525 x 11360: 8.4,
 // 11.6; 20 x 2304 x 7168: 6.2, 6.8, but 32 x 4000 x 4096: 5.7, 5.4; with r = 2 1 x 8000
@@ -89,7 +90,7 @@ inline Fp8RowsShape fp8_rows_shape(const Fp8GemmArgs& a) {
   int x8 = a.t <= 8 ? 1 : a.t <= 16 ? 2 : a.t <= 32 ? 4 : 8;
   auto workgroups = [&](int r) { return (int64_t(a.n) + 16 * r - 1) / (16 * r) * ((a.t + 8 * x8 - 1) / (8 * x8)); };
   int r = x8 <= 2 ? 2 : 4;
-  while (r > 1 && workgroups(r) < 160) r /= 2;
+  while (r > 1 && workgroups(r) <= 128) r /= 2;
   if (r > 1 || workgroups(1) > (x8 <= 2 ? 256 : 160) || a.d < 16 * kFp8Block) return {r, x8, 4, workgroups(r)};
   x8 = std::min(x8, 4);
   return {1, x8, 8, workgroups(1)};

@@ -9,9 +9,8 @@ DENSE_ROWS = {(4, 1, 1): (1, 300, 1040), (4, 1, 2): (9, 300, 1040), (4, 1, 4): (
               (8, 1, 1): (1, 300, 2064), (8, 1, 2): (9, 300, 2064), (8, 1, 4): (30, 300, 2064)}
 
 # 64 x 128 tiles: whole, with every height of a part tile, one block and many
-DENSE_64 = [(500, 513, 272), (961, 272, 272), (976, 272, 272), (977, 272, 272), (992, 272, 272), (993, 272, 272),
-            (1008, 272, 272), (1009, 272, 272), (1023, 272, 272), (1000, 272, 256), (300, 1903, 1040), (1500, 1000, 128),
-            (1500, 400, 16)]
+DENSE_64 = [(1473, 700, 272), (1488, 700, 272), (1489, 700, 272), (1504, 700, 272), (1505, 700, 272), (1520, 700, 272),
+            (1521, 700, 272), (1535, 1003, 400), (1536, 1000, 128), (2500, 513, 1040), (1500, 400, 16)]
 DENSE_256 = [(2049, 6001, 336), (2049, 6100, 400)]
 
 # n, d, rows of each segment; few-row kernel of two and four waves, then tiles

@@ -69,3 +69,17 @@ def test_every_norm_kernel_has_a_shape(driver):
     assert got == [f"norm {w} {g}" for w, g in S.NORMS]
     reached = set(ask(driver, [f"norm {t} {d}" for t in (1, 256, 257, 9000) for d in range(8, 65537, 8 * 61)]))
     assert reached == set(got)
+
+
+def test_few_row_kernel_fills_the_compute_units_once(driver):
+    """Fewer weight rows a workgroup are taken to fill 256 CUs, never where that makes
+    a second round of them."""
+    want = {(64, 4096, 7168): "rows 4 1 8", (64, 4097, 7168): "rows 4 2 8", (64, 5119, 7168): "rows 4 2 8",
+            (33, 8192, 4096): "rows 4 2 8", (33, 8193, 4096): "rows 4 4 8", (1, 4224, 13824): "rows 4 2 1",
+            (32, 4608, 4096): "rows 4 2 4"}
+    assert ask(driver, [f"dense {t} {n} {d}" for t, n, d in want]) == list(want.values())
+    sizes = [(t, n) for t in (1, 9, 17, 33, 64) for n in range(16, 12000, 48)]
+    for (t, n), got in zip(sizes, ask(driver, [f"dense {t} {n} 1024" for t, n in sizes])):
+        waves, r, x8 = map(int, got.split()[1:])
+        if r < (4 if t > 16 else 2):
+            assert -(-n // (16 * r)) * -(-t // (8 * x8)) <= 256, (t, n, got)
