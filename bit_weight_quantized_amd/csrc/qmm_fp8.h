@@ -71,14 +71,17 @@ struct Fp8GemmArgs {
 // with 4), but half of r at more than 128 workgroups is a second round of the CUs (64 x
 // 4352 x 7168: r = 2 11.1, r = 1 17.6; 64 x 9216 x 4096: r = 4 10.8, r = 2 14.2; 1 x 4224
 // x 13824: r = 2 13.3, r = 1 14.0).  Up to 16 rows r = 4 was never faster than 2.
-// Eight waves instead where even r = 1 leaves CUs without a workgroup and every wave
-// still has two blocks (1 x 3584 x 7168: 5.9 us, 7.1 with four; 81 x 525 x 11360: 8.4,
-// 11.6; 20 x 2304 x 7168: 6.2, 6.8, but 32 x 4000 x 4096: 5.7, 5.4; with r = 2 1 x 8000
-// x 8192: 14.0, 11.9), for 32 rows a pass at most, which is what their LDS holds.
+// Eight waves instead, for 32 rows a pass at most, which is what their LDS holds, where
+// even r = 1 leaves CUs without a workgroup, their own workgroups are one round, and
+// every wave still has two blocks: 1 x 3584 x 7168 5.8 us, 6.9 with four; 81 x 525 x
+// 11360 8.3, 11.3; 20 x 2304 x 7168 6.1, 6.8; 64 x 2048 x 7168 6.8, 8.2, but 64 x 2304 x
+// 7168, of 288 workgroups, 11.0, 8.2; 32 x 4000 x 4096 6.0, 5.4 (beyond 16 rows 160
+// workgroups); with r = 2 1 x 8000 x 8192 14.4, 12.0.
 //
 // Grouped: 8 rows a pass and r = 2 (the tile kernel has the longer segments).  Two
 // waves, each with a longer run of blocks, but four where there may be fewer than 512
-// workgroups (1 token, 8 experts, 1024 x 3584: 8.3 us, 13 with two).
+// workgroups (1 token, 8 experts, 1024 x 3584: 7.9 us, 10.4 with two; 2 tokens, 6 of 64
+// experts, 2816 x 2048: 15.9 us, 14.0 with two).
 constexpr int kFp8RowsMax = 64;
 inline int64_t fp8_usual_rows(const Fp8GemmArgs& a) { return (int64_t(a.m_total) + a.n_seg - 1) / a.n_seg; }
 struct Fp8RowsShape {
@@ -91,9 +94,10 @@ inline Fp8RowsShape fp8_rows_shape(const Fp8GemmArgs& a) {
   auto workgroups = [&](int r) { return (int64_t(a.n) + 16 * r - 1) / (16 * r) * ((a.t + 8 * x8 - 1) / (8 * x8)); };
   int r = x8 <= 2 ? 2 : 4;
   while (r > 1 && workgroups(r) <= 128) r /= 2;
-  if (r > 1 || workgroups(1) > (x8 <= 2 ? 256 : 160) || a.d < 16 * kFp8Block) return {r, x8, 4, workgroups(r)};
-  x8 = std::min(x8, 4);
-  return {1, x8, 8, workgroups(1)};
+  const int x4 = std::min(x8, 4);   // eight waves: 32 rows a pass
+  const int64_t four = workgroups(1), eight = (int64_t(a.n) + 15) / 16 * ((a.t + 8 * x4 - 1) / (8 * x4));
+  if (r > 1 || eight > 256 || four > (x8 <= 2 ? 256 : 160) || a.d < 16 * kFp8Block) return {r, x8, 4, workgroups(r)};
+  return {1, x4, 8, eight};
 }
 // few rows: every weight read once for up to 64 rows
 int launch_fp8_rows(const Fp8GemmArgs& a, void* stream);

@@ -83,3 +83,14 @@ def test_few_row_kernel_fills_the_compute_units_once(driver):
         waves, r, x8 = map(int, got.split()[1:])
         if r < (4 if t > 16 else 2):
             assert -(-n // (16 * r)) * -(-t // (8 * x8)) <= 256, (t, n, got)
+
+
+def test_eight_waves_are_one_round(driver):
+    """Eight waves take 32 rows a pass: 33 .. 64 rows are two passes, which count."""
+    want = {(64, 2048, 7168): "rows 8 1 4", (64, 2049, 7168): "rows 4 1 8", (33, 2304, 2048): "rows 4 1 8",
+            (64, 2560, 4096): "rows 4 1 8", (32, 2560, 4096): "rows 8 1 4", (1, 4096, 7168): "rows 8 1 1"}
+    assert ask(driver, [f"dense {t} {n} {d}" for t, n, d in want]) == list(want.values())
+    sizes = [(t, n) for t in (1, 16, 32, 33, 64, 81, 300, 943) for n in range(16, 4200, 48)]
+    for (t, n), got in zip(sizes, ask(driver, [f"dense {t} {n} 7168" for t, n in sizes])):
+        if got.startswith("rows 8"):
+            assert -(-n // 16) * -(-t // (8 * int(got.split()[3]))) <= 256, (t, n, got)
