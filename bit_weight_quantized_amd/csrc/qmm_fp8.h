@@ -112,9 +112,10 @@ inline Fp8Kernel fp8_kernel(const Fp8GemmArgs& a) {
     // few-row kernel (its waves share the steps) depends on its weight blocks and on
     // rows that share their cache lines, and of which three 64 x 128 tiles a CU hide
     // a part from each other.  Measured few-row, 64 x 128, 256 x 256: 768 x 1903 x
-    // 4240 29.6, 24.8, 51.2; 512 x 4096 x 4096 20.1, 23.8, 43.8; 1024 x 4096 x 4096
-    // 40.0, 29.3, 45.8; 1052 x 10215 x 1296 63.4, 32.7, 26.8; 129 x 5619 x 4352 19.6,
-    // 24.4, 42.2.
+    // 4240 29.4, 24.7, 50.5; 512 x 4096 x 4096 19.8, 23.0, 42.9; 1024 x 4096 x 4096
+    // 38.4, 28.6, 43.5; 1052 x 10215 x 1296 63.3, 33.2, 24.9; 129 x 5619 x 4352 18.7,
+    // 23.9, 42.4; 1500 x 5120 x 5120 90.5, 64.5, 55.4.  Over 157 drawn sizes of 17 ..
+    // 4096 rows the choice took 1.02 of the time of the best kernel (geometric mean).
     auto rounds = [](int64_t workgroups) { return double((workgroups + 255) / 256); };
     auto tiles = [&](int rows, int cols) { return ((a.t + rows - 1) / rows) * ((int64_t(a.n) + cols - 1) / cols); };
     const Fp8RowsShape p = fp8_rows_shape(a);
@@ -126,11 +127,14 @@ inline Fp8Kernel fp8_kernel(const Fp8GemmArgs& a) {
     if (a.t <= kFp8RowsMax || (few <= small && few <= large)) return Fp8Kernel::kRows;
     return large < small ? Fp8Kernel::kTile256 : Fp8Kernel::kTile64;
   }
-  // The few-row kernel up to 3 rows a segment, if none can be long (128 experts of
-  // 3584 x 2048: 1 row 74 us few-row, 83 (64 x 128); 4 rows 116 and 103).  Large tiles
-  // from 80 rows on, if half of the CUs have one (64 experts of 2816 x 2048: 63 rows
-  // 88 us (64 x 128), 87 (256 x 256), 96 rows 103 and 94, 192 rows 151 and 125; 8 of
-  // 704 x 4080 with 150 rows, 24 large tiles: 29 and 43).
+  // The few-row kernel up to 3 rows a segment on average, if none can be long: 128
+  // experts, 32 rows of SwiGLU 4096 x 3584 (25 experts have rows) 66.6 us few-row, 78.6
+  // (64 x 128); plain 3584 x 2048, 128 rows (54 experts) 64.9 and 66.4, 384 rows (88
+  // experts) 118.5 and 115.0, 512 rows 125.5 and 113.5; 8 rows of 8 experts, SwiGLU 1024
+  // x 3584, 7.9 and 25.4.  Large tiles from 80 rows on, if half of the CUs have one: 64
+  // experts of SwiGLU 2816 x 2048, 63 rows each 80.3 us (64 x 128), 84.2 (256 x 256), 96
+  // rows 98.1 and 88.0, 192 rows 149.7 and 119.7; 8 of 704 x 4080 with 150 rows, 24
+  // large tiles, 25.4 and 47.1.
   if (a.max_seg_rows <= kFp8RowsMax && fp8_usual_rows(a) <= 3) return Fp8Kernel::kRows;
   const int64_t tiles = std::max<int64_t>(a.n_seg, a.m_total / 256) * ((int64_t(a.n) + 255) / 256);
   return int64_t(a.m_total) >= int64_t(80) * a.n_seg && tiles >= 128 ? Fp8Kernel::kTile256 : Fp8Kernel::kTile64;
@@ -213,11 +217,12 @@ struct NormArgs {
   float* q_scales;          // [t][blocks]
 };
 // Waves of a row's workgroup and groups of 8 elements a lane, by width: eight waves,
-// with as few groups a lane as hold the row (8192 rows of 7168: 104.6 us, 111.4 with
-// four waves, 114.7 with sixteen), but four where eight would leave half the lanes
-// without work (8192 of 5120: 79.4, 83.7 with eight, 91.4 with sixteen, all with
-// conversions to bf16 in software), and sixteen for few rows, which wait for memory
-// once whatever they hold (64 of 5120: 4.8 us, 6.1 with four).
+// with as few groups a lane as hold the row (8192 rows of 4096: 52.3 us, 54.0 with four
+// waves, 66.3 with sixteen; 7168: 95.5, 99.6, 97.9), but four where eight would leave
+// lanes without work (8192 of 5120: 73.3, 75.1 with eight, 77.5 with sixteen), and
+// sixteen for up to 256 rows, a row for each CU, whose loads are all in flight at once
+// (by the kernel's own time 64 of 5120: 4.2 us, 4.4 with four; 256: 4.9, 5.2; 300: 6.6,
+// 6.0).
 struct NormShape {
   int waves, groups;
 };

@@ -32,9 +32,9 @@
 //
 // Bound by the matrix unit for long reductions, by a tile's start and end (4 and 3 us
 // of 256 x 256) for short ones, and by the clock, which falls to 1.9 .. 2.0 GHz under
-// this load: 8192 x 8192 x 8192 433 us (2.54 PFLOP/s), 2048 x 13824 x 5120 138 us
-// (2.10; 432 tiles in two rounds of 256 CUs), 64 experts of 4096 x 3584 with 32768
-// rows 536 us (1.79).  256 x 256 is the largest tile whose fp32 sums leave registers
+// this load, by what the codes are: 8192 x 8192 x 8192 423 us (2.60 PFLOP/s), 2048 x
+// 13824 x 5120 126 to 141 us (2.30 to 2.06; 432 tiles in two rounds of 256 CUs), 64
+// experts of 4096 x 3584 with 32768 rows 533 us (1.80).  256 x 256 is the largest tile whose fp32 sums leave registers
 // for the operands (230 of 256); it reads half the bytes of 128 x 128 for a product.
 #include <hip/hip_runtime.h>
 

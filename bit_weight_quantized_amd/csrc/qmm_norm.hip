@@ -10,7 +10,7 @@
 // by the two sums over the row for a few.  Everything between the loads and the
 // stores is fp32; h is made from v before v is rounded for the store, and the
 // e4m3 codes from h before h is rounded.  8192 x 5120 with gate and both outputs: 76.7 us
-// (74 us for its bytes at the rate of a copy); 1 x 5120: 4.5 us.  At most 128 registers,
+// (74 us for its bytes at the rate of a copy); 1 x 5120: 4.1 us.  At most 128 registers,
 // for four waves on a SIMD (1000 x 13824: 26.7 us, 32.9 with the 130 of three waves).
 #include <hip/hip_runtime.h>
 

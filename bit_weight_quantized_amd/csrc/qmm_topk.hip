@@ -16,10 +16,13 @@
 // largest and merges across the row instead where there are 5 to 8 rounds.  More
 // experts: a wave has a token, and scalar instructions find the winner in the
 // comparisons' masks.
-// Bound by instructions: 16384 tokens x 256 experts in 8 groups, k = 8, are 2 us of
-// bytes and take 24 (18.9 router, 6.8 placing in a trace; a wave a token: 34); a sigmoid
-// that rounds as the formula does is 35 instructions alone, and scores that round
-// otherwise would change choices.
+// 16384 tokens x 256 experts in 8 groups, k = 8, are 2 us of bytes and take 24 (18.5
+// router, 6.8 placing in a trace; a wave a token: 34).  Counters of the router: 1530
+// vector instructions a wave, which has four tokens once; the vector units issue 64%
+// of the time, the rest is what a wave's one pass waits for.  A sigmoid that rounds as
+// the formula does is 35 instructions a score, 560 of those a wave, and scores that
+// round otherwise would change choices; the sort is 360.  Placing waits for the counts
+// and its LDS passes: its vector units issue half of a CU's busy time.
 //
 // Grouping counts the chunk's tokens per expert in LDS (integer atomics, order
 // free).  One chunk: the same workgroup scans the counts and places its rows.
@@ -758,8 +761,8 @@ int go(const TopkArgs& a, hipStream_t s) {
   int64_t chunk = topk_chunk(a.t, a.ne);
   // One workgroup for up to 128 tokens, or more of them and a second launch where
   // its passes take longer than that (256 experts, 32 tokens: 15.1 us in one, 10.6 in
-  // two, 128 tokens 26.9 and 11.1; 896 experts, 75 tokens 64 and 15; 60 experts, 128
-  // tokens 9.6 and 9.5).
+  // two, 128 tokens 26.9 and 11.1; 896 experts, 75 tokens, k = 3, 64 and 15; 60
+  // experts, 128 tokens 9.6 and 9.5).
   if (a.t <= kTopkChunk && a.t * a.ne >= 8192) chunk = 16;
   if (a.ne <= 256 && a.k <= kTopkRowMaxK) {
     // Few tokens of many experts: a wave each (256 experts, 1 token: 5.8 us, 7.6 with
@@ -781,7 +784,8 @@ int go(const TopkArgs& a, hipStream_t s) {
 // columns: out = Σ_j weights[j]·o[slot_row[j]] (+ shared), in slot order, fp32,
 // rounded once.  Bound by the reads of o; the rows are known before the first
 // load, so all of a token's loads are in flight together (8 slots at a time).  4096
-// tokens, 8 slots of 3584: 44 us (6.0 TB/s).
+// tokens, 8 slots of 3584: 40 us by itself (6.6 TB/s, a part of o from the Infinity
+// Cache), 46 after the product that writes o (5.7).
 __global__ __launch_bounds__(256) void gather_kernel(GatherArgs a, int64_t first) {
   const int64_t tok = first + blockIdx.x;
   const int c8 = blockIdx.y * 256 + threadIdx.x;
