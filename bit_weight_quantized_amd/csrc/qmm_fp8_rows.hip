@@ -21,7 +21,7 @@
 // conversions would cost more than the reads.
 //
 // Measured: 1 x 13824 x 5120 12.6 us (5.6 TB/s), 16 rows of it 13.3; 37 x 5120 x 13824
-// 16.4 us (4.4), 64 rows 19.9 (3.7; the activations come again from L2 for every 32
+// 16.4 to 16.8 us (4.3), 64 rows 19.9 (3.7; the activations come again from L2 for every 32
 // weight rows); SwiGLU, 25 of 128 experts with a row or two, 4096 x 3584 65.4 us (5.6);
 // all with a part of the weights in the Infinity Cache.
 #include <hip/hip_runtime.h>

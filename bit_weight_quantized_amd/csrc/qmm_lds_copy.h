@@ -24,25 +24,26 @@ constexpr int vmcnt_imm(int n) { return (n & 15) | ((n >> 4) << 14) | (7 << 4) |
 // preserve m0 across the asm, which is sound only while no compiler-generated
 // instruction in a kernel that copies keeps a value in m0 (a CPU test
 // compiles the files that include this header and checks).
+//
+// Wait states that the compiler inserts for its own instructions only: one
+// between a write of m0 and a copy to LDS, which the s_nop is, and five between
+// a vector instruction that writes a scalar register (a lane read back, also
+// of a spilled scalar) and a copy that reads it, which a CPU test looks for in
+// the generated code.
+__device__ __forceinline__ void copy_at(uint32_t lds) { asm volatile("s_mov_b32 m0, %0" : : "s"(lds) : "m0"); }
 __device__ __forceinline__ void copy16_to_lds(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
-               :
-               : "v"(voff), "s"(r), "s"(lds)
-               : "memory", "m0");
+  copy_at(lds);
+  asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" : : "v"(voff), "s"(r) : "memory");
 }
 __device__ __forceinline__ void copy4_to_lds(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\tbuffer_load_dword %0, %1, 0 offen lds"
-               :
-               : "v"(voff), "s"(r), "s"(lds)
-               : "memory", "m0");
+  copy_at(lds);
+  asm volatile("s_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds" : : "v"(voff), "s"(r) : "memory");
 }
 // the same from voff + soff, soff wave-uniform (voff alone has to be in range
 // for the lanes that read)
 __device__ __forceinline__ void copy16_to_lds_from(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\tbuffer_load_dwordx4 %0, %1, %3 offen lds"
-               :
-               : "v"(voff), "s"(r), "s"(lds), "s"(soff)
-               : "memory", "m0");
+  copy_at(lds);
+  asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds" : : "v"(voff), "s"(r), "s"(soff) : "memory");
 }
 __device__ __forceinline__ uint32_t lds_addr(const void* p) {
   return uint32_t(uintptr_t((lds_ptr_t)p));
