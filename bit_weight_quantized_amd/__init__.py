@@ -22,6 +22,8 @@ __all__ = [
     "QMM_KERNEL_GROUPED_MATMUL", "QMM_KERNEL_MULTI_ROW", "EXPORTS",
     "qmm_fp8_quant", "qmm_fp8_gemm", "qmm_fp8_grouped_gemm", "qmm_fp8_grouped_gemm_swiglu",
     "qmm_route_topk_workspace_bytes", "qmm_route_topk", "qmm_moe_gather", "qmm_norm_residual",
+    "qmm_mxfp4_scale_bytes", "qmm_mxfp4_quant", "qmm_mxfp4_gemm", "qmm_mxfp4_grouped_gemm",
+    "qmm_mxfp4_grouped_gemm_swiglu", "QMM_MX_FLOOR", "QMM_MX_FIT",
     "QMM_BF16", "QMM_F32", "QMM_SCORE_SOFTMAX", "QMM_SCORE_SIGMOID", "QMM_GROUP_MAX", "QMM_GROUP_TOP2",
 ]
 
@@ -41,6 +43,8 @@ QMM_SCORE_SOFTMAX = 0
 QMM_SCORE_SIGMOID = 1
 QMM_GROUP_MAX = 0
 QMM_GROUP_TOP2 = 1
+QMM_MX_FLOOR = 0
+QMM_MX_FIT = 1
 
 STATUS = {0: "QMM_OK", 1: "QMM_E_ARG", 2: "QMM_E_SHAPE", 3: "QMM_E_ALIGN", 4: "QMM_E_UNSUPPORTED",
           5: "QMM_E_WORKSPACE", 6: "QMM_E_HIP", 7: "QMM_E_LAYOUT", 8: "QMM_E_VALUE"}
@@ -51,7 +55,8 @@ EXPORTS = ("qmm_packed_bytes", "qmm_workspace_bytes", "qmm_pack", "qmm_unpack", 
            "qmm_grouped_gemm_swiglu", "qmm_moe_combine", "qmm_gemv_int8", "qmm_gemm_noalloc",
            "qmm_set_kernel", "qmm_get_kernel", "qmm_fp8_quant", "qmm_fp8_gemm", "qmm_fp8_grouped_gemm",
            "qmm_fp8_grouped_gemm_swiglu", "qmm_route_topk_workspace_bytes", "qmm_route_topk",
-           "qmm_moe_gather", "qmm_norm_residual")
+           "qmm_moe_gather", "qmm_norm_residual", "qmm_mxfp4_scale_bytes", "qmm_mxfp4_quant", "qmm_mxfp4_gemm",
+           "qmm_mxfp4_grouped_gemm", "qmm_mxfp4_grouped_gemm_swiglu")
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _lib = None
@@ -119,6 +124,13 @@ def load():
         "qmm_moe_gather": (ctypes.c_int, [vp, i32, i64, i64, i32, vp, vp, vp, vp, vp]),
         "qmm_norm_residual": (ctypes.c_int, [i64, i64, vp, i64, vp, vp, i64, i64, vp, ctypes.c_int, i64, f32, vp, i64,
                                              vp, f32, f32, vp, i64, vp, vp, vp]),
+        "qmm_mxfp4_scale_bytes": (sz, [i64]),
+        "qmm_mxfp4_quant": (ctypes.c_int, [vp, i64, i64, i64, ctypes.c_int, vp, vp, vp]),
+        "qmm_mxfp4_gemm": (ctypes.c_int, [vp, i64, i64, i64, vp, vp, vp, i64, vp]),
+        "qmm_mxfp4_grouped_gemm": (ctypes.c_int, [vp, i64, i32, i64, i64, vp, vp, i64, vp, vp, vp, i32, i32, i32, vp,
+                                                  vp]),
+        "qmm_mxfp4_grouped_gemm_swiglu": (ctypes.c_int, [vp, i64, i32, i64, i64, vp, vp, i64, vp, vp, vp, i32, i32, i32,
+                                                         ctypes.c_int, vp, vp, vp, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -321,3 +333,34 @@ def qmm_norm_residual(t, d, o, ldo, post_w, gate, ldg, gate_rows, r, r_type, ldr
     _check(load().qmm_norm_residual(t, d, _ptr(o), ldo, _ptr(post_w), _ptr(gate), ldg, gate_rows, _ptr(r), r_type,
                                     ldr, res_scale, _ptr(r_out), ldr_out, _ptr(pre_w), w_offset, eps, _ptr(h), ldh,
                                     _ptr(q), _ptr(q_scales), _stream(stream)), "qmm_norm_residual")
+
+
+def qmm_mxfp4_scale_bytes(d: int) -> int:
+    return int(load().qmm_mxfp4_scale_bytes(d))
+
+
+def qmm_mxfp4_quant(x, t, d, ldx, rule, q, scales, stream=None):
+    _check(load().qmm_mxfp4_quant(_ptr(x), t, d, ldx, rule, _ptr(q), _ptr(scales), _stream(stream)), "qmm_mxfp4_quant")
+
+
+def qmm_mxfp4_gemm(packed, t, n, d, x, x_scales, y, ldy, stream=None):
+    _check(load().qmm_mxfp4_gemm(_ptr(packed), t, n, d, _ptr(x), _ptr(x_scales), _ptr(y), ldy, _stream(stream)),
+           "qmm_mxfp4_gemm")
+
+
+def qmm_mxfp4_grouped_gemm(packed_stack, expert_stride_bytes, n_experts, n, d, x, x_scales, t_x, row_index, seg_expert,
+                           seg_offsets, n_seg, m_total, max_seg_rows, y, stream=None):
+    _check(load().qmm_mxfp4_grouped_gemm(_ptr(packed_stack), expert_stride_bytes, n_experts, n, d, _ptr(x),
+                                         _ptr(x_scales), t_x, _ptr(row_index), _ptr(seg_expert), _ptr(seg_offsets),
+                                         n_seg, m_total, max_seg_rows, _ptr(y), _stream(stream)),
+           "qmm_mxfp4_grouped_gemm")
+
+
+def qmm_mxfp4_grouped_gemm_swiglu(packed_stack, expert_stride_bytes, n_experts, n, d, x, x_scales, t_x, row_index,
+                                  seg_expert, seg_offsets, n_seg, m_total, max_seg_rows, rule, h, hq, h_scales,
+                                  stream=None):
+    _check(load().qmm_mxfp4_grouped_gemm_swiglu(_ptr(packed_stack), expert_stride_bytes, n_experts, n, d, _ptr(x),
+                                                _ptr(x_scales), t_x, _ptr(row_index), _ptr(seg_expert),
+                                                _ptr(seg_offsets), n_seg, m_total, max_seg_rows, rule, _ptr(h),
+                                                _ptr(hq), _ptr(h_scales), _stream(stream)),
+           "qmm_mxfp4_grouped_gemm_swiglu")

@@ -474,11 +474,81 @@ qmm_status qmm_norm_residual(int64_t t, int64_t d, const qmm_bf16* o, int64_t ld
                              float w_offset, float eps, qmm_bf16* h, int64_t ldh, uint8_t* q, float* q_scales,
                              void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Microscaled 4-bit path: both sides of the product in MXFP4, the weights the same packed
+ * blobs that qmm_gemm and the grouped calls take with bf16 activations.
+ *
+ * Activations are rows of E2M1 codes (the values 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their
+ * negatives) with an E8M0 exponent for each block of 32:
+ *   codes   uint8[t][d/2]: code k of a row is the low nibble of byte k/2 for even k, the
+ *           high nibble for odd k
+ *   scales  uint8[t][qmm_mxfp4_scale_bytes(d)]: the exponents of a row's d/32 blocks, then
+ *           zeros (rows are 16 bytes for every 512 codes); 255 is NaN
+ * Limits: d a multiple of 32, 32 <= d <= 65536; 1 <= n <= 2^28 with n*d/2 of one matrix
+ * below 2^31; t <= 2^24; t = 0 is a no-op.  Codes and scales 16-byte aligned.
+ * ------------------------------------------------------------------------- */
+
+/* How a block's exponent E follows from m = max |x| of its 32 values:
+ *   QMM_MX_FLOOR  floor(log2 m) - 2 + 127, the conversion of the OCP Microscaling Formats
+ *                 v1.0 specification: m lands in [4, 8), what is over 6 saturates
+ *   QMM_MX_FIT    the smallest E with m <= 6·2^(E-127): m lands in (3, 6], nothing saturates
+ * both held to 0 .. 254 (a block of zeros: 0). */
+typedef enum { QMM_MX_FLOOR = 0, QMM_MX_FIT = 1 } qmm_mx_rule;
+
+/* Bytes of one row of activation scales: 16·ceil(d / 512); 0 for an invalid d.  Host only. */
+size_t qmm_mxfp4_scale_bytes(int64_t d);
+
+/* bf16 rows to E2M1 codes with their exponents: q = E2M1(x·2^(127-E)), to the nearest code,
+ * a midpoint to the even one, magnitudes over 6 to 6.  The scaling is exact, so the codes
+ * follow from x alone, bit for bit.  A block that holds an infinity or a NaN gets E = 255
+ * and zero codes, and stands for NaN.
+ *   x       bf16[t] rows of d at stride ldx (elements; >= d, a multiple of 8),
+ *           16-byte aligned */
+qmm_status qmm_mxfp4_quant(const qmm_bf16* x, int64_t t, int64_t d, int64_t ldx, qmm_mx_rule rule, uint8_t* q,
+                           uint8_t* scales, void* stream);
+
+/* Y = X·Wᵀ with both sides in MXFP4:
+ *   y[t][n] = Σ_b 2^(xs[t][b]-127)·2^(E[n][b]-127)·Σ_{k in b} x[t][k]·w[n][k]
+ * block sums exact, the sum over the blocks in fp32 in the matrix cores, rounded once to
+ * bf16.  A block with the exponent 255 makes its row NaN.  packed: a QMM_MXFP4_G32 blob of
+ * [n, d]; y: bf16 rows of n at stride ldy (elements, >= n); the bytes between them are left
+ * alone.  No workspace; the order of every sum depends on the sizes of the call alone. */
+qmm_status qmm_mxfp4_gemm(const void* packed, int64_t t, int64_t n, int64_t d, const uint8_t* x, const uint8_t* x_scales,
+                          qmm_bf16* y, int64_t ldy, void* stream);
+
+/* qmm_mxfp4_gemm for the segments of grouped rows: stack, stride and tables as for
+ * qmm_grouped_gemm.
+ *   x         codes of t_x rows (t_x·d/2 < 2^31) and their scales
+ *   row_index int32[m_total] (grouped row r reads x row row_index[r]) or NULL
+ *   y         bf16[m_total][n]
+ *   max_seg_rows  host upper bound on the rows of a segment: it selects kernels
+ *             and launch shapes, never memory bounds, and t is always a valid one
+ * A segment whose expert is outside [0, n_experts), or a row whose row_index is outside
+ * [0, t_x), gets NaN outputs.  Rows covered by no segment are not written. */
+qmm_status qmm_mxfp4_grouped_gemm(const void* packed_stack, int64_t expert_stride_bytes, int32_t n_experts, int64_t n,
+                                  int64_t d, const uint8_t* x, const uint8_t* x_scales, int64_t t_x,
+                                  const int32_t* row_index, const int32_t* seg_expert, const int32_t* seg_offsets,
+                                  int32_t n_seg, int32_t m_total, int32_t max_seg_rows, qmm_bf16* y, void* stream);
+
+/* The same for a gate_up stack (rows [0, n/2) the gate, rows [n/2, n) the up projection; n
+ * even) with SwiGLU in the epilogue, v = silu(gate)·up of the fp32 sums, in one of two forms:
+ *   h              bf16[m_total][n/2], v rounded once; or
+ *   hq, h_scales   v quantised as qmm_mxfp4_quant does by `rule`, but from fp32, ready to be
+ *                  the x of the down projection (n/2 a multiple of 32); NaN rows get
+ *                  exponents of 255
+ * The other form's pointers are NULL (rule then does not matter without hq). */
+qmm_status qmm_mxfp4_grouped_gemm_swiglu(const void* packed_stack, int64_t expert_stride_bytes, int32_t n_experts,
+                                         int64_t n, int64_t d, const uint8_t* x, const uint8_t* x_scales, int64_t t_x,
+                                         const int32_t* row_index, const int32_t* seg_expert,
+                                         const int32_t* seg_offsets, int32_t n_seg, int32_t m_total,
+                                         int32_t max_seg_rows, qmm_mx_rule rule, qmm_bf16* h, uint8_t* hq,
+                                         uint8_t* h_scales, void* stream);
+
 /* Per-kernel GPU timing (per-op GPU timestamps, as in the op profiling of
  * "LLM Decode / Prefill 优化案例（Metal）", Step 1).  Arms two caller-owned
  * hipEvent_t handles for the next qmm_gemv / qmm_gemm / qmm_grouped_gemm /
  * qmm_grouped_gemm_swiglu / qmm_moe_combine / qmm_route / qmm_stream_read /
- * qmm_fp8_* / qmm_route_topk / qmm_moe_gather / qmm_norm_residual call on this
+ * qmm_fp8_* / qmm_route_topk / qmm_moe_gather / qmm_norm_residual / qmm_mxfp4_* call on this
  * thread: its kernels are launched with hipExtLaunchKernel so `start`
  * is stamped by the dispatch of its first kernel and `stop` by that of its last
  * (calls of several kernels: qmm_route, qmm_route_topk, qmm_gemm split along K), and their

@@ -1,0 +1,25 @@
+"""The generated-code checks on the sources of the microscaled 4-bit path (CPU only)."""
+import re
+
+import pytest
+
+import test_build
+
+SOURCES = ["qmm_mx4_quant.hip", "qmm_mx4_rows.hip"]
+
+
+@pytest.mark.slow
+@pytest.mark.parametrize("src", SOURCES)
+def test_no_packed_fp32_and_no_scratch(tmp_path, src):
+    text = test_build.device_asm(tmp_path, src).read_text()
+    assert not re.search(r"v_pk_(fma|mul|add)_f32", text)
+    for key in (".vgpr_spill_count", ".private_segment_fixed_size"):
+        got = re.findall(re.escape(key) + r":\s*(\d+)", text)
+        assert got and set(got) == {"0"}, key
+
+
+@pytest.mark.slow
+def test_products_use_the_scaled_fp4_instruction(tmp_path):
+    text = test_build.device_asm(tmp_path, "qmm_mx4_rows.hip").read_text()
+    ops = re.findall(r"v_mfma_\S+.*", text)
+    assert ops and all("v_mfma_scale_f32_16x16x128_f8f6f4" in o and "cbsz:4 blgp:4" in o for o in ops)
