@@ -41,6 +41,7 @@ struct Fp8TileArgs {
 struct Fp8Place {
   int64_t m0, m_end;
   int n0;
+  int expert;             // grouped, unless it is a bad one
   bool bad_expert;
   bool starts;            // the first rows of its segment
   const uint8_t* w;
@@ -128,6 +129,7 @@ __device__ __forceinline__ bool fp8_place(const Fp8TileArgs& a, Fp8Place& p) {
   int tt = in_strip / width;
   const int tn = 8 * strip + in_strip - tt * width;
   p.n0 = tn * kOut;
+  p.expert = 0;
   p.bad_expert = false;
   p.starts = false;
   p.w = a.w;
@@ -147,6 +149,7 @@ __device__ __forceinline__ bool fp8_place(const Fp8TileArgs& a, Fp8Place& p) {
       p.m_end = hi;
       const int e = a.seg_expert[s0 + s];
       p.bad_expert = e < 0 || e >= a.n_experts;
+      p.expert = e;
       if (!p.bad_expert) {
         p.w += int64_t(e) * a.n * a.d;
         p.ws += int64_t(e) * (GLU ? 2 * p.sb : (a.n + kFp8Block - 1) / kFp8Block) * a.nb;

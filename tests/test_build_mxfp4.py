@@ -4,8 +4,10 @@ import re
 import pytest
 
 import test_build
+import test_build_copy_waits
 
-SOURCES = ["qmm_mx4_quant.hip", "qmm_mx4_rows.hip"]
+SOURCES = ["qmm_mx4_quant.hip", "qmm_mx4_rows.hip", "qmm_mx4_tile.hip"]
+COPIES = ["qmm_mx4_rows.hip", "qmm_mx4_tile.hip"]
 
 
 @pytest.mark.slow
@@ -19,7 +21,15 @@ def test_no_packed_fp32_and_no_scratch(tmp_path, src):
 
 
 @pytest.mark.slow
-def test_products_use_the_scaled_fp4_instruction(tmp_path):
-    text = test_build.device_asm(tmp_path, "qmm_mx4_rows.hip").read_text()
+@pytest.mark.parametrize("src", COPIES)
+def test_copies_own_m0_and_have_their_wait_states(tmp_path, src):
+    test_build.test_lds_copy_asm_owns_m0(tmp_path, src)
+    test_build_copy_waits.test_copies_have_their_wait_states(tmp_path, src)
+
+
+@pytest.mark.slow
+@pytest.mark.parametrize("src", COPIES)
+def test_products_use_the_scaled_fp4_instruction(tmp_path, src):
+    text = test_build.device_asm(tmp_path, src).read_text()
     ops = re.findall(r"v_mfma_\S+.*", text)
     assert ops and all("v_mfma_scale_f32_16x16x128_f8f6f4" in o and "cbsz:4 blgp:4" in o for o in ops)
