@@ -23,7 +23,7 @@ __all__ = [
     "qmm_fp8_quant", "qmm_fp8_gemm", "qmm_fp8_grouped_gemm", "qmm_fp8_grouped_gemm_swiglu",
     "qmm_route_topk_workspace_bytes", "qmm_route_topk", "qmm_moe_gather", "qmm_norm_residual",
     "qmm_mxfp4_scale_bytes", "qmm_mxfp4_quant", "qmm_mxfp4_gemm", "qmm_mxfp4_grouped_gemm",
-    "qmm_mxfp4_grouped_gemm_swiglu", "QMM_MX_FLOOR", "QMM_MX_FIT",
+    "qmm_mxfp4_grouped_gemm_swiglu", "qmm_moe_layer_workspace_bytes", "qmm_moe_layer", "QMM_MX_FLOOR", "QMM_MX_FIT",
     "QMM_BF16", "QMM_F32", "QMM_SCORE_SOFTMAX", "QMM_SCORE_SIGMOID", "QMM_GROUP_MAX", "QMM_GROUP_TOP2",
 ]
 
@@ -56,7 +56,7 @@ EXPORTS = ("qmm_packed_bytes", "qmm_workspace_bytes", "qmm_pack", "qmm_unpack", 
            "qmm_set_kernel", "qmm_get_kernel", "qmm_fp8_quant", "qmm_fp8_gemm", "qmm_fp8_grouped_gemm",
            "qmm_fp8_grouped_gemm_swiglu", "qmm_route_topk_workspace_bytes", "qmm_route_topk",
            "qmm_moe_gather", "qmm_norm_residual", "qmm_mxfp4_scale_bytes", "qmm_mxfp4_quant", "qmm_mxfp4_gemm",
-           "qmm_mxfp4_grouped_gemm", "qmm_mxfp4_grouped_gemm_swiglu")
+           "qmm_mxfp4_grouped_gemm", "qmm_mxfp4_grouped_gemm_swiglu", "qmm_moe_layer_workspace_bytes", "qmm_moe_layer")
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _lib = None
@@ -131,6 +131,10 @@ def load():
                                                   vp]),
         "qmm_mxfp4_grouped_gemm_swiglu": (ctypes.c_int, [vp, i64, i32, i64, i64, vp, vp, i64, vp, vp, vp, i32, i32, i32,
                                                          ctypes.c_int, vp, vp, vp, vp]),
+        "qmm_moe_layer_workspace_bytes": (sz, [i64, i32, i64]),
+        "qmm_moe_layer": (ctypes.c_int, [ctypes.c_int, vp, i64, vp, i64, i32, i64, i64, vp, i64, vp, ctypes.c_int, i64,
+                                         ctypes.c_int, vp, i32, i32, ctypes.c_int, i32, i32, f32, vp, vp, vp, vp, vp,
+                                         sz, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -364,3 +368,16 @@ def qmm_mxfp4_grouped_gemm_swiglu(packed_stack, expert_stride_bytes, n_experts, 
                                                 _ptr(seg_offsets), n_seg, m_total, max_seg_rows, rule, _ptr(h),
                                                 _ptr(hq), _ptr(h_scales), _stream(stream)),
            "qmm_mxfp4_grouped_gemm_swiglu")
+
+
+def qmm_moe_layer_workspace_bytes(t: int, k: int, inter: int) -> int:
+    return int(load().qmm_moe_layer_workspace_bytes(t, k, inter))
+
+
+def qmm_moe_layer(fmt, gate_up, gate_up_stride_bytes, down, down_stride_bytes, n_experts, d, inter, x, t, logits, dtype,
+                  ld, score, bias, n_groups, keep_groups, group_score, k, renorm, scale, shared, topk, weights, out,
+                  ws=None, stream=None):
+    _check(load().qmm_moe_layer(fmt, _ptr(gate_up), gate_up_stride_bytes, _ptr(down), down_stride_bytes, n_experts, d,
+                                inter, _ptr(x), t, _ptr(logits), dtype, ld, score, _ptr(bias), n_groups, keep_groups,
+                                group_score, k, int(renorm), scale, _ptr(shared), _ptr(topk), _ptr(weights), _ptr(out),
+                                _ptr(ws), _nbytes(ws), _stream(stream)), "qmm_moe_layer")

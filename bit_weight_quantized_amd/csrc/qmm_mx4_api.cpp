@@ -1,9 +1,12 @@
-// C-ABI entry points of the microscaled 4-bit path: argument validation (host only,
+// C-ABI entry points of the microscaled 4-bit path and of the expert layer: argument validation (host only,
 // before any HIP call) and error mapping.  See include/qmm.h.
 #include <hip/hip_runtime.h>
 
 #include "qmm_internal.h"
+#include "qmm_moe_layer.h"
 #include "qmm_mx4.h"
+
+#include <math.h>
 
 namespace {
 
@@ -140,6 +143,61 @@ qmm_status qmm_mxfp4_grouped_gemm_swiglu(const void* packed_stack, int64_t exper
   if (!h && !hq) return api_fail(QMM_E_ARG, "no output asked for");
   const int err = qmm::launch_mx4_product(a, stream);
   return err ? api_hip_fail(err, "qmm_mxfp4_grouped_gemm_swiglu") : QMM_OK;
+}
+
+size_t qmm_moe_layer_workspace_bytes(int64_t t, int32_t k, int64_t inter) {
+  if (t < 1 || t > qmm::kLayerMaxTokens || k < 1 || k > qmm::kRouteMaxK || t * k > qmm::kLayerMaxPairs) return 0;
+  if (inter < 32 || inter > qmm::kMaxD || inter % 32) return 0;
+  return size_t(2 * t * k * inter);
+}
+
+qmm_status qmm_moe_layer(qmm_format f, const void* gate_up, int64_t gate_up_stride_bytes, const void* down,
+                         int64_t down_stride_bytes, int32_t n_experts, int64_t d, int64_t inter, const qmm_bf16* x,
+                         int64_t t, const void* logits, qmm_dtype dtype, int64_t ld, qmm_score score,
+                         const float* bias, int32_t n_groups, int32_t keep_groups, qmm_group_score group_score,
+                         int32_t k, int32_t renorm, float scale, const qmm_bf16* shared, int32_t* topk,
+                         float* weights, qmm_bf16* out, void* ws, size_t ws_bytes, void* stream) {
+  api_fail(QMM_OK, "");
+  if (f != QMM_MXFP4_G32)
+    return api_fail(f == QMM_AFFINE4_G64 ? QMM_E_UNSUPPORTED : QMM_E_ARG, "the expert layer takes QMM_MXFP4_G32 weights");
+  if (dtype != QMM_BF16 && dtype != QMM_F32) return api_fail(QMM_E_ARG, "unknown type of the logits");
+  if (score != QMM_SCORE_SOFTMAX && score != QMM_SCORE_SIGMOID) return api_fail(QMM_E_ARG, "unknown score");
+  if (group_score != QMM_GROUP_MAX && group_score != QMM_GROUP_TOP2) return api_fail(QMM_E_ARG, "unknown group score");
+  if (t < 0 || n_experts < 1 || k < 1) return api_fail(QMM_E_ARG, "t >= 0, n_experts >= 1 and k >= 1 required");
+  if (d < 1 || inter < 1) return api_fail(QMM_E_ARG, "d and inter must be >= 1");
+  if (d > qmm::kMaxD || d % 32 || inter > qmm::kMaxD || inter % 32)
+    return api_fail(QMM_E_SHAPE, "d and inter must be multiples of 32 and <= 65536");
+  qmm_status st = check_matrix(2 * inter, d);
+  if (st || (st = check_matrix(d, inter))) return st;
+  if (n_experts > qmm::kRouteMaxExperts) return api_fail(QMM_E_SHAPE, "n_experts must be <= 1024");
+  if (k > qmm::kRouteMaxK || k > n_experts) return api_fail(QMM_E_SHAPE, "k must be <= min(64, n_experts)");
+  if (n_groups < 1 || n_groups > 64 || n_experts % n_groups)
+    return api_fail(QMM_E_SHAPE, "n_groups must divide n_experts and be <= 64");
+  if (keep_groups < 1 || keep_groups > n_groups) return api_fail(QMM_E_ARG, "keep_groups must be in 1..n_groups");
+  if (ld < n_experts) return api_fail(QMM_E_ARG, "ld must be >= n_experts");
+  if (t > qmm::kLayerMaxTokens || t * k > qmm::kLayerMaxPairs) return api_fail(QMM_E_SHAPE, "t must be <= 16 and t*k <= 256");
+  if (!isfinite(scale)) return api_fail(QMM_E_ARG, "scale must be finite");
+  if (gate_up_stride_bytes < int64_t(qmm_packed_bytes(f, 2 * inter, d)) || gate_up_stride_bytes % 256 ||
+      down_stride_bytes < int64_t(qmm_packed_bytes(f, d, inter)) || down_stride_bytes % 256)
+    return api_fail(QMM_E_ARG, "the stride of a stack must be a multiple of 256 and >= qmm_packed_bytes()");
+  if (t == 0) return QMM_OK;
+  if (!gate_up || !down || !x || !logits || !topk || !weights || !out) return api_fail(QMM_E_ARG, "NULL pointer");
+  if (!aligned(gate_up, 256) || !aligned(down, 256)) return api_fail(QMM_E_ALIGN, "stacks must be 256-byte aligned");
+  if (!aligned(x, 16)) return api_fail(QMM_E_ALIGN, "x must be 16-byte aligned");
+  if (!aligned(shared, 8) || !aligned(out, 8)) return api_fail(QMM_E_ALIGN, "shared and out must be 8-byte aligned");
+  if (!aligned(logits, dtype == QMM_BF16 ? 2 : 4)) return api_fail(QMM_E_ALIGN, "logits must be aligned to their type");
+  if (!aligned(bias, 4) || !aligned(topk, 4) || !aligned(weights, 4))
+    return api_fail(QMM_E_ALIGN, "bias, topk and weights must be 4-byte aligned");
+  if (!ws || ws_bytes < qmm_moe_layer_workspace_bytes(t, k, inter))
+    return api_fail(QMM_E_WORKSPACE, "workspace NULL or smaller than qmm_moe_layer_workspace_bytes()");
+  if (!aligned(ws, 16)) return api_fail(QMM_E_ALIGN, "ws must be 16-byte aligned");
+  const qmm::MoeLayerArgs a{static_cast<const uint8_t*>(gate_up), gate_up_stride_bytes,
+                            static_cast<const uint8_t*>(down), down_stride_bytes, n_experts, int(d), int(inter), x,
+                            int(t), logits, dtype == QMM_BF16, ld, score == QMM_SCORE_SIGMOID, bias, n_groups,
+                            keep_groups, group_score == QMM_GROUP_TOP2, k, renorm != 0, scale, shared, topk, weights,
+                            out, static_cast<uint16_t*>(ws)};
+  const int err = qmm::launch_moe_layer(a, stream);
+  return err ? api_hip_fail(err, "qmm_moe_layer") : QMM_OK;
 }
 
 }  // extern "C"

@@ -544,14 +544,42 @@ qmm_status qmm_mxfp4_grouped_gemm_swiglu(const void* packed_stack, int64_t exper
                                          int32_t max_seg_rows, qmm_mx_rule rule, qmm_bf16* h, uint8_t* hq,
                                          uint8_t* h_scales, void* stream);
 
+/* Workspace of qmm_moe_layer in bytes: 2·t·k·inter (0 for invalid arguments).  Host only. */
+size_t qmm_moe_layer_workspace_bytes(int64_t t, int32_t k, int64_t inter);
+
+/* A mixture-of-experts layer for a few tokens, from the router's logits to the sum of the
+ * experts' outputs, in two launches, the weights packed MXFP4 and the activations bf16:
+ *   topk, weights   chosen and weighted as qmm_route_topk does: dtype, ld, score, bias,
+ *                   n_groups, keep_groups, group_score, k, renorm and scale as there
+ *   h[i][j]   = silu(G_e·x_i)·(U_e·x_i), e = topk[i][j], of fp32 sums, rounded once to bf16
+ *   out[i]    = sum_j weights[i][j]·(D_e·h[i][j]) + shared[i], in fp32, rounded once to bf16;
+ *               slots of -1 add nothing
+ *   gate_up   [n_experts] packed matrices [2·inter, d] (rows [0, inter) the gate G, then the
+ *             up projection U), down [n_experts] of [d, inter], at strides of bytes as for
+ *             qmm_grouped_gemm
+ *   x bf16[t][d], 16-byte aligned; shared bf16[t][d] or NULL (may be out) and out 8-byte
+ *   topk int32[t][k], weights fp32[t][k]: outputs
+ *   ws        qmm_moe_layer_workspace_bytes(t, k, inter) bytes, 16-byte aligned; calls on
+ *             different streams need one each
+ * Limits: t <= 16 and t·k <= 256; d and inter multiples of 32, <= 65536; one matrix's codes
+ * below 2 GiB; n_experts, k, n_groups as for qmm_route_topk.  t = 0 is a no-op.
+ * QMM_AFFINE4_G64 returns QMM_E_UNSUPPORTED.  The order of every sum depends on the shape and
+ * on which tokens choose which experts alone. */
+qmm_status qmm_moe_layer(qmm_format f, const void* gate_up, int64_t gate_up_stride_bytes, const void* down,
+                         int64_t down_stride_bytes, int32_t n_experts, int64_t d, int64_t inter, const qmm_bf16* x,
+                         int64_t t, const void* logits, qmm_dtype dtype, int64_t ld, qmm_score score,
+                         const float* bias, int32_t n_groups, int32_t keep_groups, qmm_group_score group_score,
+                         int32_t k, int32_t renorm, float scale, const qmm_bf16* shared, int32_t* topk,
+                         float* weights, qmm_bf16* out, void* ws, size_t ws_bytes, void* stream);
+
 /* Per-kernel GPU timing (per-op GPU timestamps, as in the op profiling of
  * "LLM Decode / Prefill 优化案例（Metal）", Step 1).  Arms two caller-owned
  * hipEvent_t handles for the next qmm_gemv / qmm_gemm / qmm_grouped_gemm /
  * qmm_grouped_gemm_swiglu / qmm_moe_combine / qmm_route / qmm_stream_read /
- * qmm_fp8_* / qmm_route_topk / qmm_moe_gather / qmm_norm_residual / qmm_mxfp4_* call on this
- * thread: its kernels are launched with hipExtLaunchKernel so `start`
+ * qmm_fp8_* / qmm_route_topk / qmm_moe_gather / qmm_norm_residual / qmm_mxfp4_* / qmm_moe_layer call
+ * on this thread: its kernels are launched with hipExtLaunchKernel so `start`
  * is stamped by the dispatch of its first kernel and `stop` by that of its last
- * (calls of several kernels: qmm_route, qmm_route_topk, qmm_gemm split along K), and their
+ * (calls of several kernels: qmm_route, qmm_route_topk, qmm_moe_layer, qmm_gemm split along K), and their
  * elapsed time is the call's execution time.  Either may be NULL.  The arming
  * is consumed by that next call; a call rejected by validation leaves it armed. */
 qmm_status qmm_profile_next(void* start_event, void* stop_event);

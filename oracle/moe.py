@@ -1,0 +1,40 @@
+"""A mixture-of-experts layer for given choices in fp64, with what fp32 sums and bf16
+intermediates may be off by."""
+import numpy as np
+
+from .mxfp4 import swiglu
+
+STEP = 2.0 ** -23
+
+
+def product(x, tol_x, w):
+    """(x @ w.T, its error bound): x off by tol_x, and a sum in fp32 in which a term goes
+    through at most 32 additions in the matrix instruction that reads it, one for each 32
+    codes after it, and 16 in the joining of parts; each loses at most 2^-23 of the sum of the
+    magnitudes (products of a weight's 2 and a bf16's 8 bits are exact)."""
+    a = (np.abs(x) + tol_x) @ np.abs(w).T
+    return x @ w.T, tol_x @ np.abs(w).T + (32 + x.shape[1] / 32 + 16) * STEP * a
+
+
+def layer(x, gate_up, down, ids, weights, shared):
+    """(out, tolerance of the bf16 output): gate_up[e] and down[e] dequantised matrices, ids
+    [t][k] (-1: none), weights [t][k]."""
+    t, d = x.shape
+    out, tol, mag = np.zeros((t, d)), np.zeros((t, d)), np.zeros((t, d))
+    for i in range(t):
+        for j, e in enumerate(ids[i]):
+            if e < 0:
+                continue
+            half = gate_up[e].shape[0] // 2
+            s, ts = product(x[i:i + 1], np.zeros((1, d)), gate_up[e])
+            h, th = swiglu(s[:, :half], s[:, half:], ts[:, :half], ts[:, half:])
+            th = th + 2.0 ** -8 * (np.abs(h) + th) + 2.0 ** -133     # rounded to bf16
+            y, ty = product(h, th, down[e])
+            out[i] += weights[i, j] * y[0]
+            tol[i] += abs(weights[i, j]) * ty[0]
+            mag[i] += abs(weights[i, j]) * (np.abs(y[0]) + ty[0])
+    if shared is not None:
+        out, mag = out + shared, mag + np.abs(shared)
+    # every expert's product with its weight, the sum over experts, parts, waves and shared
+    tol = tol + (ids.shape[1] + 20) * STEP * mag
+    return out, 2.0 ** -8 * (np.abs(out) + tol) + tol + 2.0 ** -133

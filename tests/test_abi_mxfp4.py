@@ -113,3 +113,70 @@ def test_grouped_refusals(glu):
         expect(E_ALIGN, f, *with_(14, P + 1))
     f(*with_(11, 0), stream=0)
     f(*with_(12, 0), stream=0)
+
+
+def test_moe_layer_workspace():
+    f = qmm.qmm_moe_layer_workspace_bytes
+    assert f(1, 8, 2048) == 2 * 8 * 2048 and f(16, 16, 32) == 2 * 256 * 32
+    assert [f(0, 1, 32), f(17, 1, 32), f(1, 65, 32), f(16, 17, 32), f(1, 0, 32), f(1, 1, 33), f(1, 1, 65568)] == [0] * 7
+
+
+def test_moe_layer_refusals():
+    f = qmm.qmm_moe_layer
+    d, inter, ne, t, k = 128, 64, 8, 4, 2
+    gu, dn = qmm.qmm_packed_bytes(qmm.QMM_MXFP4_G32, 2 * inter, d), qmm.qmm_packed_bytes(qmm.QMM_MXFP4_G32, d, inter)
+    # 0 fmt, 1 gate_up, 2 stride, 3 down, 4 stride, 5 n_experts, 6 d, 7 inter, 8 x, 9 t, 10 logits, 11 dtype, 12 ld,
+    # 13 score, 14 bias, 15 n_groups, 16 keep, 17 group score, 18 k, 19 renorm, 20 scale, 21 shared, 22 topk,
+    # 23 weights, 24 out, 25 ws
+    class Ws:
+        def __init__(self, at, n):
+            self.at, self.n = at, n
+
+        def data_ptr(self):
+            return self.at
+
+        def numel(self):
+            return self.n
+
+        def element_size(self):
+            return 1
+    need = qmm.qmm_moe_layer_workspace_bytes(t, k, inter)
+    with_ = changer([qmm.QMM_MXFP4_G32, P, gu, P, dn, ne, d, inter, P, t, P, qmm.QMM_F32, ne, 0, None, 1, 1, 0, k, 1, 1.0,
+                     None, P, P, P, Ws(P, need)])
+    expect(E_UNSUPPORTED, f, *with_(0, qmm.QMM_AFFINE4_G64))
+    expect(E_ARG, f, *with_(0, 7))
+    for i in (1, 3, 8, 10, 22, 23, 24):
+        expect(E_ARG, f, *with_(i, None))
+    expect(E_ARG, f, *with_(2, gu - 256))
+    expect(E_ARG, f, *with_(2, gu + 64))
+    expect(E_ARG, f, *with_(4, dn - 256))
+    expect(E_ARG, f, *with_(4, dn + 64))
+    expect(E_ARG, f, *with_(5, 0))
+    expect(E_SHAPE, f, *with_(5, 1025, 12, 1025))
+    for i in (6, 7):
+        expect(E_ARG, f, *with_(i, 0))
+        expect(E_SHAPE, f, *with_(i, 48))
+        expect(E_SHAPE, f, *with_(i, 65568))
+    expect(E_SHAPE, f, *with_(6, 65536, 7, 65536))            # 4 GiB of codes
+    expect(E_ARG, f, *with_(9, -1))
+    expect(E_SHAPE, f, *with_(9, 17))
+    expect(E_SHAPE, f, *with_(9, 16, 18, 17, 5, 32, 12, 32))  # 272 pairs
+    expect(E_ARG, f, *with_(11, 3))
+    expect(E_ARG, f, *with_(12, ne - 1))
+    expect(E_ARG, f, *with_(13, 2))
+    expect(E_SHAPE, f, *with_(15, 3))
+    expect(E_SHAPE, f, *with_(15, 0))
+    expect(E_ARG, f, *with_(15, 4, 16, 5))
+    expect(E_ARG, f, *with_(16, 0))
+    expect(E_ARG, f, *with_(17, 2))
+    expect(E_ARG, f, *with_(18, 0))
+    expect(E_SHAPE, f, *with_(18, 9))
+    expect(E_SHAPE, f, *with_(18, 65, 5, 128, 12, 128, 9, 1))
+    expect(E_ARG, f, *with_(20, float("inf")))
+    expect(E_ARG, f, *with_(20, float("nan")))
+    for i, off in ((1, 128), (3, 128), (8, 8), (10, 2), (14, 2), (21, 4), (22, 2), (23, 2), (24, 4)):
+        expect(E_ALIGN, f, *with_(i, P + off))
+    expect(E_WS, f, *with_(25, None))
+    expect(E_WS, f, *with_(25, Ws(P, need - 1)))
+    expect(E_ALIGN, f, *with_(25, Ws(P + 8, need)))
+    f(*with_(9, 0, 1, None, 8, None, 25, None), stream=0)
