@@ -32,7 +32,8 @@ struct MoeLayerArgs {
   int32_t* topk;            // [t][k]
   float* weights;           // [t][k]
   uint16_t* out;            // [t][d]
-  uint16_t* h;              // [t·k][inter], the workspace
+  uint16_t* h;              // [t·k][inter], the workspace: by expert, then token
+  int cols;                 // columns of a workgroup in the second kernel, even, <= 16; set by the launch
 };
 int launch_moe_layer(const MoeLayerArgs& a, void* stream);
 

@@ -38,55 +38,98 @@ namespace {
 
 constexpr int kLayerWaves = 8;
 constexpr int kLayerRing = 18 * 1024;     // a wave's ring
+constexpr int kRowKinds = 5;              // groups of up to 1, 2, 4, 8 or 16 rows
 
 struct LayerTables {
   int32_t ids[kLayerMaxPairs];            // experts of the pairs (token, choice), -1: none
-  float weights[kLayerMaxPairs];
-  uint32_t bits[kRouteMaxExperts / 32];   // chosen experts
-  uint16_t pairs[kLayerMaxPairs];         // by expert, then token
-  uint16_t expert[kLayerMaxPairs];        // the chosen ones, ascending
-  uint16_t first[kLayerMaxPairs + 2];     // where an expert's pairs begin
-  int32_t count, most;                    // chosen experts; most tokens of one
+  float weights[kLayerMaxPairs];          // of the pairs
+  // "rows" are the pairs with an expert, by expert, then token
+  float row_weight[kLayerMaxPairs];
+  uint8_t token[kLayerMaxPairs];          // of the rows
+  uint16_t expert[kLayerMaxPairs];        // of the groups
+  uint16_t first[kLayerMaxPairs + 2];     // a group's first row
+  uint32_t sums[2][kLayerWaves];
+  int32_t groups, kind;                   // groups, of up to 1 << kind rows
 };
 constexpr int kLayerRed = kLayerWaves * kLayerRing;                    // the waves' sums
 constexpr int kLayerTables = kLayerRed + kLayerWaves * 1024;
 constexpr int kLayerLds = kLayerTables + int(sizeof(LayerTables));
 static_assert(kLayerLds <= 160 * 1024, "LDS");
 
-// The tables from ids, by a thread for each pair; every thread of the workgroup calls it.
-__device__ __forceinline__ void make_tables(LayerTables& T, int pairs) {
-  const int tid = threadIdx.x;
-  if (tid < kRouteMaxExperts / 32) T.bits[tid] = 0u;
-  if (tid == 0) T.most = 0;
+// Inclusive sums of a wave's lanes.
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);   // row_shr:1, 2, 4, 8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);   // row_bcast:15, 31
+  return v + __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);
+}
+
+// The tables from ids; every thread of the workgroup calls it.  An expert's rows are taken in
+// groups of up to 1 << kind, each of which reads the expert's weights: the fewer rows a step
+// of the ring holds, the more steps it has.  `tokens` is scratch for n_experts words: which
+// tokens an expert has, a bit each, and its first row in the upper half.  Thread i counts for
+// experts 2i and 2i + 1; the counts of all kinds go through one scan, 10 bits each.
+__device__ __forceinline__ void make_tables(LayerTables& T, uint32_t* tokens, int pairs, int k, int ne) {
+  static_assert(kRouteMaxExperts <= 2 * 64 * kLayerWaves, "a thread has two experts");
+  const int tid = threadIdx.x, wave = tid >> 6;
+  for (int e = tid; e < ne; e += 64 * kLayerWaves) tokens[e] = 0u;
   __syncthreads();
-  const int e = tid < pairs ? T.ids[tid] : -1;
-  if (e >= 0) atomicOr(&T.bits[e >> 5], 1u << (e & 31));
+  const int id = tid < pairs ? T.ids[tid] : -1, tok = tid / k;
+  if (id >= 0) atomicOr(&tokens[id], 1u << tok);
   __syncthreads();
-  int before = 0, same = 0, all = 0, valid = 0;   // pairs that come before, of this expert before and at all
-  for (int q = 0; q < pairs; ++q) {
-    const int o = T.ids[q];
-    before += o >= 0 && (o < e || (o == e && q < tid)) ? 1 : 0;
-    same += o == e && q < tid ? 1 : 0;
-    all += o == e ? 1 : 0;
-    valid += o >= 0 ? 1 : 0;
+  uint32_t mask[2], a = 0, b = 0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    mask[i] = 2 * tid + i < ne ? tokens[2 * tid + i] : 0u;
+    const uint32_t r = __builtin_popcount(mask[i]);
+    a += r | (r + 1) / 2 << 10 | (r + 3) / 4 << 20;
+    b += (r + 7) / 8 | (r + 15) / 16 << 10;
   }
-  int rank = 0, count = 0;
-  for (int w = 0; w < kRouteMaxExperts / 32; ++w) {
-    const uint32_t b = T.bits[w];
-    count += __builtin_popcount(b);
-    rank += w < e >> 5 ? __builtin_popcount(b) : w == e >> 5 ? __builtin_popcount(b & ((1u << (e & 31)) - 1u)) : 0;
+  const uint32_t as = wave_scan(a), bs = wave_scan(b);
+  if ((tid & 63) == 63) {
+    T.sums[0][wave] = as;
+    T.sums[1][wave] = bs;
   }
-  if (e >= 0) {
-    T.pairs[before] = uint16_t(tid);
-    if (same == 0) {
-      T.expert[rank] = uint16_t(e);
-      T.first[rank] = uint16_t(before);
-      atomicMax(&T.most, all);
+  __syncthreads();
+  uint32_t at_a = as - a, at_b = bs - b, all_a = 0, all_b = 0;
+#pragma unroll
+  for (int w = 0; w < kLayerWaves; ++w) {
+    const uint32_t sa = T.sums[0][w], sb = T.sums[1][w];
+    at_a += w < wave ? sa : 0u;
+    at_b += w < wave ? sb : 0u;
+    all_a += sa;
+    all_b += sb;
+  }
+  auto of = [](int kind, uint32_t u, uint32_t v) {
+    return int((kind == 0 ? u : kind == 1 ? u >> 10 : kind == 2 ? u >> 20 : kind == 3 ? v : v >> 10) & 1023u);
+  };
+  const int most = of(4, all_a, all_b);           // chosen experts
+  int kind = 0;
+  while (kind < kRowKinds - 1 && 4 * of(kind, all_a, all_b) > 5 * most) ++kind;
+  int at = of(kind, at_a, at_b), row = of(0, at_a, at_b);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = __builtin_popcount(mask[i]);
+    if (r) tokens[2 * tid + i] = mask[i] | uint32_t(row) << 16;
+    for (int q = 0; q < r; q += 1 << kind) {
+      T.expert[at] = uint16_t(2 * tid + i);
+      T.first[at++] = uint16_t(row + q);
     }
+    row += r;
   }
   if (tid == 0) {
-    T.count = count;
-    T.first[count] = uint16_t(valid);
+    T.groups = of(kind, all_a, all_b);
+    T.kind = kind;
+    T.first[T.groups] = uint16_t(of(0, all_a, all_b));
+  }
+  __syncthreads();
+  if (id >= 0) {
+    const uint32_t m = tokens[id];
+    const int r = int(m >> 16) + __builtin_popcount(m & 0xffffu & ((1u << tok) - 1u));
+    T.token[r] = uint8_t(tok);
+    T.row_weight[r] = T.weights[tid];
   }
   __syncthreads();
 }
@@ -118,15 +161,17 @@ __device__ __forceinline__ void choose(const MoeLayerArgs& a, int tok, float* mi
 // are then in different banks.
 __device__ __forceinline__ int spread(int row) { return (row & 7) | ((row >> 3 ^ row >> 2) & 1) << 3; }
 
-// The steps of a wave.  AC copies of 4 activation rows a step.
-template <bool DOWN, int AC>
+// The steps of a wave, groups of up to ROWS tokens.
+template <bool DOWN, int ROWS>
 __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds, LayerTables& T) {
-  constexpr int kStage = 1024 + 1024 * AC + 256, D = kLayerRing / kStage, kOps = 2 + AC;
+  // rows of 256 bytes: one or two in copies of 4 bytes a lane, else four in one of 16
+  constexpr int kCopies = ROWS <= 2 ? ROWS : ROWS / 4, kOps = 2 + kCopies;
+  constexpr int kMetaAt = 1024 + 256 * ROWS, kStage = kMetaAt + 256, D = kLayerRing / kStage;
   static_assert((D - 1) * kOps <= 63, "the waits count the copies in flight");
   const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int axis = DOWN ? a.inter : a.d, n = DOWN ? a.d : 2 * a.inter;
-  const int steps = (axis + 127) / 128, nd = __builtin_amdgcn_readfirstlane(T.count);
+  const int steps = (axis + 127) / 128, groups = __builtin_amdgcn_readfirstlane(T.groups);
   const Slabs L{n, axis, QMM_MXFP4_G32};
   const int last = L.count() - 1;
   const uint32_t width = uint32_t(L.width(0) / 2), width_last = uint32_t(L.width(last) / 2);
@@ -141,82 +186,91 @@ __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds
   unsigned char* ring = lds + wave * kLayerRing;
   const uint32_t ring_at = lds_addr(ring);
 
-  // Tasks.  First kernel: an expert and 8 outputs, dealt out to all waves of the grid, those of
-  // a CU far apart.  Second: for each block of 16 columns of the workgroup all experts, each in
-  // `parts` parts, so that the waves have like shares.
-  const int blocks = DOWN ? a.d / 16 : a.inter / 8;
-  int parts = 1;
-  if (DOWN)
-    while (2 * parts <= min(8, steps) && (nd * parts + 7) / 8 * 8 * 20 > 23 * nd * parts) parts *= 2;
+  // Pieces of work.  First kernel: up to 8 outputs of a group, as many as give all waves of the
+  // grid as many pieces, dealt out in turn.  Second: a wave has an even share, in a row, of the
+  // (group, step) of a block of columns; a piece is its steps of a group.
+  const int waves = kLayerWaves * int(gridDim.x), me = wave * int(gridDim.x) + int(blockIdx.x);
+  int outputs = 8;
+  if (!DOWN) {
+    const int turns = (groups * (a.inter / 8) + waves - 1) / waves;
+    outputs = max(1, (groups * a.inter + turns * waves - 1) / max(turns * waves, 1));
+    while (outputs < 8 && groups * ((a.inter + outputs - 1) / outputs) > turns * waves) ++outputs;
+  }
+  const int of_group = DOWN ? steps : (a.inter + outputs - 1) / outputs;
+  const int work = groups * of_group;
+  const int begin = DOWN ? work * wave / kLayerWaves : me, end = DOWN ? work * (wave + 1) / kLayerWaves : work;
+  const int blocks = DOWN ? (a.d + a.cols - 1) / a.cols : 0;
   const int rounds = DOWN ? (blocks - int(blockIdx.x) + int(gridDim.x) - 1) / int(gridDim.x) : 1;
-  const int of_round = DOWN ? nd * parts : nd * blocks, stride_of = DOWN ? kLayerWaves : kLayerWaves * int(gridDim.x);
-  const int begin = DOWN ? wave : wave * int(gridDim.x) + int(blockIdx.x);
-  struct Task {
-    int j, block, from, to;
+  struct Piece {
+    int j, at, size, next;    // group, first output or step in it, outputs or steps; what follows
   };
-  auto task_of = [&](int round, int i) {
+  auto piece_at = [&](int pos) {
+    const int j = pos / of_group, at = pos - j * of_group;
     if (DOWN) {
-      const int j = i / parts, p = i - j * parts;
-      return Task{j, int(blockIdx.x) + round * int(gridDim.x), steps * p / parts, steps * (p + 1) / parts};
+      const int size = min(end - pos, of_group - at);
+      return Piece{j, at, size, pos + size};
     }
-    const int j = i / blocks;
-    return Task{j, i - j * blocks, 0, steps};
+    return Piece{j, at * outputs, min(outputs, a.inter - at * outputs), pos + waves};
   };
 
   // ---- the copies' place in the sequence
   const int wrow = lane >> 2, wpiece = (lane & 3) ^ (wrow >> 1 & 3);
-  int c_round = 0, c_task = begin, c_h = 0, c_to = 0;
+  int c_round = 0, c_pos = begin, c_h = 0, c_to = 0;
   __amdgpu_buffer_rsrc_t cr = make_rsrc(stack, 0), mr = cr;
-  uint32_t w_full = 0, w_last = 0, m_full = 0, m_last = 0, aoff[AC];
+  uint32_t w_full = 0, w_last = 0, m_full = 0, m_last = 0, aoff[kCopies];
 #pragma unroll
-  for (int i = 0; i < AC; ++i) aoff[i] = kOOB8;
-  auto packed_row = [&](int block, int row) {
-    return DOWN ? 16 * block + row : 8 * block + (row & 7) + (row >= 8 ? a.inter : 0);
-  };
+  for (int i = 0; i < kCopies; ++i) aoff[i] = kOOB8;
+  auto copied_row = [&](int i) { return ROWS <= 2 ? i : 4 * i + (lane >> 4); };
+  auto copied_at = [&](int i) { return ROWS <= 2 ? 2 * lane : 8 * ((lane & 15) ^ spread(copied_row(i))); };   // code
   auto open = [&]() {
-    const Task t = task_of(c_round, c_task);
+    const Piece t = piece_at(c_pos);
     int e = __builtin_amdgcn_readfirstlane(T.expert[t.j]), at = __builtin_amdgcn_readfirstlane(T.first[t.j]);
-    int end = __builtin_amdgcn_readfirstlane(T.first[t.j + 1]);
+    int stop = __builtin_amdgcn_readfirstlane(T.first[t.j + 1]);
     // wait states between these, which vector instructions write, and the copies that read what follows from them
-    asm volatile("s_nop 4" : "+s"(e), "+s"(at), "+s"(end));
+    asm volatile("s_nop 4" : "+s"(e), "+s"(at), "+s"(stop));
     const uint8_t* blob = stack + int64_t(e) * stride;
     cr = make_rsrc(blob + kHeaderBytes, codes_bytes);
     mr = make_rsrc(blob + meta_offset, meta_bytes);
-    const uint32_t row = uint32_t(packed_row(t.block, wrow)), row_m = uint32_t(packed_row(t.block, c));
-    w_full = row * width + 16u * uint32_t(wpiece);
-    w_last = row * width_last + 16u * uint32_t(wpiece);
-    m_full = lane < 16 ? (row_m >> 2) * mquad + (row_m & 3u) * mrow : kOOB8;
-    m_last = lane < 16 ? (row_m >> 2) * mquad + (row_m & 3u) * mrow_last : kOOB8;
+    // row r of the 16: columns of the block, or 8 outputs' gate rows and their up rows
+    const int column = (int(blockIdx.x) + c_round * int(gridDim.x)) * a.cols;
+    const int rows = DOWN ? min(a.cols, a.d - column) : t.size;
+    auto row = [&](int r) { return uint32_t(DOWN ? column + r : t.at + (r & 7) + (r >= 8 ? a.inter : 0)); };
+    auto any = [&](int r) { return (DOWN ? r : r & 7) < rows; };
+    w_full = any(wrow) ? row(wrow) * width + 16u * uint32_t(wpiece) : kOOB8;
+    w_last = any(wrow) ? row(wrow) * width_last + 16u * uint32_t(wpiece) : kOOB8;
+    m_full = lane < 16 && any(c) ? (row(c) >> 2) * mquad + (row(c) & 3u) * mrow : kOOB8;
+    m_last = lane < 16 && any(c) ? (row(c) >> 2) * mquad + (row(c) & 3u) * mrow_last : kOOB8;
 #pragma unroll
-    for (int i = 0; i < AC; ++i) {
-      const int r = 4 * i + (lane >> 4), p = T.pairs[min(at + r, kLayerMaxPairs - 1)];
-      aoff[i] = at + r < end ? uint32_t(DOWN ? p : p / a.k) * row_bytes + 16u * uint32_t((lane & 15) ^ spread(r)) : kOOB8;
+    for (int i = 0; i < kCopies; ++i) {
+      const int r = at + copied_row(i), q = min(r, kLayerMaxPairs - 1);
+      aoff[i] = r < stop ? uint32_t(DOWN ? q : T.token[q]) * row_bytes + 2u * uint32_t(copied_at(i)) : kOOB8;
     }
-    c_h = t.from;
-    c_to = t.to;
+    c_h = DOWN ? t.at : 0;
+    c_to = DOWN ? t.at + t.size : steps;
+    c_pos = t.next;
   };
+  bool more = rounds > 0 && begin < end;
   auto copies = [&](int stage) {
-    const bool in = c_round < rounds && c_task < of_round;
     const int h = c_h, s = h >> 2;
-    const uint32_t at = ring_at + uint32_t(stage * kStage), none = in ? 0u : kOOB8;
+    const uint32_t at = ring_at + uint32_t(stage * kStage), none = more ? 0u : kOOB8;
     copy16_to_lds_from(cr, (s == last ? w_last : w_full) | none | (128 * h + 32 * wpiece < axis ? 0u : kOOB8),
-                       in ? uint32_t(s) * slab_bytes + 64u * uint32_t(h & 3) : 0u, at);
+                       more ? uint32_t(s) * slab_bytes + 64u * uint32_t(h & 3) : 0u, at);
 #pragma unroll
-    for (int i = 0; i < AC; ++i)
-      copy16_to_lds_from(ar, aoff[i] | none | (128 * h + 8 * ((lane & 15) ^ spread(4 * i + (lane >> 4))) < axis ? 0u : kOOB8),
-                         in ? 256u * uint32_t(h) : 0u, at + 1024u + 1024u * uint32_t(i));
-    copy4_to_lds(mr, ((s == last ? m_last : m_full) + 64u * uint32_t(s) + 4u * uint32_t(h & 3)) | none,
-                 at + 1024u + 1024u * AC);
-    if (in && ++c_h == c_to) {
-      c_task += stride_of;
-      if (c_task >= of_round) {
-        c_task = begin;
-        ++c_round;
+    for (int i = 0; i < kCopies; ++i) {
+      const uint32_t from = aoff[i] | none | (128 * h + copied_at(i) < axis ? 0u : kOOB8);
+      if (ROWS <= 2) copy4_to_lds(ar, from + (more ? 256u * uint32_t(h) : 0u), at + 1024u + 256u * uint32_t(i));
+      else copy16_to_lds_from(ar, from, more ? 256u * uint32_t(h) : 0u, at + 1024u + 1024u * uint32_t(i));
+    }
+    copy4_to_lds(mr, ((s == last ? m_last : m_full) + 64u * uint32_t(s) + 4u * uint32_t(h & 3)) | none, at + kMetaAt);
+    if (more && ++c_h == c_to) {
+      if (c_pos >= end) {
+        c_pos = begin;
+        more = ++c_round < rounds;
       }
-      if (c_round < rounds && c_task < of_round) open();
+      if (more) open();
     }
   };
-  if (rounds > 0 && begin < of_round) open();
+  if (more) open();
 #pragma unroll 1
   for (int i = 0; i < D; ++i) copies(i);
 
@@ -224,31 +278,32 @@ __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds
   f32x4_t* red = reinterpret_cast<f32x4_t*>(lds + kLayerRed);
   for (int round = 0; round < rounds; ++round) {
     f32x4_t sum = {0.f, 0.f, 0.f, 0.f};           // token c, columns 4g .. 4g + 3
-    for (int i = begin; i < of_round; i += stride_of) {
-      const Task t = task_of(round, i);
+    for (int pos = begin; pos < end;) {
+      const Piece t = piece_at(pos);
+      pos = t.next;
       const int at = T.first[t.j], rows = T.first[t.j + 1] - at;
-      // the lane's pair, and its row in LDS: the c-th of the expert's, or token c's
-      int row = min(c, rows - 1), pair = -1;
+      // the lane's row in LDS, in the second kernel its token's; whether it has one
+      int row = min(c, rows - 1);
+      bool has = c < rows;
       if (DOWN) {
         row = 0;
-        for (int r = 0; r < rows; ++r) {
-          const int p = T.pairs[at + r];
-          if (p / a.k == c) {
+        has = false;
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r)
+          if (r < rows && T.token[at + r] == c) {
             row = r;
-            pair = p;
+            has = true;
           }
-        }
-      } else if (c < rows) {
-        pair = T.pairs[at + c];
       }
       const uint32_t a_at = 1024u + 256u * uint32_t(row);
-      const int x0 = spread(row);
+      const int x0 = ROWS <= 2 ? 0 : spread(row);
       f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-      for (int h = t.from; h < t.to; ++h) {
+      const int n_steps = DOWN ? t.size : steps;
+      for (int h = 0; h < n_steps; ++h) {
         wait_copies<(D - 1) * kOps>();
         const unsigned char* st = ring + stage * kStage;
         const u32x4_t w = *reinterpret_cast<const u32x4_t*>(st + 64 * c + 16 * (g ^ (c >> 1 & 3)));
-        const uint32_t e8 = st[1024 + 1024 * AC + 4 * c + g];
+        const uint32_t e8 = st[kMetaAt + 4 * c + g];
         u32x4_t b[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const u32x4_t*>(st + a_at + 16 * ((4 * g + j) ^ x0));
@@ -262,18 +317,18 @@ __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds
                                                         __builtin_bit_cast(bf16x8_t, b[j]), acc, 0, 0, 0);
       }
       if (DOWN) {
-        const float weight = pair >= 0 ? T.weights[pair] : 0.f;
-        if (pair >= 0)
+        if (has) {
+          const float weight = T.row_weight[at + row];
 #pragma unroll
           for (int e = 0; e < 4; ++e) sum[e] = __builtin_fmaf(weight, acc[e], sum[e]);
+        }
       } else {
         // gate rows in the lanes with g < 2, the same outputs' up rows 32 lanes on
-        float v[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = silu(acc[e]) * __shfl_xor(acc[e], 32);
-        if (g < 2 && pair >= 0)
-          *reinterpret_cast<u32x2_t*>(a.h + int64_t(pair) * a.inter + 8 * t.block + 4 * g) =
-              u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+        for (int e = 0; e < 4; ++e) {
+          const float v = silu(acc[e]) * __shfl_xor(acc[e], 32);
+          if (has && g < 2 && 4 * g + e < t.size) a.h[int64_t(at + row) * a.inter + t.at + 4 * g + e] = uint16_t(pack_bf16x2(v, v));
+        }
       }
     }
     if (DOWN) {
@@ -283,12 +338,15 @@ __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds
       if (wave == 0 && c < a.t) {
 #pragma unroll
         for (int w = 1; w < kLayerWaves; ++w) sum += red[64 * w + lane];
-        const int64_t o = int64_t(c) * a.d + 16 * (int(blockIdx.x) + round * int(gridDim.x)) + 4 * g;
-        if (a.shared) {
-          const u32x2_t v = *reinterpret_cast<const u32x2_t*>(a.shared + o);
-          sum += f32x4_t{bf16_lo(v[0]), bf16_hi(v[0]), bf16_lo(v[1]), bf16_hi(v[1])};
+        const int column = (int(blockIdx.x) + round * int(gridDim.x)) * a.cols, cols = min(a.cols, a.d - column);
+#pragma unroll
+        for (int e = 0; e < 4; e += 2) {
+          if (4 * g + e >= cols) continue;
+          const int64_t o = int64_t(c) * a.d + column + 4 * g + e;
+          uint32_t v = 0;
+          if (a.shared) v = *reinterpret_cast<const uint32_t*>(a.shared + o);
+          *reinterpret_cast<uint32_t*>(a.out + o) = pack_bf16x2(sum[e] + bf16_lo(v), sum[e + 1] + bf16_hi(v));
         }
-        *reinterpret_cast<u32x2_t*>(a.out + o) = u32x2_t{pack_bf16x2(sum[0], sum[1]), pack_bf16x2(sum[2], sum[3])};
       }
       wait_reads();
       phase_end();                                // the next columns' sums take the place
@@ -299,10 +357,12 @@ __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds
 
 template <bool DOWN>
 __device__ __forceinline__ void stream_any(const MoeLayerArgs& a, unsigned char* lds, LayerTables& T) {
-  const int most = __builtin_amdgcn_readfirstlane(T.most);
-  if (most <= 4) stream<DOWN, 1>(a, lds, T);
-  else if (most <= 8) stream<DOWN, 2>(a, lds, T);
-  else stream<DOWN, 4>(a, lds, T);
+  const int kind = __builtin_amdgcn_readfirstlane(T.kind);
+  if (kind == 0) stream<DOWN, 1>(a, lds, T);
+  else if (kind == 1) stream<DOWN, 2>(a, lds, T);
+  else if (kind == 2) stream<DOWN, 4>(a, lds, T);
+  else if (kind == 3) stream<DOWN, 8>(a, lds, T);
+  else stream<DOWN, 16>(a, lds, T);
 }
 
 __global__ __launch_bounds__(64 * kLayerWaves) void layer_gate_up_kernel(MoeLayerArgs a) {
@@ -325,7 +385,7 @@ __global__ __launch_bounds__(64 * kLayerWaves) void layer_gate_up_kernel(MoeLaye
     a.topk[tid] = T.ids[tid];
     a.weights[tid] = T.weights[tid];
   }
-  make_tables(T, pairs);
+  make_tables(T, reinterpret_cast<uint32_t*>(lds), pairs, a.k, a.n_experts);
   stream_any<false>(a, lds, T);
 }
 
@@ -338,24 +398,29 @@ __global__ __launch_bounds__(64 * kLayerWaves) void layer_down_kernel(MoeLayerAr
     T.ids[tid] = e >= 0 && e < a.n_experts ? e : -1;
     T.weights[tid] = a.weights[tid];
   }
-  make_tables(T, pairs);
+  make_tables(T, reinterpret_cast<uint32_t*>(lds), pairs, a.k, a.n_experts);
   stream_any<true>(a, lds, T);
 }
 
 }  // namespace
 
-int launch_moe_layer(const MoeLayerArgs& a, void* stream) {
+int launch_moe_layer(const MoeLayerArgs& args, void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
   DevInfo di{};
   const int cus = device_info(&di) == 0 && di.cus > 0 ? di.cus : 256;
+  MoeLayerArgs a = args;
+  // columns of a workgroup: as many as give every CU the same number of blocks
+  const int rounds = (a.d + 16 * cus - 1) / (16 * cus);
+  a.cols = std::max(8, (a.d + 2 * cus * rounds - 1) / (2 * cus * rounds) * 2);
+  const int64_t outputs = int64_t(a.t) * a.k * a.inter;
+  const int blocks = (a.d + a.cols - 1) / a.cols;
+  const dim3 block(64 * kLayerWaves), up_grid(unsigned(std::min<int64_t>(cus, (outputs + 31) / 32)));
   const ProfileEvents pe = take_profile_events();
-  const dim3 block(64 * kLayerWaves);
-  const int64_t tasks = int64_t(std::min(a.n_experts, a.t * a.k)) * (a.inter / 8);
-  hipExtLaunchKernelGGL(layer_gate_up_kernel, dim3(unsigned(std::min<int64_t>(cus, tasks))), block, kLayerLds, s,
-                        static_cast<hipEvent_t>(pe.start), nullptr, 0, a);
+  hipExtLaunchKernelGGL(layer_gate_up_kernel, up_grid, block, kLayerLds, s, static_cast<hipEvent_t>(pe.start), nullptr,
+                        0, a);
   const int err = int(hipGetLastError());
   if (err) return err;
-  hipExtLaunchKernelGGL(layer_down_kernel, dim3(unsigned(std::min(cus, a.d / 16))), block, kLayerLds, s, nullptr,
+  hipExtLaunchKernelGGL(layer_down_kernel, dim3(unsigned(std::min(cus, blocks))), block, kLayerLds, s, nullptr,
                         static_cast<hipEvent_t>(pe.stop), 0, a);
   return int(hipGetLastError());
 }
