@@ -38,7 +38,7 @@ namespace {
 
 constexpr int kLayerWaves = 8;
 constexpr int kLayerRing = 18 * 1024;     // a wave's ring
-constexpr int kRowKinds = 5;              // groups of up to 1, 2, 4, 8 or 16 rows
+constexpr int kRowKinds = 4;              // groups of up to 2, 4, 8 or 16 rows
 
 struct LayerTables {
   int32_t ids[kLayerMaxPairs];            // experts of the pairs (token, choice), -1: none
@@ -46,10 +46,11 @@ struct LayerTables {
   // "rows" are the pairs with an expert, by expert, then token
   float row_weight[kLayerMaxPairs];
   uint8_t token[kLayerMaxPairs];          // of the rows
+  uint16_t tokens[kLayerMaxPairs];        // of a group, a bit each
   uint16_t expert[kLayerMaxPairs];        // of the groups
   uint16_t first[kLayerMaxPairs + 2];     // a group's first row
   uint32_t sums[2][kLayerWaves];
-  int32_t groups, kind;                   // groups, of up to 1 << kind rows
+  int32_t groups, kind;                   // groups, of up to 2 << kind rows
 };
 constexpr int kLayerRed = kLayerWaves * kLayerRing;                    // the waves' sums
 constexpr int kLayerTables = kLayerRed + kLayerWaves * 1024;
@@ -67,7 +68,7 @@ __device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
 }
 
 // The tables from ids; every thread of the workgroup calls it.  An expert's rows are taken in
-// groups of up to 1 << kind, each of which reads the expert's weights: the fewer rows a step
+// groups of up to 2 << kind, each of which reads the expert's weights: the fewer rows a step
 // of the ring holds, the more steps it has.  `tokens` is scratch for n_experts words: which
 // tokens an expert has, a bit each, and its first row in the upper half.  Thread i counts for
 // experts 2i and 2i + 1; the counts of all kinds go through one scan, 10 bits each.
@@ -103,26 +104,31 @@ __device__ __forceinline__ void make_tables(LayerTables& T, uint32_t* tokens, in
     all_b += sb;
   }
   auto of = [](int kind, uint32_t u, uint32_t v) {
-    return int((kind == 0 ? u : kind == 1 ? u >> 10 : kind == 2 ? u >> 20 : kind == 3 ? v : v >> 10) & 1023u);
+    return int((kind == 0 ? u >> 10 : kind == 1 ? u >> 20 : kind == 2 ? v : v >> 10) & 1023u);
   };
-  const int most = of(4, all_a, all_b);           // chosen experts
+  const int most = of(kRowKinds - 1, all_a, all_b);   // chosen experts
   int kind = 0;
   while (kind < kRowKinds - 1 && 4 * of(kind, all_a, all_b) > 5 * most) ++kind;
-  int at = of(kind, at_a, at_b), row = of(0, at_a, at_b);
+  int at = of(kind, at_a, at_b), row = int(at_a & 1023u);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int r = __builtin_popcount(mask[i]);
     if (r) tokens[2 * tid + i] = mask[i] | uint32_t(row) << 16;
-    for (int q = 0; q < r; q += 1 << kind) {
+    uint32_t left = mask[i];
+    for (int q = 0; q < r; q += 2 << kind) {
+      uint32_t rest = left;
+      for (int n = 0; n < 2 << kind; ++n) rest &= rest - 1u;
+      T.tokens[at] = uint16_t(left ^ rest);
       T.expert[at] = uint16_t(2 * tid + i);
       T.first[at++] = uint16_t(row + q);
+      left = rest;
     }
     row += r;
   }
   if (tid == 0) {
     T.groups = of(kind, all_a, all_b);
     T.kind = kind;
-    T.first[T.groups] = uint16_t(of(0, all_a, all_b));
+    T.first[T.groups] = uint16_t(all_a & 1023u);
   }
   __syncthreads();
   if (id >= 0) {
@@ -147,8 +153,11 @@ __device__ __forceinline__ void choose(const MoeLayerArgs& a, int tok, float* mi
     const float v = a.bf16 ? logit<true>(a.logits, at) : logit<false>(a.logits, at);
     l[j] = e < a.n_experts ? v : -INFINITY;
   }
+  float b[J];
+#pragma unroll
+  for (int j = 0; j < J; ++j) b[j] = a.bias ? a.bias[min(J * lane + j, a.n_experts - 1)] : 0.f;
   const TopkChoice c = topk_wave<J, SIGMOID>(
-      l, rule, [&](int j) { return a.bias ? a.bias[min(J * lane + j, a.n_experts - 1)] : 0.f; },
+      l, rule, [&](int j) { return b[j]; },
       [&](int j) { return min(J * lane + j, a.n_experts - 1) / rule.gs * rule.per; }, mine);
   if (lane < a.k) {
     T.ids[tok * a.k + lane] = c.expert;
@@ -161,17 +170,19 @@ __device__ __forceinline__ void choose(const MoeLayerArgs& a, int tok, float* mi
 // are then in different banks.
 __device__ __forceinline__ int spread(int row) { return (row & 7) | ((row >> 3 ^ row >> 2) & 1) << 3; }
 
-// The steps of a wave, groups of up to ROWS tokens.
-template <bool DOWN, int ROWS>
+// The steps of a wave, CODES codes each, groups of up to ROWS tokens.
+template <bool DOWN, int ROWS, int CODES>
 __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds, LayerTables& T) {
-  // rows of 256 bytes: one or two in copies of 4 bytes a lane, else four in one of 16
-  constexpr int kCopies = ROWS <= 2 ? ROWS : ROWS / 4, kOps = 2 + kCopies;
-  constexpr int kMetaAt = 1024 + 256 * ROWS, kStage = kMetaAt + 256, D = kLayerRing / kStage;
+  constexpr int kParts = CODES / 128;             // 1 KB of weights each
+  constexpr int kRowBytes = 2 * CODES, kPieces = kRowBytes / 16, kPerCopy = 1024 / kRowBytes;   // rows of activations
+  constexpr int kCopies = ROWS / kPerCopy, kOps = kParts + kCopies + 1;
+  constexpr int kRowsAt = 1024 * kParts, kMetaAt = kRowsAt + 1024 * kCopies, kStage = kMetaAt + 256;
+  constexpr int D = kLayerRing / kStage;
   static_assert((D - 1) * kOps <= 63, "the waits count the copies in flight");
   const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int axis = DOWN ? a.inter : a.d, n = DOWN ? a.d : 2 * a.inter;
-  const int steps = (axis + 127) / 128, groups = __builtin_amdgcn_readfirstlane(T.groups);
+  const int steps = (axis + CODES - 1) / CODES, groups = __builtin_amdgcn_readfirstlane(T.groups);
   const Slabs L{n, axis, QMM_MXFP4_G32};
   const int last = L.count() - 1;
   const uint32_t width = uint32_t(L.width(0) / 2), width_last = uint32_t(L.width(last) / 2);
@@ -215,13 +226,14 @@ __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds
 
   // ---- the copies' place in the sequence
   const int wrow = lane >> 2, wpiece = (lane & 3) ^ (wrow >> 1 & 3);
+  const int part = lane % kParts;                 // of a step's exponents
   int c_round = 0, c_pos = begin, c_h = 0, c_to = 0;
   __amdgpu_buffer_rsrc_t cr = make_rsrc(stack, 0), mr = cr;
   uint32_t w_full = 0, w_last = 0, m_full = 0, m_last = 0, aoff[kCopies];
 #pragma unroll
   for (int i = 0; i < kCopies; ++i) aoff[i] = kOOB8;
-  auto copied_row = [&](int i) { return ROWS <= 2 ? i : 4 * i + (lane >> 4); };
-  auto copied_at = [&](int i) { return ROWS <= 2 ? 2 * lane : 8 * ((lane & 15) ^ spread(copied_row(i))); };   // code
+  auto copied_row = [&](int i) { return kPerCopy * i + lane / kPieces; };
+  auto copied_at = [&](int i) { return 8 * ((lane % kPieces) ^ spread(copied_row(i))); };   // code
   auto open = [&]() {
     const Piece t = piece_at(c_pos);
     int e = __builtin_amdgcn_readfirstlane(T.expert[t.j]), at = __builtin_amdgcn_readfirstlane(T.first[t.j]);
@@ -238,8 +250,10 @@ __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds
     auto any = [&](int r) { return (DOWN ? r : r & 7) < rows; };
     w_full = any(wrow) ? row(wrow) * width + 16u * uint32_t(wpiece) : kOOB8;
     w_last = any(wrow) ? row(wrow) * width_last + 16u * uint32_t(wpiece) : kOOB8;
-    m_full = lane < 16 && any(c) ? (row(c) >> 2) * mquad + (row(c) & 3u) * mrow : kOOB8;
-    m_last = lane < 16 && any(c) ? (row(c) >> 2) * mquad + (row(c) & 3u) * mrow_last : kOOB8;
+    const int mr16 = lane / kParts & 15;
+    const bool meta = lane < 16 * kParts && any(mr16);
+    m_full = meta ? (row(mr16) >> 2) * mquad + (row(mr16) & 3u) * mrow + 4u * uint32_t(part) : kOOB8;
+    m_last = meta ? (row(mr16) >> 2) * mquad + (row(mr16) & 3u) * mrow_last + 4u * uint32_t(part) : kOOB8;
 #pragma unroll
     for (int i = 0; i < kCopies; ++i) {
       const int r = at + copied_row(i), q = min(r, kLayerMaxPairs - 1);
@@ -249,20 +263,21 @@ __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds
     c_to = DOWN ? t.at + t.size : steps;
     c_pos = t.next;
   };
-  bool more = rounds > 0 && begin < end;
+  bool more = rounds > 0 && begin < end;          // copies left
   auto copies = [&](int stage) {
-    const int h = c_h, s = h >> 2;
-    const uint32_t at = ring_at + uint32_t(stage * kStage), none = more ? 0u : kOOB8;
-    copy16_to_lds_from(cr, (s == last ? w_last : w_full) | none | (128 * h + 32 * wpiece < axis ? 0u : kOOB8),
-                       more ? uint32_t(s) * slab_bytes + 64u * uint32_t(h & 3) : 0u, at);
+    const int h = c_h, s = h * CODES / kSlabCodes, in_slab = h & (kSlabCodes / CODES - 1);
+    const uint32_t at = ring_at + uint32_t(stage * kStage), from = s == last ? w_last : w_full;
 #pragma unroll
-    for (int i = 0; i < kCopies; ++i) {
-      const uint32_t from = aoff[i] | none | (128 * h + copied_at(i) < axis ? 0u : kOOB8);
-      if (ROWS <= 2) copy4_to_lds(ar, from + (more ? 256u * uint32_t(h) : 0u), at + 1024u + 256u * uint32_t(i));
-      else copy16_to_lds_from(ar, from, more ? 256u * uint32_t(h) : 0u, at + 1024u + 1024u * uint32_t(i));
-    }
-    copy4_to_lds(mr, ((s == last ? m_last : m_full) + 64u * uint32_t(s) + 4u * uint32_t(h & 3)) | none, at + kMetaAt);
-    if (more && ++c_h == c_to) {
+    for (int i = 0; i < kParts; ++i)
+      copy16_to_lds_from(cr, from | (CODES * h + 128 * i + 32 * wpiece < axis ? 0u : kOOB8),
+                         uint32_t(s) * slab_bytes + uint32_t(CODES / 2 * in_slab + 64 * i), at + 1024u * uint32_t(i));
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i)
+      copy16_to_lds_from(ar, aoff[i] | (CODES * h + copied_at(i) < axis ? 0u : kOOB8), uint32_t(kRowBytes * h),
+                         at + kRowsAt + 1024u * uint32_t(i));
+    copy4_to_lds(mr, ((s == last ? m_last : m_full) + uint32_t(64 * s + CODES / 32 * in_slab)) |
+                         (CODES * h + 128 * part < axis ? 0u : kOOB8), at + kMetaAt);
+    if (++c_h == c_to) {
       if (c_pos >= end) {
         c_pos = begin;
         more = ++c_round < rounds;
@@ -272,7 +287,7 @@ __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds
   };
   if (more) open();
 #pragma unroll 1
-  for (int i = 0; i < D; ++i) copies(i);
+  for (int i = 0; i < D && more; ++i) copies(i);
 
   int stage = 0;
   f32x4_t* red = reinterpret_cast<f32x4_t*>(lds + kLayerRed);
@@ -286,35 +301,40 @@ __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds
       int row = min(c, rows - 1);
       bool has = c < rows;
       if (DOWN) {
-        row = 0;
-        has = false;
-#pragma unroll
-        for (int r = 0; r < ROWS; ++r)
-          if (r < rows && T.token[at + r] == c) {
-            row = r;
-            has = true;
-          }
+        const uint32_t m = T.tokens[t.j];
+        has = m >> c & 1u;
+        row = has ? __builtin_popcount(m & ((1u << c) - 1u)) : 0;
       }
-      const uint32_t a_at = 1024u + 256u * uint32_t(row);
-      const int x0 = ROWS <= 2 ? 0 : spread(row);
+      const uint32_t a_at = uint32_t(kRowsAt + kRowBytes * row);
+      const int x0 = spread(row);
       f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
       const int n_steps = DOWN ? t.size : steps;
       for (int h = 0; h < n_steps; ++h) {
-        wait_copies<(D - 1) * kOps>();
+        if (more) wait_copies<(D - 1) * kOps>();
+        else wait_copies<0>();
         const unsigned char* st = ring + stage * kStage;
-        const u32x4_t w = *reinterpret_cast<const u32x4_t*>(st + 64 * c + 16 * (g ^ (c >> 1 & 3)));
-        const uint32_t e8 = st[kMetaAt + 4 * c + g];
-        u32x4_t b[4];
+        u32x4_t w[kParts], b[kParts][4];
+        uint32_t e8[kParts];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const u32x4_t*>(st + a_at + 16 * ((4 * g + j) ^ x0));
+        for (int i = 0; i < kParts; ++i) {
+          w[i] = *reinterpret_cast<const u32x4_t*>(st + 1024 * i + 64 * c + 16 * (g ^ (c >> 1 & 3)));
+          e8[i] = st[kMetaAt + 4 * kParts * c + 4 * i + g];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            b[i][j] = *reinterpret_cast<const u32x4_t*>(st + a_at + 16 * ((16 * i + 4 * g + j) ^ x0));
+        }
         wait_reads();                             // ... and is in registers: its stage is free
-        copies(stage);
+        if (more) copies(stage);
         stage = stage + 1 == D ? 0 : stage + 1;
-        const float scale = e8m0_scale(e8);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, mxfp4_word_to_bf16x8(w[j], scale)),
-                                                        __builtin_bit_cast(bf16x8_t, b[j]), acc, 0, 0, 0);
+        for (int i = 0; i < kParts; ++i) {
+          const float scale = e8m0_scale(e8[i]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                __builtin_bit_cast(bf16x8_t, mxfp4_word_to_bf16x8(w[i][j], scale)),
+                __builtin_bit_cast(bf16x8_t, b[i][j]), acc, 0, 0, 0);
+        }
       }
       if (DOWN) {
         if (has) {
@@ -358,11 +378,10 @@ __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds
 template <bool DOWN>
 __device__ __forceinline__ void stream_any(const MoeLayerArgs& a, unsigned char* lds, LayerTables& T) {
   const int kind = __builtin_amdgcn_readfirstlane(T.kind);
-  if (kind == 0) stream<DOWN, 1>(a, lds, T);
-  else if (kind == 1) stream<DOWN, 2>(a, lds, T);
-  else if (kind == 2) stream<DOWN, 4>(a, lds, T);
-  else if (kind == 3) stream<DOWN, 8>(a, lds, T);
-  else stream<DOWN, 16>(a, lds, T);
+  if (kind == 0) stream<DOWN, 2, 256>(a, lds, T);
+  else if (kind == 1) stream<DOWN, 4, 256>(a, lds, T);
+  else if (kind == 2) stream<DOWN, 8, 128>(a, lds, T);
+  else stream<DOWN, 16, 128>(a, lds, T);
 }
 
 __global__ __launch_bounds__(64 * kLayerWaves) void layer_gate_up_kernel(MoeLayerArgs a) {
