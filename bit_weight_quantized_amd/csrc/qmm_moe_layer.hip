@@ -289,6 +289,15 @@ __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds
 #pragma unroll 1
   for (int i = 0; i < D && more; ++i) copies(i);
 
+  // Of the two waves on a SIMD the one with the lower index issues its copies first and is done
+  // earlier, and the tail has half the copies in flight.  The other half of the workgroup is
+  // therefore raised; over many steps the first is too, every other step.  One token, 8 of 256
+  // experts of 3584x2048: 32.8 us without, 32.0 as it is, 32.6 in turns; 16 tokens, 8 of 256:
+  // 232.7, 232.5, 224.8.
+  const int mine = DOWN ? end - begin : (work - begin + waves - 1) / waves * steps;
+  const bool in_turns = mine > 40;
+  if (wave >= kLayerWaves / 2) __builtin_amdgcn_s_setprio(1);
+
   int stage = 0;
   f32x4_t* red = reinterpret_cast<f32x4_t*>(lds + kLayerRed);
   for (int round = 0; round < rounds; ++round) {
@@ -310,6 +319,10 @@ __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds
       f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
       const int n_steps = DOWN ? t.size : steps;
       for (int h = 0; h < n_steps; ++h) {
+        if (in_turns && wave < kLayerWaves / 2) {
+          if (h & 1) __builtin_amdgcn_s_setprio(1);
+          else __builtin_amdgcn_s_setprio(0);
+        }
         if (more) wait_copies<(D - 1) * kOps>();
         else wait_copies<0>();
         const unsigned char* st = ring + stage * kStage;
