@@ -37,12 +37,14 @@ namespace qmm {
 namespace {
 
 constexpr int kLayerWaves = 8;
-constexpr int kLayerRing = 18 * 1024;     // a wave's ring
+constexpr int kLayerRing = 3 * 6400;      // a wave's ring
 constexpr int kRowKinds = 4;              // groups of up to 2, 4, 8 or 16 rows
 
-struct LayerTables {
+struct LayerChoice {
   int32_t ids[kLayerMaxPairs];            // experts of the pairs (token, choice), -1: none
   float weights[kLayerMaxPairs];          // of the pairs
+};
+struct LayerTables {
   // "rows" are the pairs with an expert, by expert, then token
   float row_weight[kLayerMaxPairs];
   uint8_t token[kLayerMaxPairs];          // of the rows
@@ -52,9 +54,10 @@ struct LayerTables {
   uint32_t sums[2][kLayerWaves];
   int32_t groups, kind;                   // groups, of up to 2 << kind rows
 };
-constexpr int kLayerRed = kLayerWaves * kLayerRing;                    // the waves' sums
-constexpr int kLayerTables = kLayerRed + kLayerWaves * 1024;
+constexpr int kLayerRed = kLayerWaves * kLayerRing;                    // sums of waves but the first
+constexpr int kLayerTables = kLayerRed + (kLayerWaves - 1) * 1024;
 constexpr int kLayerLds = kLayerTables + int(sizeof(LayerTables));
+static_assert(kLayerRed + sizeof(LayerChoice) <= kLayerTables, "the choice lies where the sums will");
 static_assert(kLayerLds <= 160 * 1024, "LDS");
 
 // Inclusive sums of a wave's lanes.
@@ -72,12 +75,12 @@ __device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
 // of the ring holds, the more steps it has.  `tokens` is scratch for n_experts words: which
 // tokens an expert has, a bit each, and its first row in the upper half.  Thread i counts for
 // experts 2i and 2i + 1; the counts of all kinds go through one scan, 10 bits each.
-__device__ __forceinline__ void make_tables(LayerTables& T, uint32_t* tokens, int pairs, int k, int ne) {
+__device__ __forceinline__ void make_tables(LayerTables& T, const LayerChoice& C, uint32_t* tokens, int pairs, int k, int ne) {
   static_assert(kRouteMaxExperts <= 2 * 64 * kLayerWaves, "a thread has two experts");
   const int tid = threadIdx.x, wave = tid >> 6;
   for (int e = tid; e < ne; e += 64 * kLayerWaves) tokens[e] = 0u;
   __syncthreads();
-  const int id = tid < pairs ? T.ids[tid] : -1, tok = tid / k;
+  const int id = tid < pairs ? C.ids[tid] : -1, tok = tid / k;
   if (id >= 0) atomicOr(&tokens[id], 1u << tok);
   __syncthreads();
   uint32_t mask[2], a = 0, b = 0;
@@ -135,14 +138,14 @@ __device__ __forceinline__ void make_tables(LayerTables& T, uint32_t* tokens, in
     const uint32_t m = tokens[id];
     const int r = int(m >> 16) + __builtin_popcount(m & 0xffffu & ((1u << tok) - 1u));
     T.token[r] = uint8_t(tok);
-    T.row_weight[r] = T.weights[tid];
+    T.row_weight[r] = C.weights[tid];
   }
   __syncthreads();
 }
 
 // One wave's choice for one token.
 template <int J, bool SIGMOID>
-__device__ __forceinline__ void choose(const MoeLayerArgs& a, int tok, float* mine, LayerTables& T) {
+__device__ __forceinline__ void choose(const MoeLayerArgs& a, int tok, float* mine, LayerChoice& C) {
   const int lane = threadIdx.x & 63;
   const TopkRule rule = topk_rule<J, SIGMOID>(a.n_experts, a.k, a.bias != nullptr, a.groups, a.keep, a.top2, a.renorm);
   float l[J];
@@ -160,8 +163,8 @@ __device__ __forceinline__ void choose(const MoeLayerArgs& a, int tok, float* mi
       l, rule, [&](int j) { return b[j]; },
       [&](int j) { return min(J * lane + j, a.n_experts - 1) / rule.gs * rule.per; }, mine);
   if (lane < a.k) {
-    T.ids[tok * a.k + lane] = c.expert;
-    T.weights[tok * a.k + lane] = c.weight * a.scale;
+    C.ids[tok * a.k + lane] = c.expert;
+    C.weights[tok * a.k + lane] = c.weight * a.scale;
   }
 }
 
@@ -175,7 +178,8 @@ template <bool DOWN, int ROWS, int CODES>
 __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds, LayerTables& T) {
   constexpr int kParts = CODES / 128;             // 1 KB of weights each
   constexpr int kRowBytes = 2 * CODES, kPieces = kRowBytes / 16, kPerCopy = 1024 / kRowBytes;   // rows of activations
-  constexpr int kCopies = ROWS / kPerCopy, kOps = kParts + kCopies + 1;
+  constexpr int kPlanes = DOWN ? 2 : 1, kOfPlane = ROWS / kPerCopy;   // h is in two bf16 parts
+  constexpr int kCopies = kPlanes * kOfPlane, kOps = kParts + kCopies + 1;
   constexpr int kRowsAt = 1024 * kParts, kMetaAt = kRowsAt + 1024 * kCopies, kStage = kMetaAt + 256;
   constexpr int D = kLayerRing / kStage;
   static_assert((D - 1) * kOps <= 63, "the waits count the copies in flight");
@@ -193,7 +197,8 @@ __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds
   const uint8_t* stack = DOWN ? a.down : a.gate_up;
   const int64_t stride = DOWN ? a.down_stride : a.gate_up_stride;
   const uint32_t row_bytes = uint32_t(axis) * 2u;
-  const __amdgpu_buffer_rsrc_t ar = make_rsrc(DOWN ? a.h : a.x, uint32_t(DOWN ? a.t * a.k : a.t) * row_bytes);
+  const __amdgpu_buffer_rsrc_t ar = make_rsrc(DOWN ? a.h : a.x, uint32_t(DOWN ? 2 * a.t * a.k : a.t) * row_bytes);
+  const uint32_t plane = DOWN ? uint32_t(a.t * a.k) * row_bytes : 0u;
   unsigned char* ring = lds + wave * kLayerRing;
   const uint32_t ring_at = lds_addr(ring);
 
@@ -229,9 +234,9 @@ __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds
   const int part = lane % kParts;                 // of a step's exponents
   int c_round = 0, c_pos = begin, c_h = 0, c_to = 0;
   __amdgpu_buffer_rsrc_t cr = make_rsrc(stack, 0), mr = cr;
-  uint32_t w_full = 0, w_last = 0, m_full = 0, m_last = 0, aoff[kCopies];
+  uint32_t w_full = 0, w_last = 0, m_full = 0, m_last = 0, aoff[kOfPlane];
 #pragma unroll
-  for (int i = 0; i < kCopies; ++i) aoff[i] = kOOB8;
+  for (int i = 0; i < kOfPlane; ++i) aoff[i] = kOOB8;
   auto copied_row = [&](int i) { return kPerCopy * i + lane / kPieces; };
   auto copied_at = [&](int i) { return 8 * ((lane % kPieces) ^ spread(copied_row(i))); };   // code
   auto open = [&]() {
@@ -255,7 +260,7 @@ __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds
     m_full = meta ? (row(mr16) >> 2) * mquad + (row(mr16) & 3u) * mrow + 4u * uint32_t(part) : kOOB8;
     m_last = meta ? (row(mr16) >> 2) * mquad + (row(mr16) & 3u) * mrow_last + 4u * uint32_t(part) : kOOB8;
 #pragma unroll
-    for (int i = 0; i < kCopies; ++i) {
+    for (int i = 0; i < kOfPlane; ++i) {
       const int r = at + copied_row(i), q = min(r, kLayerMaxPairs - 1);
       aoff[i] = r < stop ? uint32_t(DOWN ? q : T.token[q]) * row_bytes + 2u * uint32_t(copied_at(i)) : kOOB8;
     }
@@ -273,8 +278,8 @@ __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds
                          uint32_t(s) * slab_bytes + uint32_t(CODES / 2 * in_slab + 64 * i), at + 1024u * uint32_t(i));
 #pragma unroll
     for (int i = 0; i < kCopies; ++i)
-      copy16_to_lds_from(ar, aoff[i] | (CODES * h + copied_at(i) < axis ? 0u : kOOB8), uint32_t(kRowBytes * h),
-                         at + kRowsAt + 1024u * uint32_t(i));
+      copy16_to_lds_from(ar, aoff[i % kOfPlane] | (CODES * h + copied_at(i % kOfPlane) < axis ? 0u : kOOB8),
+                         uint32_t(kRowBytes * h) + (i < kOfPlane ? 0u : plane), at + kRowsAt + 1024u * uint32_t(i));
     copy4_to_lds(mr, ((s == last ? m_last : m_full) + uint32_t(64 * s + CODES / 32 * in_slab)) |
                          (CODES * h + 128 * part < axis ? 0u : kOOB8), at + kMetaAt);
     if (++c_h == c_to) {
@@ -326,15 +331,18 @@ __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds
         if (more) wait_copies<(D - 1) * kOps>();
         else wait_copies<0>();
         const unsigned char* st = ring + stage * kStage;
-        u32x4_t w[kParts], b[kParts][4];
+        u32x4_t w[kParts], b[kParts][4][kPlanes];
         uint32_t e8[kParts];
 #pragma unroll
         for (int i = 0; i < kParts; ++i) {
           w[i] = *reinterpret_cast<const u32x4_t*>(st + 1024 * i + 64 * c + 16 * (g ^ (c >> 1 & 3)));
           e8[i] = st[kMetaAt + 4 * kParts * c + 4 * i + g];
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            b[i][j] = *reinterpret_cast<const u32x4_t*>(st + a_at + 16 * ((16 * i + 4 * g + j) ^ x0));
+          for (int j = 0; j < 4; ++j) {
+#pragma unroll
+            for (int p = 0; p < kPlanes; ++p)
+              b[i][j][p] = *reinterpret_cast<const u32x4_t*>(st + a_at + 1024 * kOfPlane * p + 16 * ((16 * i + 4 * g + j) ^ x0));
+          }
         }
         wait_reads();                             // ... and is in registers: its stage is free
         if (more) copies(stage);
@@ -343,10 +351,12 @@ __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds
         for (int i = 0; i < kParts; ++i) {
           const float scale = e8m0_scale(e8[i]);
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                __builtin_bit_cast(bf16x8_t, mxfp4_word_to_bf16x8(w[i][j], scale)),
-                __builtin_bit_cast(bf16x8_t, b[i][j]), acc, 0, 0, 0);
+          for (int j = 0; j < 4; ++j) {
+            const bf16x8_t v = __builtin_bit_cast(bf16x8_t, mxfp4_word_to_bf16x8(w[i][j], scale));
+#pragma unroll
+            for (int p = 0; p < kPlanes; ++p)
+              acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, __builtin_bit_cast(bf16x8_t, b[i][j][p]), acc, 0, 0, 0);
+          }
         }
       }
       if (DOWN) {
@@ -360,17 +370,24 @@ __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float v = silu(acc[e]) * __shfl_xor(acc[e], 32);
-          if (has && g < 2 && 4 * g + e < t.size) a.h[int64_t(at + row) * a.inter + t.at + 4 * g + e] = uint16_t(pack_bf16x2(v, v));
+          if (has && g < 2 && 4 * g + e < t.size) {
+            // the nearest bf16 and what it leaves: 16 bits of v, so that out has its own rounding alone
+            const uint32_t hi = pack_bf16x2(v, v) & 0xffffu;
+            const float rest = __builtin_isfinite(v) ? v - bf16_lo(hi) : 0.f;
+            const int64_t o = int64_t(at + row) * a.inter + t.at + 4 * g + e;
+            a.h[o] = uint16_t(hi);
+            a.h[o + int64_t(a.t) * a.k * a.inter] = uint16_t(pack_bf16x2(rest, rest));
+          }
         }
       }
     }
     if (DOWN) {
-      red[64 * wave + lane] = sum;
+      if (wave) red[64 * (wave - 1) + lane] = sum;
       wait_reads();
       phase_end();
       if (wave == 0 && c < a.t) {
 #pragma unroll
-        for (int w = 1; w < kLayerWaves; ++w) sum += red[64 * w + lane];
+        for (int w = 0; w < kLayerWaves - 1; ++w) sum += red[64 * w + lane];
         const int column = (int(blockIdx.x) + round * int(gridDim.x)) * a.cols, cols = min(a.cols, a.d - column);
 #pragma unroll
         for (int e = 0; e < 4; e += 2) {
@@ -400,37 +417,39 @@ __device__ __forceinline__ void stream_any(const MoeLayerArgs& a, unsigned char*
 __global__ __launch_bounds__(64 * kLayerWaves) void layer_gate_up_kernel(MoeLayerArgs a) {
   extern __shared__ __attribute__((aligned(1024))) unsigned char lds[];
   LayerTables& T = *reinterpret_cast<LayerTables*>(lds + kLayerTables);
+  LayerChoice& C = *reinterpret_cast<LayerChoice*>(lds + kLayerRed);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   float* mine = reinterpret_cast<float*>(lds + wave * kLayerRing);
   for (int tok = wave; tok < a.t; tok += kLayerWaves) {
     if (a.n_experts <= 256) {
-      if (a.sigmoid) choose<4, true>(a, tok, mine, T);
-      else choose<4, false>(a, tok, mine, T);
+      if (a.sigmoid) choose<4, true>(a, tok, mine, C);
+      else choose<4, false>(a, tok, mine, C);
     } else {
-      if (a.sigmoid) choose<16, true>(a, tok, mine, T);
-      else choose<16, false>(a, tok, mine, T);
+      if (a.sigmoid) choose<16, true>(a, tok, mine, C);
+      else choose<16, false>(a, tok, mine, C);
     }
   }
   __syncthreads();
   const int pairs = a.t * a.k, tid = threadIdx.x;
   if (blockIdx.x == 0 && tid < pairs) {
-    a.topk[tid] = T.ids[tid];
-    a.weights[tid] = T.weights[tid];
+    a.topk[tid] = C.ids[tid];
+    a.weights[tid] = C.weights[tid];
   }
-  make_tables(T, reinterpret_cast<uint32_t*>(lds), pairs, a.k, a.n_experts);
+  make_tables(T, C, reinterpret_cast<uint32_t*>(lds), pairs, a.k, a.n_experts);
   stream_any<false>(a, lds, T);
 }
 
 __global__ __launch_bounds__(64 * kLayerWaves) void layer_down_kernel(MoeLayerArgs a) {
   extern __shared__ __attribute__((aligned(1024))) unsigned char lds[];
   LayerTables& T = *reinterpret_cast<LayerTables*>(lds + kLayerTables);
+  LayerChoice& C = *reinterpret_cast<LayerChoice*>(lds + kLayerRed);
   const int pairs = a.t * a.k, tid = threadIdx.x;
   if (tid < pairs) {
     const int e = a.topk[tid];
-    T.ids[tid] = e >= 0 && e < a.n_experts ? e : -1;
-    T.weights[tid] = a.weights[tid];
+    C.ids[tid] = e >= 0 && e < a.n_experts ? e : -1;
+    C.weights[tid] = a.weights[tid];
   }
-  make_tables(T, reinterpret_cast<uint32_t*>(lds), pairs, a.k, a.n_experts);
+  make_tables(T, C, reinterpret_cast<uint32_t*>(lds), pairs, a.k, a.n_experts);
   stream_any<true>(a, lds, T);
 }
 

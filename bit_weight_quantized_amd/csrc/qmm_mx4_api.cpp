@@ -148,7 +148,7 @@ qmm_status qmm_mxfp4_grouped_gemm_swiglu(const void* packed_stack, int64_t exper
 size_t qmm_moe_layer_workspace_bytes(int64_t t, int32_t k, int64_t inter) {
   if (t < 1 || t > qmm::kLayerMaxTokens || k < 1 || k > qmm::kRouteMaxK || t * k > qmm::kLayerMaxPairs) return 0;
   if (inter < 32 || inter > qmm::kMaxD || inter % 32) return 0;
-  return size_t(2 * t * k * inter);
+  return size_t(4 * t * k * inter);
 }
 
 qmm_status qmm_moe_layer(qmm_format f, const void* gate_up, int64_t gate_up_stride_bytes, const void* down,

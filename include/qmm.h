@@ -544,14 +544,14 @@ qmm_status qmm_mxfp4_grouped_gemm_swiglu(const void* packed_stack, int64_t exper
                                          int32_t max_seg_rows, qmm_mx_rule rule, qmm_bf16* h, uint8_t* hq,
                                          uint8_t* h_scales, void* stream);
 
-/* Workspace of qmm_moe_layer in bytes: 2·t·k·inter (0 for invalid arguments).  Host only. */
+/* Workspace of qmm_moe_layer in bytes: 4·t·k·inter (0 for invalid arguments).  Host only. */
 size_t qmm_moe_layer_workspace_bytes(int64_t t, int32_t k, int64_t inter);
 
 /* A mixture-of-experts layer for a few tokens, from the router's logits to the sum of the
  * experts' outputs, in two launches, the weights packed MXFP4 and the activations bf16:
  *   topk, weights   chosen and weighted as qmm_route_topk does: dtype, ld, score, bias,
  *                   n_groups, keep_groups, group_score, k, renorm and scale as there
- *   h[i][j]   = silu(G_e·x_i)·(U_e·x_i), e = topk[i][j], of fp32 sums, rounded once to bf16
+ *   h[i][j]   = silu(G_e·x_i)·(U_e·x_i), e = topk[i][j], of fp32 sums, kept to 16 bits
  *   out[i]    = sum_j weights[i][j]·(D_e·h[i][j]) + shared[i], in fp32, rounded once to bf16;
  *               slots of -1 add nothing
  *   gate_up   [n_experts] packed matrices [2·inter, d] (rows [0, inter) the gate G, then the

@@ -1,5 +1,5 @@
-"""A mixture-of-experts layer for given choices in fp64, with what fp32 sums and bf16
-intermediates may be off by."""
+"""A mixture-of-experts layer for given choices in fp64, with what fp32 sums and
+intermediates of 16 bits may be off by."""
 import numpy as np
 
 from .mxfp4 import swiglu
@@ -10,10 +10,10 @@ STEP = 2.0 ** -23
 def product(x, tol_x, w):
     """(x @ w.T, its error bound): x off by tol_x, and a sum in fp32 in which a term goes
     through at most 32 additions in the matrix instruction that reads it, one for each 32
-    codes after it, and 16 in the joining of parts; each loses at most 2^-23 of the sum of the
+    codes after it (two where x has two parts), and 16 in the joining of parts; each loses at most 2^-23 of the sum of the
     magnitudes (products of a weight's 2 and a bf16's 8 bits are exact)."""
     a = (np.abs(x) + tol_x) @ np.abs(w).T
-    return x @ w.T, tol_x @ np.abs(w).T + (32 + x.shape[1] / 32 + 16) * STEP * a
+    return x @ w.T, tol_x @ np.abs(w).T + (33 + x.shape[1] / 16 + 16) * STEP * a
 
 
 def layer(x, gate_up, down, ids, weights, shared):
@@ -28,7 +28,7 @@ def layer(x, gate_up, down, ids, weights, shared):
             half = gate_up[e].shape[0] // 2
             s, ts = product(x[i:i + 1], np.zeros((1, d)), gate_up[e])
             h, th = swiglu(s[:, :half], s[:, half:], ts[:, :half], ts[:, half:])
-            th = th + 2.0 ** -8 * (np.abs(h) + th) + 2.0 ** -133     # rounded to bf16
+            th = th + 2.0 ** -16 * (np.abs(h) + th) + 2.0 ** -132     # kept in two bf16 parts
             y, ty = product(h, th, down[e])
             out[i] += weights[i, j] * y[0]
             tol[i] += abs(weights[i, j]) * ty[0]

@@ -117,7 +117,7 @@ def test_grouped_refusals(glu):
 
 def test_moe_layer_workspace():
     f = qmm.qmm_moe_layer_workspace_bytes
-    assert f(1, 8, 2048) == 2 * 8 * 2048 and f(16, 16, 32) == 2 * 256 * 32
+    assert f(1, 8, 2048) == 4 * 8 * 2048 and f(16, 16, 32) == 4 * 256 * 32
     assert [f(0, 1, 32), f(17, 1, 32), f(1, 65, 32), f(16, 17, 32), f(1, 0, 32), f(1, 1, 33), f(1, 1, 65568)] == [0] * 7
 
 
