@@ -264,3 +264,14 @@ def test_agrees_with_the_calls_it_joins():
     each = np.abs(y.float().cpu().numpy().astype(np.float64))[slot.cpu().numpy()]       # [t][k][d]
     extra = 2.0 ** -8 * 1.02 * (np.abs(w.cpu().numpy())[..., None] * each).sum(1)
     assert np.all(np.abs(got[0] - got[1]) <= 2 * tol + extra)
+
+
+def test_events_bracket_both_launches():
+    from test_gpu_fp8_profile import bracketed
+    l = Layer((16, 24, 6, 1568, 800, "softmax", False, 1, 1, False, True, F32, 0, True), 9050)
+    i, o = l.inputs(), l.buffers()
+    l.call(i, o)
+    want = o["out"].clone()
+    o["out"].fill_(0)
+    assert 0.0 < bracketed(lambda: l.call(i, o)) < 100.0
+    assert torch.equal(o["out"], want)
