@@ -230,13 +230,19 @@ __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds
   };
 
   // ---- the copies' place in the sequence
-  const int wrow = lane >> 2, wpiece = (lane & 3) ^ (wrow >> 1 & 3);
+  // A copy of weights: 16 >> (kParts - 1) rows of 64 * kParts bytes.  Reads of 16-byte pieces by
+  // 16 rows are free of conflicts with the pieces at piece ^ (row >> 1).
+  constexpr int kRowPieces = 4 * kParts, kRowsOf = 64 / kRowPieces;
+  auto wrow = [&](int i) { return kRowsOf * i + lane / kRowPieces; };
+  auto wpiece = [&](int i) { return (lane % kRowPieces) ^ (wrow(i) >> 1 & (kRowPieces - 1)); };
   const int part = lane % kParts;                 // of a step's exponents
   int c_round = 0, c_pos = begin, c_h = 0, c_to = 0;
   __amdgpu_buffer_rsrc_t cr = make_rsrc(stack, 0), mr = cr;
-  uint32_t w_full = 0, w_last = 0, m_full = 0, m_last = 0, aoff[kOfPlane];
+  uint32_t w_full[kParts], w_last[kParts], m_full = 0, m_last = 0, aoff[kOfPlane];
 #pragma unroll
   for (int i = 0; i < kOfPlane; ++i) aoff[i] = kOOB8;
+#pragma unroll
+  for (int i = 0; i < kParts; ++i) w_full[i] = w_last[i] = kOOB8;
   auto copied_row = [&](int i) { return kPerCopy * i + lane / kPieces; };
   auto copied_at = [&](int i) { return 8 * ((lane % kPieces) ^ spread(copied_row(i))); };   // code
   auto open = [&]() {
@@ -253,8 +259,11 @@ __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds
     const int rows = DOWN ? min(a.cols, a.d - column) : t.size;
     auto row = [&](int r) { return uint32_t(DOWN ? column + r : t.at + (r & 7) + (r >= 8 ? a.inter : 0)); };
     auto any = [&](int r) { return (DOWN ? r : r & 7) < rows; };
-    w_full = any(wrow) ? row(wrow) * width + 16u * uint32_t(wpiece) : kOOB8;
-    w_last = any(wrow) ? row(wrow) * width_last + 16u * uint32_t(wpiece) : kOOB8;
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) {
+      w_full[i] = any(wrow(i)) ? row(wrow(i)) * width + 16u * uint32_t(wpiece(i)) : kOOB8;
+      w_last[i] = any(wrow(i)) ? row(wrow(i)) * width_last + 16u * uint32_t(wpiece(i)) : kOOB8;
+    }
     const int mr16 = lane / kParts & 15;
     const bool meta = lane < 16 * kParts && any(mr16);
     m_full = meta ? (row(mr16) >> 2) * mquad + (row(mr16) & 3u) * mrow + 4u * uint32_t(part) : kOOB8;
@@ -271,11 +280,11 @@ __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds
   bool more = rounds > 0 && begin < end;          // copies left
   auto copies = [&](int stage) {
     const int h = c_h, s = h * CODES / kSlabCodes, in_slab = h & (kSlabCodes / CODES - 1);
-    const uint32_t at = ring_at + uint32_t(stage * kStage), from = s == last ? w_last : w_full;
+    const uint32_t at = ring_at + uint32_t(stage * kStage);
 #pragma unroll
     for (int i = 0; i < kParts; ++i)
-      copy16_to_lds_from(cr, from | (CODES * h + 128 * i + 32 * wpiece < axis ? 0u : kOOB8),
-                         uint32_t(s) * slab_bytes + uint32_t(CODES / 2 * in_slab + 64 * i), at + 1024u * uint32_t(i));
+      copy16_to_lds_from(cr, (s == last ? w_last[i] : w_full[i]) | (CODES * h + 32 * wpiece(i) < axis ? 0u : kOOB8),
+                         uint32_t(s) * slab_bytes + uint32_t(CODES / 2 * in_slab), at + 1024u * uint32_t(i));
 #pragma unroll
     for (int i = 0; i < kCopies; ++i)
       copy16_to_lds_from(ar, aoff[i % kOfPlane] | (CODES * h + copied_at(i % kOfPlane) < axis ? 0u : kOOB8),
@@ -335,7 +344,7 @@ __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds
         uint32_t e8[kParts];
 #pragma unroll
         for (int i = 0; i < kParts; ++i) {
-          w[i] = *reinterpret_cast<const u32x4_t*>(st + 1024 * i + 64 * c + 16 * (g ^ (c >> 1 & 3)));
+          w[i] = *reinterpret_cast<const u32x4_t*>(st + 64 * kParts * c + 16 * ((4 * i + g) ^ (c >> 1 & (kRowPieces - 1))));
           e8[i] = st[kMetaAt + 4 * kParts * c + 4 * i + g];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
