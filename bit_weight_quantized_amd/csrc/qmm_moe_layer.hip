@@ -182,6 +182,8 @@ __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds
   constexpr int kCopies = kPlanes * kOfPlane, kOps = kParts + kCopies + 1;
   constexpr int kRowsAt = 1024 * kParts, kMetaAt = kRowsAt + 1024 * kCopies, kStage = kMetaAt + 256;
   constexpr int D = kLayerRing / kStage;
+  constexpr bool kBoth = DOWN && ROWS <= 8;
+  constexpr int kReads = kBoth ? 1 : kPlanes;     // of a column
   static_assert((D - 1) * kOps <= 63, "the waits count the copies in flight");
   const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -320,15 +322,10 @@ __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds
       const Piece t = piece_at(pos);
       pos = t.next;
       const int at = T.first[t.j], rows = T.first[t.j + 1] - at;
-      // the lane's row in LDS, in the second kernel its token's; whether it has one
-      int row = min(c, rows - 1);
-      bool has = c < rows;
-      if (DOWN) {
-        const uint32_t m = T.tokens[t.j];
-        has = m >> c & 1u;
-        row = has ? __builtin_popcount(m & ((1u << c) - 1u)) : 0;
-      }
-      const uint32_t a_at = uint32_t(kRowsAt + kRowBytes * row);
+      // A column of the products is a row of the group; with up to 8 rows both parts of h have
+      // columns in one product, h's rests those from 8 on.
+      const int row = min(kBoth ? c & 7 : c, rows - 1);
+      const uint32_t a_at = uint32_t(kRowsAt + kRowBytes * row) + (kBoth && c >= 8 ? 1024u * kOfPlane : 0u);
       const int x0 = spread(row);
       f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
       const int n_steps = DOWN ? t.size : steps;
@@ -340,7 +337,7 @@ __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds
         if (more) wait_copies<(D - 1) * kOps>();
         else wait_copies<0>();
         const unsigned char* st = ring + stage * kStage;
-        u32x4_t w[kParts], b[kParts][4][kPlanes];
+        u32x4_t w[kParts], b[kParts][4][kReads];
         uint32_t e8[kParts];
 #pragma unroll
         for (int i = 0; i < kParts; ++i) {
@@ -349,7 +346,7 @@ __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
 #pragma unroll
-            for (int p = 0; p < kPlanes; ++p)
+            for (int p = 0; p < kReads; ++p)
               b[i][j][p] = *reinterpret_cast<const u32x4_t*>(st + a_at + 1024 * kOfPlane * p + 16 * ((16 * i + 4 * g + j) ^ x0));
           }
         }
@@ -363,23 +360,29 @@ __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds
           for (int j = 0; j < 4; ++j) {
             const bf16x8_t v = __builtin_bit_cast(bf16x8_t, mxfp4_word_to_bf16x8(w[i][j], scale));
 #pragma unroll
-            for (int p = 0; p < kPlanes; ++p)
+            for (int p = 0; p < kReads; ++p)
               acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, __builtin_bit_cast(bf16x8_t, b[i][j][p]), acc, 0, 0, 0);
           }
         }
       }
       if (DOWN) {
-        if (has) {
-          const float weight = T.row_weight[at + row];
+        // to the lanes of the rows' tokens: column c is token c
+        const uint32_t m = T.tokens[t.j];
+        const int from = __builtin_popcount(m & ((1u << c) - 1u));
+        const bool has = m >> c & 1u;
+        const float weight = has ? T.row_weight[at + from] : 0.f;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sum[e] = __builtin_fmaf(weight, acc[e], sum[e]);
+        for (int e = 0; e < 4; ++e) {
+          float v = __shfl(acc[e], 16 * g + from);
+          if (kBoth) v += __shfl(acc[e], 16 * g + from + 8);
+          sum[e] = has ? __builtin_fmaf(weight, v, sum[e]) : sum[e];
         }
       } else {
         // gate rows in the lanes with g < 2, the same outputs' up rows 32 lanes on
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float v = silu(acc[e]) * __shfl_xor(acc[e], 32);
-          if (has && g < 2 && 4 * g + e < t.size) {
+          if (c < rows && g < 2 && 4 * g + e < t.size) {
             // the nearest bf16 and what it leaves: 16 bits of v, so that out has its own rounding alone
             const uint32_t hi = pack_bf16x2(v, v) & 0xffffu;
             const float rest = __builtin_isfinite(v) ? v - bf16_lo(hi) : 0.f;
