@@ -7,20 +7,31 @@
 // Bound by the chosen experts' bytes, read once each whatever the tokens.  Every workgroup
 // (one a CU) makes the choice itself, a wave a token: a launch of its own would take as long
 // as the layer's start.  The second kernel reads the choice that the first one's workgroup 0
-// has written.  From the choice follows a table of the chosen experts, ascending, and of each
-// one's tokens.
+// has written.  From the choice follow, by a bit for each token of an expert and one scan, the
+// groups of rows that the waves work on.
 //
-// Work is dealt out to waves in tasks of 16 weight rows of an expert: 8 gate rows and the 8 up
-// rows of the same outputs in the first kernel, whose sums meet in registers; 16 output columns
-// in the second, where a workgroup has all experts of its columns (and, where they are few, parts
-// of the reduction axis), its waves' weighted sums meet in LDS in the waves' order, and nothing
+// A wave goes through its pieces of work (first kernel: up to 8 gate rows and the 8 up rows of
+// the same outputs, whose sums meet in registers; second: a share of the steps of a block of
+// up to 16 columns over all experts) as one sequence of steps of 256 codes: weights, exponents
+// and the group's activation rows of a step come through a private LDS ring (global -> LDS, no
+// registers, no barriers), the copies a whole ring ahead, across the borders of pieces.  A
+// copy takes a CU 25 to 30 clocks whatever its size, which counts where a wave has few steps,
+// so a step has as few as possible: with groups of two rows four for 256 codes (steps of 128
+// codes had six: 38.3 and 32.8 us at one token, 174 and 147 at 16, as below), and none past
+// the work.  A lane's 16-byte piece of weights is a block of 32 codes, converted exactly to bf16 for
+// four v_mfma_f32_16x16x32_bf16 with 16 weight rows (A operand) and the group's rows (B
+// operand).  The second kernel's waves' weighted sums meet in LDS in the waves' order: nothing
 // depends on timing.
 //
-// A wave goes through its tasks as one sequence of steps of 128 codes: weights, exponents and
-// the expert's activation rows of a step come through a private LDS ring (global -> LDS, no
-// registers, no barriers), the copies a whole ring ahead, across the borders of tasks.  A
-// lane's 16-byte piece of weights is a block of 32 codes, converted exactly to bf16 for four
-// v_mfma_f32_16x16x32_bf16 with 16 weight rows (A operand) and the tokens (B operand).
+// h is kept in two bf16 parts: rounded to one, the output's error against 64 bits was up to 1.55
+// times that of its own rounding, now 1.0 (second kernel 48 -> 54 us at 16 tokens, 11.7 -> 11.4
+// at one).
+//
+// Measured, back to back (the two kernels by themselves): one token, 8 of 256 experts of 3584 x
+// 2048: 31.7 us (20.2 and 11.4; 93.6 MB, 2.95 TB/s: 3.7 us choice and 1.3 tables, then 62 MB at
+// 5.2 TB/s; 3 us before the second one's first copy), 2 tokens, 2 of 8, 1024 x 512: 15.7, 7
+// tokens, 4 of 60, 2080 x 1056: 35.5, 16 tokens, 8 of 64, 3584 x 2048: 151 (98 and 53; 666 MB,
+// 4.4 TB/s), 8 of 256: 230 (5.2 TB/s).
 #include <hip/hip_runtime.h>
 
 #include "qmm_device.h"
@@ -72,7 +83,9 @@ __device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
 
 // The tables from ids; every thread of the workgroup calls it.  An expert's rows are taken in
 // groups of up to 2 << kind, each of which reads the expert's weights: the fewer rows a step
-// of the ring holds, the more steps it has.  `tokens` is scratch for n_experts words: which
+// of the ring holds, the fewer copies it takes and the more steps fit.  The smallest kind with
+// at most 1.25 groups an expert: 16 tokens, 8 of 64 experts of 3584 x 2048, 155 us so (groups
+// of 4) and 181 with up to 1.5 (groups of 2).  `tokens` is scratch for n_experts words: which
 // tokens an expert has, a bit each, and its first row in the upper half.  Thread i counts for
 // experts 2i and 2i + 1; the counts of all kinds go through one scan, 10 bits each.
 __device__ __forceinline__ void make_tables(LayerTables& T, const LayerChoice& C, uint32_t* tokens, int pairs, int k, int ne) {
@@ -240,13 +253,14 @@ __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds
   const int part = lane % kParts;                 // of a step's exponents
   int c_round = 0, c_pos = begin, c_h = 0, c_to = 0;
   __amdgpu_buffer_rsrc_t cr = make_rsrc(stack, 0), mr = cr;
-  uint32_t w_full[kParts], w_last[kParts], m_full = 0, m_last = 0, aoff[kOfPlane];
+  uint32_t w_full[kParts], w_last[kParts], m_full = 0, m_last = 0, aoff[kCopies];
 #pragma unroll
-  for (int i = 0; i < kOfPlane; ++i) aoff[i] = kOOB8;
+  for (int i = 0; i < kCopies; ++i) aoff[i] = kOOB8;
 #pragma unroll
   for (int i = 0; i < kParts; ++i) w_full[i] = w_last[i] = kOOB8;
-  auto copied_row = [&](int i) { return kPerCopy * i + lane / kPieces; };
-  auto copied_at = [&](int i) { return 8 * ((lane % kPieces) ^ spread(copied_row(i))); };   // code
+  auto copied_row = [&](int i) { return kPerCopy * (i % kOfPlane) + lane / kPieces; };
+  auto column = [&](int i) { return copied_row(i) + (kBoth && i >= kOfPlane ? 8 : 0); };
+  auto copied_at = [&](int i) { return 8 * ((lane % kPieces) ^ spread(column(i))); };       // code
   auto open = [&]() {
     const Piece t = piece_at(c_pos);
     int e = __builtin_amdgcn_readfirstlane(T.expert[t.j]), at = __builtin_amdgcn_readfirstlane(T.first[t.j]);
@@ -257,9 +271,9 @@ __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds
     cr = make_rsrc(blob + kHeaderBytes, codes_bytes);
     mr = make_rsrc(blob + meta_offset, meta_bytes);
     // row r of the 16: columns of the block, or 8 outputs' gate rows and their up rows
-    const int column = (int(blockIdx.x) + c_round * int(gridDim.x)) * a.cols;
-    const int rows = DOWN ? min(a.cols, a.d - column) : t.size;
-    auto row = [&](int r) { return uint32_t(DOWN ? column + r : t.at + (r & 7) + (r >= 8 ? a.inter : 0)); };
+    const int n0 = (int(blockIdx.x) + c_round * int(gridDim.x)) * a.cols;
+    const int rows = DOWN ? min(a.cols, a.d - n0) : t.size;
+    auto row = [&](int r) { return uint32_t(DOWN ? n0 + r : t.at + (r & 7) + (r >= 8 ? a.inter : 0)); };
     auto any = [&](int r) { return (DOWN ? r : r & 7) < rows; };
 #pragma unroll
     for (int i = 0; i < kParts; ++i) {
@@ -271,9 +285,9 @@ __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds
     m_full = meta ? (row(mr16) >> 2) * mquad + (row(mr16) & 3u) * mrow + 4u * uint32_t(part) : kOOB8;
     m_last = meta ? (row(mr16) >> 2) * mquad + (row(mr16) & 3u) * mrow_last + 4u * uint32_t(part) : kOOB8;
 #pragma unroll
-    for (int i = 0; i < kOfPlane; ++i) {
+    for (int i = 0; i < kCopies; ++i) {
       const int r = at + copied_row(i), q = min(r, kLayerMaxPairs - 1);
-      aoff[i] = r < stop ? uint32_t(DOWN ? q : T.token[q]) * row_bytes + 2u * uint32_t(copied_at(i)) : kOOB8;
+      aoff[i] = r < stop ? uint32_t(DOWN ? q : T.token[q]) * row_bytes + 2u * uint32_t(copied_at(i)) + (i < kOfPlane ? 0u : plane) : kOOB8;
     }
     c_h = DOWN ? t.at : 0;
     c_to = DOWN ? t.at + t.size : steps;
@@ -289,8 +303,8 @@ __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds
                          uint32_t(s) * slab_bytes + uint32_t(CODES / 2 * in_slab), at + 1024u * uint32_t(i));
 #pragma unroll
     for (int i = 0; i < kCopies; ++i)
-      copy16_to_lds_from(ar, aoff[i % kOfPlane] | (CODES * h + copied_at(i % kOfPlane) < axis ? 0u : kOOB8),
-                         uint32_t(kRowBytes * h) + (i < kOfPlane ? 0u : plane), at + kRowsAt + 1024u * uint32_t(i));
+      copy16_to_lds_from(ar, aoff[i] | (CODES * h + copied_at(i) < axis ? 0u : kOOB8), uint32_t(kRowBytes * h),
+                         at + kRowsAt + 1024u * uint32_t(i));
     copy4_to_lds(mr, ((s == last ? m_last : m_full) + uint32_t(64 * s + CODES / 32 * in_slab)) |
                          (CODES * h + 128 * part < axis ? 0u : kOOB8), at + kMetaAt);
     if (++c_h == c_to) {
@@ -326,7 +340,7 @@ __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds
       // columns in one product, h's rests those from 8 on.
       const int row = min(kBoth ? c & 7 : c, rows - 1);
       const uint32_t a_at = uint32_t(kRowsAt + kRowBytes * row) + (kBoth && c >= 8 ? 1024u * kOfPlane : 0u);
-      const int x0 = spread(row);
+      const int x0 = spread(row + (kBoth && c >= 8 ? 8 : 0));
       f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
       const int n_steps = DOWN ? t.size : steps;
       for (int h = 0; h < n_steps; ++h) {
@@ -419,6 +433,7 @@ __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds
 
 template <bool DOWN>
 __device__ __forceinline__ void stream_any(const MoeLayerArgs& a, unsigned char* lds, LayerTables& T) {
+  // with 8 and 16 rows steps of 128 codes: of 256 the ring would hold one or two
   const int kind = __builtin_amdgcn_readfirstlane(T.kind);
   if (kind == 0) stream<DOWN, 2, 256>(a, lds, T);
   else if (kind == 1) stream<DOWN, 4, 256>(a, lds, T);
