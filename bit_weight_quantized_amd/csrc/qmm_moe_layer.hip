@@ -399,7 +399,7 @@ __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds
           if (c < rows && g < 2 && 4 * g + e < t.size) {
             // the nearest bf16 and what it leaves: 16 bits of v, so that out has its own rounding alone
             const uint32_t hi = pack_bf16x2(v, v) & 0xffffu;
-            const float rest = __builtin_isfinite(v) ? v - bf16_lo(hi) : 0.f;
+            const float rest = __builtin_isfinite(bf16_lo(hi)) ? v - bf16_lo(hi) : 0.f;
             const int64_t o = int64_t(at + row) * a.inter + t.at + 4 * g + e;
             a.h[o] = uint16_t(hi);
             a.h[o + int64_t(a.t) * a.k * a.inter] = uint16_t(pack_bf16x2(rest, rest));
