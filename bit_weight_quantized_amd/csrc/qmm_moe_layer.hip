@@ -156,29 +156,42 @@ __device__ __forceinline__ void make_tables(LayerTables& T, const LayerChoice& C
   __syncthreads();
 }
 
-// One wave's choice for one token.
-template <int J, bool SIGMOID>
+// One wave's choice for token tok, or for it and the wave's second one.
+template <int J, bool SIGMOID, int N>
 __device__ __forceinline__ void choose(const MoeLayerArgs& a, int tok, float* mine, LayerChoice& C) {
   const int lane = threadIdx.x & 63;
   const TopkRule rule = topk_rule<J, SIGMOID>(a.n_experts, a.k, a.bias != nullptr, a.groups, a.keep, a.top2, a.renorm);
-  float l[J];
+  float l[N][J], b[J];
 #pragma unroll
-  for (int j = 0; j < J; ++j) {
-    const int e = J * lane + j;
-    const int64_t at = int64_t(tok) * a.ld + min(e, a.n_experts - 1);
-    const float v = a.bf16 ? logit<true>(a.logits, at) : logit<false>(a.logits, at);
-    l[j] = e < a.n_experts ? v : -INFINITY;
-  }
-  float b[J];
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const int e = J * lane + j;
+      const int64_t at = int64_t(tok + kLayerWaves * n) * a.ld + min(e, a.n_experts - 1);
+      const float v = a.bf16 ? logit<true>(a.logits, at) : logit<false>(a.logits, at);
+      l[n][j] = e < a.n_experts ? v : -INFINITY;
+    }
 #pragma unroll
   for (int j = 0; j < J; ++j) b[j] = a.bias ? a.bias[min(J * lane + j, a.n_experts - 1)] : 0.f;
-  const TopkChoice c = topk_wave<J, SIGMOID>(
+  TopkChoice c[N];
+  topk_wave<J, SIGMOID, J <= 4>(
       l, rule, [&](int j) { return b[j]; },
-      [&](int j) { return min(J * lane + j, a.n_experts - 1) / rule.gs * rule.per; }, mine);
-  if (lane < a.k) {
-    C.ids[tok * a.k + lane] = c.expert;
-    C.weights[tok * a.k + lane] = c.weight * a.scale;
-  }
+      [&](int j) { return min(J * lane + j, a.n_experts - 1) / rule.gs * rule.per; }, mine, c);
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+    if (lane < a.k) {
+      const int p = (tok + kLayerWaves * n) * a.k + lane;
+      C.ids[p] = c[n].expert;
+      C.weights[p] = c[n].weight * a.scale;
+    }
+}
+
+template <int J, bool SIGMOID>
+__device__ __forceinline__ void choose_all(const MoeLayerArgs& a, int wave, float* mine, LayerChoice& C) {
+  static_assert(kLayerMaxTokens <= 2 * kLayerWaves, "a wave has up to two tokens");
+  static_assert(2 * 64 * J * 4 <= kLayerRing, "LDS");
+  if (wave + kLayerWaves < a.t) choose<J, SIGMOID, 2>(a, wave, mine, C);
+  else if (wave < a.t) choose<J, SIGMOID, 1>(a, wave, mine, C);
 }
 
 // 16-byte pieces of a row of 128 activations lie in LDS at piece ^ spread(row): 16 lanes that
@@ -447,14 +460,12 @@ __global__ __launch_bounds__(64 * kLayerWaves) void layer_gate_up_kernel(MoeLaye
   LayerChoice& C = *reinterpret_cast<LayerChoice*>(lds + kLayerRed);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   float* mine = reinterpret_cast<float*>(lds + wave * kLayerRing);
-  for (int tok = wave; tok < a.t; tok += kLayerWaves) {
-    if (a.n_experts <= 256) {
-      if (a.sigmoid) choose<4, true>(a, tok, mine, C);
-      else choose<4, false>(a, tok, mine, C);
-    } else {
-      if (a.sigmoid) choose<16, true>(a, tok, mine, C);
-      else choose<16, false>(a, tok, mine, C);
-    }
+  if (a.n_experts <= 256) {
+    if (a.sigmoid) choose_all<4, true>(a, wave, mine, C);
+    else choose_all<4, false>(a, wave, mine, C);
+  } else {
+    if (a.sigmoid) choose_all<16, true>(a, wave, mine, C);
+    else choose_all<16, false>(a, wave, mine, C);
   }
   __syncthreads();
   const int pairs = a.t * a.k, tid = threadIdx.x;

@@ -460,20 +460,21 @@ __global__ __launch_bounds__(64 * WAVES) void topk_kernel(TopkArgs a, int chunk)
   __syncthreads();
 
   for (int64_t tok = t0 + wave; tok < t1; tok += WAVES) {
-    float l[J];
+    float l[1][J];
     if constexpr (!kKeep) {
       asm volatile("" : "+v"(base));              // what hangs on it is not kept from token to token
       load(tok);
     }
 #pragma unroll
-    for (int j = 0; j < J; ++j) l[j] = next[j];
+    for (int j = 0; j < J; ++j) l[0][j] = next[j];
     if (kKeep && tok + WAVES < t1) load(tok + WAVES);
-    const TopkChoice choice = topk_wave<J, SIGMOID>(l, rule, [&](int j) { return kKeep ? bias[j] : bias_of(j); },
-                                                    [&](int j) { return kKeep ? gid[j] : first_lane(j); }, cs[wave]);
-    const int mine_e = choice.expert;
+    TopkChoice choice[1];
+    topk_wave<J, SIGMOID, false>(l, rule, [&](int j) { return kKeep ? bias[j] : bias_of(j); },
+                                 [&](int j) { return kKeep ? gid[j] : first_lane(j); }, cs[wave], choice);
+    const int mine_e = choice[0].expert;
     if (lane < k) {
       a.topk[tok * k + lane] = mine_e;
-      a.weights[tok * k + lane] = choice.weight * a.scale;
+      a.weights[tok * k + lane] = choice[0].weight * a.scale;
       if (mine_e >= 0) atomicAdd(&lds.count[mine_e], 1);
       if constexpr (ONE) chosen[(tok - t0) * k + lane] = mine_e;
     }
