@@ -246,15 +246,27 @@ __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds
   const int blocks = DOWN ? (a.d + a.cols - 1) / a.cols : 0;
   const int rounds = DOWN ? (blocks - int(blockIdx.x) + int(gridDim.x) - 1) / int(gridDim.x) : 1;
   struct Piece {
-    int j, at, size, next;    // group, first output or step in it, outputs or steps; what follows
+    int pos, j, at;     // in the work; its group, and its place in it
+    // its first output or step, and how many it has
+    __device__ int from(int outputs) const { return DOWN ? at : at * outputs; }
   };
-  auto piece_at = [&](int pos) {
-    const int j = pos / of_group, at = pos - j * of_group;
+  auto size = [&](const Piece& p) { return DOWN ? min(end - p.pos, steps - p.at) : min(outputs, a.inter - p.at * outputs); };
+  const Piece start{begin, begin / of_group, begin % of_group};
+  const int hop_j = waves / of_group, hop_at = waves % of_group;
+  auto advance = [&](Piece& p) {
     if (DOWN) {
-      const int size = min(end - pos, of_group - at);
-      return Piece{j, at, size, pos + size};
+      p.pos += size(p);
+      p.at = 0;
+      ++p.j;
+      return;
     }
-    return Piece{j, at * outputs, min(outputs, a.inter - at * outputs), pos + waves};
+    p.pos += waves;
+    p.at += hop_at;
+    p.j += hop_j;
+    if (p.at >= of_group) {
+      p.at -= of_group;
+      ++p.j;
+    }
   };
 
   // ---- the copies' place in the sequence
@@ -264,7 +276,8 @@ __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds
   auto wrow = [&](int i) { return kRowsOf * i + lane / kRowPieces; };
   auto wpiece = [&](int i) { return (lane % kRowPieces) ^ (wrow(i) >> 1 & (kRowPieces - 1)); };
   const int part = lane % kParts;                 // of a step's exponents
-  int c_round = 0, c_pos = begin, c_h = 0, c_to = 0;
+  int c_round = 0, c_h = 0, c_to = 0;
+  Piece next = start;
   __amdgpu_buffer_rsrc_t cr = make_rsrc(stack, 0), mr = cr;
   uint32_t w_full[kParts], w_last[kParts], m_full = 0, m_last = 0, aoff[kCopies];
 #pragma unroll
@@ -275,9 +288,9 @@ __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds
   auto column = [&](int i) { return copied_row(i) + (kBoth && i >= kOfPlane ? 8 : 0); };
   auto copied_at = [&](int i) { return 8 * ((lane % kPieces) ^ spread(column(i))); };       // code
   auto open = [&]() {
-    const Piece t = piece_at(c_pos);
-    int e = __builtin_amdgcn_readfirstlane(T.expert[t.j]), at = __builtin_amdgcn_readfirstlane(T.first[t.j]);
-    int stop = __builtin_amdgcn_readfirstlane(T.first[t.j + 1]);
+    int e = __builtin_amdgcn_readfirstlane(T.expert[next.j]), at = __builtin_amdgcn_readfirstlane(T.first[next.j]);
+    int stop = __builtin_amdgcn_readfirstlane(T.first[next.j + 1]);
+    const int from = next.from(outputs), many = size(next);
     // wait states between these, which vector instructions write, and the copies that read what follows from them
     asm volatile("s_nop 4" : "+s"(e), "+s"(at), "+s"(stop));
     const uint8_t* blob = stack + int64_t(e) * stride;
@@ -285,8 +298,8 @@ __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds
     mr = make_rsrc(blob + meta_offset, meta_bytes);
     // row r of the 16: columns of the block, or 8 outputs' gate rows and their up rows
     const int n0 = (int(blockIdx.x) + c_round * int(gridDim.x)) * a.cols;
-    const int rows = DOWN ? min(a.cols, a.d - n0) : t.size;
-    auto row = [&](int r) { return uint32_t(DOWN ? n0 + r : t.at + (r & 7) + (r >= 8 ? a.inter : 0)); };
+    const int rows = DOWN ? min(a.cols, a.d - n0) : many;
+    auto row = [&](int r) { return uint32_t(DOWN ? n0 + r : from + (r & 7) + (r >= 8 ? a.inter : 0)); };
     auto any = [&](int r) { return (DOWN ? r : r & 7) < rows; };
 #pragma unroll
     for (int i = 0; i < kParts; ++i) {
@@ -302,9 +315,9 @@ __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds
       const int r = at + copied_row(i), q = min(r, kLayerMaxPairs - 1);
       aoff[i] = r < stop ? uint32_t(DOWN ? q : T.token[q]) * row_bytes + 2u * uint32_t(copied_at(i)) + (i < kOfPlane ? 0u : plane) : kOOB8;
     }
-    c_h = DOWN ? t.at : 0;
-    c_to = DOWN ? t.at + t.size : steps;
-    c_pos = t.next;
+    c_h = DOWN ? from : 0;
+    c_to = DOWN ? from + many : steps;
+    advance(next);
   };
   bool more = rounds > 0 && begin < end;          // copies left
   auto copies = [&](int stage) {
@@ -321,8 +334,8 @@ __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds
     copy4_to_lds(mr, ((s == last ? m_last : m_full) + uint32_t(64 * s + CODES / 32 * in_slab)) |
                          (CODES * h + 128 * part < axis ? 0u : kOOB8), at + kMetaAt);
     if (++c_h == c_to) {
-      if (c_pos >= end) {
-        c_pos = begin;
+      if (next.pos >= end) {
+        next = start;
         more = ++c_round < rounds;
       }
       if (more) open();
@@ -341,21 +354,20 @@ __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds
   const bool in_turns = mine > 40;
   if (wave >= kLayerWaves / 2) __builtin_amdgcn_s_setprio(1);
 
+  // A column of the products is a row of the group (zeros past it); with up to 8 rows both
+  // parts of h have columns in one product, h's rests those from 8 on.
+  const int row = min(kBoth ? c & 7 : c, ROWS - 1);
+  const uint32_t a_at = uint32_t(kRowsAt + kRowBytes * row) + (kBoth && c >= 8 ? 1024u * kOfPlane : 0u);
+  const int x0 = spread(row + (kBoth && c >= 8 ? 8 : 0));
+
   int stage = 0;
   f32x4_t* red = reinterpret_cast<f32x4_t*>(lds + kLayerRed);
   for (int round = 0; round < rounds; ++round) {
     f32x4_t sum = {0.f, 0.f, 0.f, 0.f};           // token c, columns 4g .. 4g + 3
-    for (int pos = begin; pos < end;) {
-      const Piece t = piece_at(pos);
-      pos = t.next;
-      const int at = T.first[t.j], rows = T.first[t.j + 1] - at;
-      // A column of the products is a row of the group; with up to 8 rows both parts of h have
-      // columns in one product, h's rests those from 8 on.
-      const int row = min(kBoth ? c & 7 : c, rows - 1);
-      const uint32_t a_at = uint32_t(kRowsAt + kRowBytes * row) + (kBoth && c >= 8 ? 1024u * kOfPlane : 0u);
-      const int x0 = spread(row + (kBoth && c >= 8 ? 8 : 0));
+    for (Piece t = start; t.pos < end; advance(t)) {
+      const int from = t.from(outputs), many = size(t);
       f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-      const int n_steps = DOWN ? t.size : steps;
+      const int n_steps = DOWN ? many : steps;
       for (int h = 0; h < n_steps; ++h) {
         if (in_turns && wave < kLayerWaves / 2) {
           if (h & 1) __builtin_amdgcn_s_setprio(1);
@@ -395,25 +407,26 @@ __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds
       if (DOWN) {
         // to the lanes of the rows' tokens: column c is token c
         const uint32_t m = T.tokens[t.j];
-        const int from = __builtin_popcount(m & ((1u << c) - 1u));
+        const int of_token = __builtin_popcount(m & ((1u << c) - 1u));
         const bool has = m >> c & 1u;
-        const float weight = has ? T.row_weight[at + from] : 0.f;
+        const float weight = has ? T.row_weight[T.first[t.j] + of_token] : 0.f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          float v = __shfl(acc[e], 16 * g + from);
-          if (kBoth) v += __shfl(acc[e], 16 * g + from + 8);
+          float v = __shfl(acc[e], 16 * g + of_token);
+          if (kBoth) v += __shfl(acc[e], 16 * g + of_token + 8);
           sum[e] = has ? __builtin_fmaf(weight, v, sum[e]) : sum[e];
         }
       } else {
         // gate rows in the lanes with g < 2, the same outputs' up rows 32 lanes on
+        const int at = T.first[t.j], rows = T.first[t.j + 1] - at;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float v = silu(acc[e]) * __shfl_xor(acc[e], 32);
-          if (c < rows && g < 2 && 4 * g + e < t.size) {
+          if (c < rows && g < 2 && 4 * g + e < many) {
             // the nearest bf16 and what it leaves: 16 bits of v, so that out has its own rounding alone
             const uint32_t hi = pack_bf16x2(v, v) & 0xffffu;
             const float rest = __builtin_isfinite(bf16_lo(hi)) ? v - bf16_lo(hi) : 0.f;
-            const int64_t o = int64_t(at + row) * a.inter + t.at + 4 * g + e;
+            const int64_t o = int64_t(at + c) * a.inter + from + 4 * g + e;
             a.h[o] = uint16_t(hi);
             a.h[o + int64_t(a.t) * a.k * a.inter] = uint16_t(pack_bf16x2(rest, rest));
           }
