@@ -28,10 +28,10 @@
 // at one).
 //
 // Measured, back to back (the two kernels by themselves): one token, 8 of 256 experts of 3584 x
-// 2048: 31.7 us (20.2 and 11.4; 93.6 MB, 2.95 TB/s: 3.7 us choice and 1.3 tables, then 62 MB at
-// 5.2 TB/s; 3 us before the second one's first copy), 2 tokens, 2 of 8, 1024 x 512: 15.7, 7
-// tokens, 4 of 60, 2080 x 1056: 35.5, 16 tokens, 8 of 64, 3584 x 2048: 151 (98 and 53; 666 MB,
-// 4.4 TB/s), 8 of 256: 230 (5.2 TB/s).
+// 2048: 30.3 us (18.7 and 11.2; 93.6 MB, 3.1 TB/s: 3 us choice and 1 tables, then 62 MB at 5 TB/s;
+// 3 us before the second one's first copy), 2 tokens, 2 of 8, 1024 x 512: 14.0, 4 tokens, 8 of
+// 128, 2048 x 768: 30.5, 7 tokens, 4 of 60, 2080 x 1056: 32.4, 16 tokens, 8 of 64, 3584 x 2048:
+// 146 (93 and 53; 666 MB, 4.6 TB/s), 8 of 256: 224 (5.3 TB/s).
 #include <hip/hip_runtime.h>
 
 #include "qmm_device.h"
@@ -49,6 +49,8 @@ namespace {
 
 constexpr int kLayerWaves = 8;
 constexpr int kLayerRing = 3 * 6400;      // a wave's ring
+constexpr int kLayerTokens = 8 * 1024;    // in the first wave's ring, before it is one: masks of the experts' tokens
+static_assert(kLayerTokens + 4 * kRouteMaxExperts <= kLayerRing, "LDS");
 constexpr int kRowKinds = 4;              // groups of up to 2, 4, 8 or 16 rows
 
 struct LayerChoice {
@@ -81,21 +83,22 @@ __device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
   return v + __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);
 }
 
+__device__ __forceinline__ void clear_tokens(uint32_t* tokens, int ne) {
+  for (int e = threadIdx.x; e < ne; e += 64 * kLayerWaves) tokens[e] = 0u;
+  __syncthreads();
+}
+
 // The tables from ids; every thread of the workgroup calls it.  An expert's rows are taken in
 // groups of up to 2 << kind, each of which reads the expert's weights: the fewer rows a step
 // of the ring holds, the fewer copies it takes and the more steps fit.  The smallest kind with
 // at most 1.25 groups an expert: 16 tokens, 8 of 64 experts of 3584 x 2048, 155 us so (groups
-// of 4) and 181 with up to 1.5 (groups of 2).  `tokens` is scratch for n_experts words: which
-// tokens an expert has, a bit each, and its first row in the upper half.  Thread i counts for
-// experts 2i and 2i + 1; the counts of all kinds go through one scan, 10 bits each.
+// of 4) and 181 with up to 1.5 (groups of 2).  `tokens`, n_experts words, has
+// which tokens an expert has, a bit each, and gets its first row in the upper half.  Thread i
+// counts for experts 2i and 2i + 1; the counts of all kinds go through one scan, 10 bits each.
 __device__ __forceinline__ void make_tables(LayerTables& T, const LayerChoice& C, uint32_t* tokens, int pairs, int k, int ne) {
   static_assert(kRouteMaxExperts <= 2 * 64 * kLayerWaves, "a thread has two experts");
   const int tid = threadIdx.x, wave = tid >> 6;
-  for (int e = tid; e < ne; e += 64 * kLayerWaves) tokens[e] = 0u;
-  __syncthreads();
   const int id = tid < pairs ? C.ids[tid] : -1, tok = tid / k;
-  if (id >= 0) atomicOr(&tokens[id], 1u << tok);
-  __syncthreads();
   uint32_t mask[2], a = 0, b = 0;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -158,7 +161,7 @@ __device__ __forceinline__ void make_tables(LayerTables& T, const LayerChoice& C
 
 // One wave's choice for token tok, or for it and the wave's second one.
 template <int J, bool SIGMOID, int N>
-__device__ __forceinline__ void choose(const MoeLayerArgs& a, int tok, float* mine, LayerChoice& C) {
+__device__ __forceinline__ void choose(const MoeLayerArgs& a, int tok, float* mine, LayerChoice& C, uint32_t* tokens) {
   const int lane = threadIdx.x & 63;
   const TopkRule rule = topk_rule<J, SIGMOID>(a.n_experts, a.k, a.bias != nullptr, a.groups, a.keep, a.top2, a.renorm);
   float l[N][J], b[J];
@@ -183,15 +186,16 @@ __device__ __forceinline__ void choose(const MoeLayerArgs& a, int tok, float* mi
       const int p = (tok + kLayerWaves * n) * a.k + lane;
       C.ids[p] = c[n].expert;
       C.weights[p] = c[n].weight * a.scale;
+      if (c[n].expert >= 0) atomicOr(&tokens[c[n].expert], 1u << (tok + kLayerWaves * n));
     }
 }
 
 template <int J, bool SIGMOID>
-__device__ __forceinline__ void choose_all(const MoeLayerArgs& a, int wave, float* mine, LayerChoice& C) {
+__device__ __forceinline__ void choose_all(const MoeLayerArgs& a, int wave, float* mine, LayerChoice& C, uint32_t* tokens) {
   static_assert(kLayerMaxTokens <= 2 * kLayerWaves, "a wave has up to two tokens");
-  static_assert(2 * 64 * J * 4 <= kLayerRing, "LDS");
-  if (wave + kLayerWaves < a.t) choose<J, SIGMOID, 2>(a, wave, mine, C);
-  else if (wave < a.t) choose<J, SIGMOID, 1>(a, wave, mine, C);
+  static_assert(2 * 64 * J * 4 <= kLayerTokens, "LDS");
+  if (wave + kLayerWaves < a.t) choose<J, SIGMOID, 2>(a, wave, mine, C, tokens);
+  else if (wave < a.t) choose<J, SIGMOID, 1>(a, wave, mine, C, tokens);
 }
 
 // 16-byte pieces of a row of 128 activations lie in LDS at piece ^ spread(row): 16 lanes that
@@ -348,8 +352,8 @@ __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds
   // Of the two waves on a SIMD the one with the lower index issues its copies first and is done
   // earlier, and the tail has half the copies in flight.  The other half of the workgroup is
   // therefore raised; over many steps the first is too, every other step.  One token, 8 of 256
-  // experts of 3584x2048: 32.8 us without, 32.0 as it is, 32.6 in turns; 16 tokens, 8 of 256:
-  // 232.7, 232.5, 224.8.
+  // experts of 3584x2048 (before later steps): 32.8 us without, 32.0 as it is, 32.6 in turns; 16
+  // tokens, 8 of 256: 232.7, 232.5, 224.8.
   const int mine = DOWN ? end - begin : (work - begin + waves - 1) / waves * steps;
   const bool in_turns = mine > 40;
   if (wave >= kLayerWaves / 2) __builtin_amdgcn_s_setprio(1);
@@ -473,20 +477,25 @@ __global__ __launch_bounds__(64 * kLayerWaves) void layer_gate_up_kernel(MoeLaye
   LayerChoice& C = *reinterpret_cast<LayerChoice*>(lds + kLayerRed);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   float* mine = reinterpret_cast<float*>(lds + wave * kLayerRing);
+  uint32_t* tokens = reinterpret_cast<uint32_t*>(lds + kLayerTokens);
+  clear_tokens(tokens, a.n_experts);
   // experts a lane: as few as hold them (16 tokens, 6 of 300 experts of 512 x 256: 34.1 us with 8,
   // 40.1 with 16)
   if (a.n_experts <= 64) {
-    if (a.sigmoid) choose_all<1, true>(a, wave, mine, C);
-    else choose_all<1, false>(a, wave, mine, C);
+    if (a.sigmoid) choose_all<1, true>(a, wave, mine, C, tokens);
+    else choose_all<1, false>(a, wave, mine, C, tokens);
+  } else if (a.n_experts <= 128) {
+    if (a.sigmoid) choose_all<2, true>(a, wave, mine, C, tokens);
+    else choose_all<2, false>(a, wave, mine, C, tokens);
   } else if (a.n_experts <= 256) {
-    if (a.sigmoid) choose_all<4, true>(a, wave, mine, C);
-    else choose_all<4, false>(a, wave, mine, C);
+    if (a.sigmoid) choose_all<4, true>(a, wave, mine, C, tokens);
+    else choose_all<4, false>(a, wave, mine, C, tokens);
   } else if (a.n_experts <= 512) {
-    if (a.sigmoid) choose_all<8, true>(a, wave, mine, C);
-    else choose_all<8, false>(a, wave, mine, C);
+    if (a.sigmoid) choose_all<8, true>(a, wave, mine, C, tokens);
+    else choose_all<8, false>(a, wave, mine, C, tokens);
   } else {
-    if (a.sigmoid) choose_all<16, true>(a, wave, mine, C);
-    else choose_all<16, false>(a, wave, mine, C);
+    if (a.sigmoid) choose_all<16, true>(a, wave, mine, C, tokens);
+    else choose_all<16, false>(a, wave, mine, C, tokens);
   }
   __syncthreads();
   const int pairs = a.t * a.k, tid = threadIdx.x;
@@ -494,7 +503,7 @@ __global__ __launch_bounds__(64 * kLayerWaves) void layer_gate_up_kernel(MoeLaye
     a.topk[tid] = C.ids[tid];
     a.weights[tid] = C.weights[tid];
   }
-  make_tables(T, C, reinterpret_cast<uint32_t*>(lds), pairs, a.k, a.n_experts);
+  make_tables(T, C, tokens, pairs, a.k, a.n_experts);
   stream_any<false>(a, lds, T);
 }
 
@@ -503,12 +512,18 @@ __global__ __launch_bounds__(64 * kLayerWaves) void layer_down_kernel(MoeLayerAr
   LayerTables& T = *reinterpret_cast<LayerTables*>(lds + kLayerTables);
   LayerChoice& C = *reinterpret_cast<LayerChoice*>(lds + kLayerRed);
   const int pairs = a.t * a.k, tid = threadIdx.x;
+  uint32_t* tokens = reinterpret_cast<uint32_t*>(lds + kLayerTokens);
+  int e = -1;
   if (tid < pairs) {
-    const int e = a.topk[tid];
-    C.ids[tid] = e >= 0 && e < a.n_experts ? e : -1;
+    e = a.topk[tid];
+    e = e < a.n_experts ? e : -1;
+    C.ids[tid] = e;
     C.weights[tid] = a.weights[tid];
   }
-  make_tables(T, C, reinterpret_cast<uint32_t*>(lds), pairs, a.k, a.n_experts);
+  clear_tokens(tokens, a.n_experts);
+  if (e >= 0) atomicOr(&tokens[e], 1u << tid / a.k);
+  __syncthreads();
+  make_tables(T, C, tokens, pairs, a.k, a.n_experts);
   stream_any<true>(a, lds, T);
 }
 
