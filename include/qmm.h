@@ -558,9 +558,9 @@ size_t qmm_moe_layer_workspace_bytes(int64_t t, int32_t k, int64_t inter);
  *             up projection U), down [n_experts] of [d, inter], at strides of bytes as for
  *             qmm_grouped_gemm
  *   x bf16[t][d], 16-byte aligned; shared bf16[t][d] or NULL (may be out) and out 8-byte
- *   topk int32[t][k], weights fp32[t][k]: outputs
- *   ws        qmm_moe_layer_workspace_bytes(t, k, inter) bytes, 16-byte aligned; calls on
- *             different streams need one each
+ *   topk int32[t][k], weights fp32[t][k]: outputs, which the second launch reads
+ *   ws        qmm_moe_layer_workspace_bytes(t, k, inter) bytes, 16-byte aligned
+ * Calls that may run at the same time need ws, topk and weights of their own.
  * Limits: t <= 16 and t·k <= 256; d and inter multiples of 32, <= 65536; one matrix's codes
  * below 2 GiB; n_experts, k, n_groups as for qmm_route_topk.  t = 0 is a no-op.
  * QMM_AFFINE4_G64 returns QMM_E_UNSUPPORTED.  The order of every sum depends on the shape and
