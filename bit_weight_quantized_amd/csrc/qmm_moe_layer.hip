@@ -25,7 +25,7 @@
 //
 // h is kept in two bf16 parts: rounded to one, the output's error against 64 bits was up to 1.55
 // times that of its own rounding, now 1.0 (second kernel 48 -> 54 us at 16 tokens, 11.7 -> 11.4
-// at one).
+// at one).  In a workspace of half the size, which the call took first, it is one part.
 //
 // Measured, back to back (the two kernels by themselves): one token, 8 of 256 experts of 3584 x
 // 2048: 30.3 us (18.7 and 11.2; 93.6 MB, 3.1 TB/s: 3 us choice and 1 tables, then 62 MB at 5 TB/s;
@@ -203,16 +203,16 @@ __device__ __forceinline__ void choose_all(const MoeLayerArgs& a, int wave, floa
 // are then in different banks.
 __device__ __forceinline__ int spread(int row) { return (row & 7) | ((row >> 3 ^ row >> 2) & 1) << 3; }
 
-// The steps of a wave, CODES codes each, groups of up to ROWS tokens.
-template <bool DOWN, int ROWS, int CODES>
+// The steps of a wave, CODES codes each, groups of up to ROWS tokens.  PARTS: of h, in the second kernel.
+template <bool DOWN, int PARTS, int ROWS, int CODES>
 __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds, LayerTables& T) {
   constexpr int kParts = CODES / 128;             // 1 KB of weights each
   constexpr int kRowBytes = 2 * CODES, kPieces = kRowBytes / 16, kPerCopy = 1024 / kRowBytes;   // rows of activations
-  constexpr int kPlanes = DOWN ? 2 : 1, kOfPlane = ROWS / kPerCopy;   // h is in two bf16 parts
+  constexpr int kPlanes = DOWN ? PARTS : 1, kOfPlane = ROWS / kPerCopy;
   constexpr int kCopies = kPlanes * kOfPlane, kOps = kParts + kCopies + 1;
   constexpr int kRowsAt = 1024 * kParts, kMetaAt = kRowsAt + 1024 * kCopies, kStage = kMetaAt + 256;
   constexpr int D = kLayerRing / kStage;
-  constexpr bool kBoth = DOWN && ROWS <= 8;
+  constexpr bool kBoth = DOWN && PARTS == 2 && ROWS <= 8;
   constexpr int kReads = kBoth ? 1 : kPlanes;     // of a column
   static_assert((D - 1) * kOps <= 63, "the waits count the copies in flight");
   const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
@@ -229,7 +229,7 @@ __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds
   const uint8_t* stack = DOWN ? a.down : a.gate_up;
   const int64_t stride = DOWN ? a.down_stride : a.gate_up_stride;
   const uint32_t row_bytes = uint32_t(axis) * 2u;
-  const __amdgpu_buffer_rsrc_t ar = make_rsrc(DOWN ? a.h : a.x, uint32_t(DOWN ? 2 * a.t * a.k : a.t) * row_bytes);
+  const __amdgpu_buffer_rsrc_t ar = make_rsrc(DOWN ? a.h : a.x, uint32_t(DOWN ? PARTS * a.t * a.k : a.t) * row_bytes);
   const uint32_t plane = DOWN ? uint32_t(a.t * a.k) * row_bytes : 0u;
   unsigned char* ring = lds + wave * kLayerRing;
   const uint32_t ring_at = lds_addr(ring);
@@ -427,12 +427,14 @@ __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds
         for (int e = 0; e < 4; ++e) {
           const float v = silu(acc[e]) * __shfl_xor(acc[e], 32);
           if (c < rows && g < 2 && 4 * g + e < many) {
-            // the nearest bf16 and what it leaves: 16 bits of v, so that out has its own rounding alone
             const uint32_t hi = pack_bf16x2(v, v) & 0xffffu;
-            const float rest = __builtin_isfinite(bf16_lo(hi)) ? v - bf16_lo(hi) : 0.f;
             const int64_t o = int64_t(at + c) * a.inter + from + 4 * g + e;
             a.h[o] = uint16_t(hi);
-            a.h[o + int64_t(a.t) * a.k * a.inter] = uint16_t(pack_bf16x2(rest, rest));
+            if (a.parts == 2) {
+              // what the nearest bf16 leaves: 16 bits of v, so that out has its own rounding alone
+              const float rest = __builtin_isfinite(bf16_lo(hi)) ? v - bf16_lo(hi) : 0.f;
+              a.h[o + int64_t(a.t) * a.k * a.inter] = uint16_t(pack_bf16x2(rest, rest));
+            }
           }
         }
       }
@@ -461,14 +463,14 @@ __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds
   wait_copies<0>();
 }
 
-template <bool DOWN>
+template <bool DOWN, int PARTS>
 __device__ __forceinline__ void stream_any(const MoeLayerArgs& a, unsigned char* lds, LayerTables& T) {
   // with 8 and 16 rows steps of 128 codes: of 256 the ring would hold one or two
   const int kind = __builtin_amdgcn_readfirstlane(T.kind);
-  if (kind == 0) stream<DOWN, 2, 256>(a, lds, T);
-  else if (kind == 1) stream<DOWN, 4, 256>(a, lds, T);
-  else if (kind == 2) stream<DOWN, 8, 128>(a, lds, T);
-  else stream<DOWN, 16, 128>(a, lds, T);
+  if (kind == 0) stream<DOWN, PARTS, 2, 256>(a, lds, T);
+  else if (kind == 1) stream<DOWN, PARTS, 4, 256>(a, lds, T);
+  else if (kind == 2) stream<DOWN, PARTS, 8, 128>(a, lds, T);
+  else stream<DOWN, PARTS, 16, 128>(a, lds, T);
 }
 
 __global__ __launch_bounds__(64 * kLayerWaves) void layer_gate_up_kernel(MoeLayerArgs a) {
@@ -504,9 +506,10 @@ __global__ __launch_bounds__(64 * kLayerWaves) void layer_gate_up_kernel(MoeLaye
     a.weights[tid] = C.weights[tid];
   }
   make_tables(T, C, tokens, pairs, a.k, a.n_experts);
-  stream_any<false>(a, lds, T);
+  stream_any<false, 1>(a, lds, T);
 }
 
+template <int PARTS>
 __global__ __launch_bounds__(64 * kLayerWaves) void layer_down_kernel(MoeLayerArgs a) {
   extern __shared__ __attribute__((aligned(1024))) unsigned char lds[];
   LayerTables& T = *reinterpret_cast<LayerTables*>(lds + kLayerTables);
@@ -524,7 +527,7 @@ __global__ __launch_bounds__(64 * kLayerWaves) void layer_down_kernel(MoeLayerAr
   if (e >= 0) atomicOr(&tokens[e], 1u << tid / a.k);
   __syncthreads();
   make_tables(T, C, tokens, pairs, a.k, a.n_experts);
-  stream_any<true>(a, lds, T);
+  stream_any<true, PARTS>(a, lds, T);
 }
 
 }  // namespace
@@ -545,8 +548,8 @@ int launch_moe_layer(const MoeLayerArgs& args, void* stream) {
                         0, a);
   const int err = int(hipGetLastError());
   if (err) return err;
-  hipExtLaunchKernelGGL(layer_down_kernel, dim3(unsigned(std::min(cus, blocks))), block, kLayerLds, s, nullptr,
-                        static_cast<hipEvent_t>(pe.stop), 0, a);
+  hipExtLaunchKernelGGL(a.parts == 2 ? layer_down_kernel<2> : layer_down_kernel<1>, dim3(unsigned(std::min(cus, blocks))),
+                        block, kLayerLds, s, nullptr, static_cast<hipEvent_t>(pe.stop), 0, a);
   return int(hipGetLastError());
 }
 

@@ -16,9 +16,18 @@ def product(x, tol_x, w):
     return x @ w.T, tol_x @ np.abs(w).T + (33 + x.shape[1] / 16 + 16) * STEP * a
 
 
-def layer(x, gate_up, down, ids, weights, shared):
+def two_parts(h):
+    """What h is off by that is kept in two bf16 parts."""
+    return 2.0 ** -16 * h + 2.0 ** -132
+
+
+def one_part(h):
+    return 2.0 ** -8 * h + 2.0 ** -133
+
+
+def layer(x, gate_up, down, ids, weights, shared, kept=two_parts):
     """(out, tolerance of the bf16 output): gate_up[e] and down[e] dequantised matrices, ids
-    [t][k] (-1: none), weights [t][k]."""
+    [t][k] (-1: none), weights [t][k]; kept: what h of given magnitudes is off by in the workspace."""
     t, d = x.shape
     out, tol, mag = np.zeros((t, d)), np.zeros((t, d)), np.zeros((t, d))
     for i in range(t):
@@ -28,7 +37,7 @@ def layer(x, gate_up, down, ids, weights, shared):
             half = gate_up[e].shape[0] // 2
             s, ts = product(x[i:i + 1], np.zeros((1, d)), gate_up[e])
             h, th = swiglu(s[:, :half], s[:, half:], ts[:, :half], ts[:, half:])
-            th = th + 2.0 ** -16 * (np.abs(h) + th) + 2.0 ** -132     # kept in two bf16 parts
+            th = th + kept(np.abs(h) + th)
             y, ty = product(h, th, down[e])
             out[i] += weights[i, j] * y[0]
             tol[i] += abs(weights[i, j]) * ty[0]
