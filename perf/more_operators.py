@@ -216,7 +216,7 @@ def prepare(case, seed):
     s["bias"] = 0.1 * torch.randn(e, generator=g, device=DEV) if c["bias"] else None
     s["shared"] = _activations(g, t, d) if c["shared"] else None
     s["topk"], s["weights"] = empty(t, k, dtype=torch.int32), empty(t, k, dtype=torch.float32)
-    s["ws"] = empty(4 * t * k * i, dtype=u8)          # h of every slot to more than bf16, which costs out precision
+    s["ws"] = empty(2 * t * k * i, dtype=u8)          # h of every slot in bf16
     return s
 
 
