@@ -32,8 +32,8 @@ struct MoeLayerArgs {
   int32_t* topk;            // [t][k]
   float* weights;           // [t][k]
   uint16_t* out;            // [t][d]
-  uint16_t* h;              // [parts][t·k][inter], the workspace: bf16 parts, rows by expert, then token
-  int parts;                // 2, or 1 in a workspace of half the size
+  uint16_t* h;              // the workspace, rows by expert, then token: [2][t·k][inter] two bf16 parts, or
+  bool pairs;               // [t·k][inter] pairs with an exponent
   int cols;                 // columns of a workgroup in the second kernel, even, <= 16; set by the launch
 };
 int launch_moe_layer(const MoeLayerArgs& a, void* stream);

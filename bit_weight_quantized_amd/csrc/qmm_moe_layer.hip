@@ -25,7 +25,10 @@
 //
 // h is kept in two bf16 parts: rounded to one, the output's error against 64 bits was up to 1.55
 // times that of its own rounding, now 1.0 (second kernel 48 -> 54 us at 16 tokens, 11.7 -> 11.4
-// at one).  In a workspace of half the size, which the call took first, it is one part.
+// at one).  In a workspace of half the size, which the call took first, two neighbours share an
+// exponent and have 12 bits each; a wave takes a step's rows apart into the same two parts before it
+// reads operands (one token, 8 of 256 experts: 31.6 us, 16 of 8 of 64: 153).  One bf16 part takes 29.8
+// and 129 there, at 1.35 to 1.55 times the error.
 //
 // Measured, back to back (the two kernels by themselves): one token, 8 of 256 experts of 3584 x
 // 2048: 30.3 us (18.7 and 11.2; 93.6 MB, 3.1 TB/s: 3 us choice and 1 tables, then 62 MB at 5 TB/s;
@@ -203,17 +206,44 @@ __device__ __forceinline__ void choose_all(const MoeLayerArgs& a, int wave, floa
 // are then in different banks.
 __device__ __forceinline__ int spread(int row) { return (row & 7) | ((row >> 3 ^ row >> 2) & 1) << 3; }
 
-// The steps of a wave, CODES codes each, groups of up to ROWS tokens.  PARTS: of h, in the second kernel.
-template <bool DOWN, int PARTS, int ROWS, int CODES>
+// Two neighbours of h in 32 bits: whole numbers of 12 bits, the even one's lowest, and the exponent
+// byte, as fp32 has it, of their unit, 2^-10 of the larger one's binade.  0 stands for zeros.
+constexpr uint32_t kPairEnds = 0xFE000000u;       // from here on: pairs with an infinity, NaN
+__device__ __forceinline__ uint32_t pack_pair(float a, float b) {
+  const uint32_t most = umax(__float_as_uint(a) & 0x7FFFFFFFu, __float_as_uint(b) & 0x7FFFFFFFu);
+  if (most > 0x7F800000u) return 0xFF000000u;     // 0·inf, NaN
+  // the larger one to the next binade where it rounds there; no unit below fp32's smallest normal
+  const uint32_t unit = umax((most + 0x1000u) >> 23, 11u) - 10u;
+  const float per = __uint_as_float((254u - unit) << 23);
+  uint32_t qa = uint32_t(int(__builtin_rintf(a * per))), qb = uint32_t(int(__builtin_rintf(b * per)));
+  if (most == 0x7F800000u) {
+    // 2^11 - 1 times 2^127 is infinite; a number beside an infinity does not matter
+    auto end = [](float v) { return __builtin_isinf(v) ? v > 0.f ? 0x7FFu : 0x801u : 0u; };
+    return kPairEnds | end(b) << 12 | end(a);
+  }
+  return unit << 24 | (qb & 0xFFFu) << 12 | (qa & 0xFFFu);
+}
+// The pair as two bf16 parts each, exact: cut to 8 bits, and the rest (0 beside an infinity).
+__device__ __forceinline__ void pair_parts(uint32_t v, uint32_t& high, uint32_t& low) {
+  const float unit = __uint_as_float(v >> 1 & 0x7F800000u);
+  const uint32_t a = __float_as_uint(float(int(v << 20) >> 20) * unit), b = __float_as_uint(float(int(v << 8) >> 20) * unit);
+  auto rest = [](uint32_t p) { return __float_as_uint(__uint_as_float(p) - __uint_as_float(p & 0xFFFF0000u)); };
+  high = __builtin_amdgcn_perm(b, a, 0x07060302u);
+  low = __builtin_amdgcn_perm(rest(b), rest(a), 0x07060302u);
+}
+
+// The steps of a wave, CODES codes each, groups of up to ROWS tokens.  PAIRS: how the second kernel finds h.
+template <bool DOWN, bool PAIRS, int ROWS, int CODES>
 __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds, LayerTables& T) {
   constexpr int kParts = CODES / 128;             // 1 KB of weights each
   constexpr int kRowBytes = 2 * CODES, kPieces = kRowBytes / 16, kPerCopy = 1024 / kRowBytes;   // rows of activations
-  constexpr int kPlanes = DOWN ? PARTS : 1, kOfPlane = ROWS / kPerCopy;
+  constexpr int kPlanes = DOWN && !PAIRS ? 2 : 1, kOfPlane = ROWS / kPerCopy;   // as copied
   constexpr int kCopies = kPlanes * kOfPlane, kOps = kParts + kCopies + 1;
   constexpr int kRowsAt = 1024 * kParts, kMetaAt = kRowsAt + 1024 * kCopies, kStage = kMetaAt + 256;
-  constexpr int D = kLayerRing / kStage;
-  constexpr bool kBoth = DOWN && PARTS == 2 && ROWS <= 8;
-  constexpr int kReads = kBoth ? 1 : kPlanes;     // of a column
+  constexpr int kRests = DOWN && PAIRS ? 1024 * kOfPlane : 0;         // behind the ring: pairs' lower parts of a step
+  constexpr int D = (kLayerRing - kRests) / kStage;
+  constexpr bool kBoth = DOWN && ROWS <= 8;
+  constexpr int kReads = DOWN && !kBoth ? 2 : 1;  // of a column
   static_assert((D - 1) * kOps <= 63, "the waits count the copies in flight");
   const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -229,7 +259,7 @@ __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds
   const uint8_t* stack = DOWN ? a.down : a.gate_up;
   const int64_t stride = DOWN ? a.down_stride : a.gate_up_stride;
   const uint32_t row_bytes = uint32_t(axis) * 2u;
-  const __amdgpu_buffer_rsrc_t ar = make_rsrc(DOWN ? a.h : a.x, uint32_t(DOWN ? PARTS * a.t * a.k : a.t) * row_bytes);
+  const __amdgpu_buffer_rsrc_t ar = make_rsrc(DOWN ? a.h : a.x, uint32_t(DOWN ? kPlanes * a.t * a.k : a.t) * row_bytes);
   const uint32_t plane = DOWN ? uint32_t(a.t * a.k) * row_bytes : 0u;
   unsigned char* ring = lds + wave * kLayerRing;
   const uint32_t ring_at = lds_addr(ring);
@@ -243,6 +273,7 @@ __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds
     const int turns = (groups * (a.inter / 8) + waves - 1) / waves;
     outputs = max(1, (groups * a.inter + turns * waves - 1) / max(turns * waves, 1));
     while (outputs < 8 && groups * ((a.inter + outputs - 1) / outputs) > turns * waves) ++outputs;
+    if (a.pairs) outputs += outputs & 1;
   }
   const int of_group = DOWN ? steps : (a.inter + outputs - 1) / outputs;
   const int work = groups * of_group;
@@ -361,8 +392,40 @@ __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds
   // A column of the products is a row of the group (zeros past it); with up to 8 rows both
   // parts of h have columns in one product, h's rests those from 8 on.
   const int row = min(kBoth ? c & 7 : c, ROWS - 1);
-  const uint32_t a_at = uint32_t(kRowsAt + kRowBytes * row) + (kBoth && c >= 8 ? 1024u * kOfPlane : 0u);
-  const int x0 = spread(row + (kBoth && c >= 8 ? 8 : 0));
+  const bool low = kBoth && c >= 8;
+  const int x0 = spread(row + (low ? 8 : 0));
+  unsigned char* const rests = ring + D * kStage;
+
+  // Pairs of a step into their parts, a row of the group at once, the upper parts in place, the
+  // lower ones behind the ring.
+  auto part_pairs = [&](unsigned char* st, int rows) {
+    constexpr int kWords = kRowBytes / 256;       // of a lane
+    typedef uint32_t words_t __attribute__((ext_vector_type(kWords)));
+    words_t v[ROWS];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) v[r] = reinterpret_cast<const words_t*>(st + kRowsAt + kRowBytes * r)[lane];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      if (r > 0 && r >= rows) break;
+      words_t high, rest;
+      uint32_t most = 0;
+#pragma unroll
+      for (int q = 0; q < kWords; ++q) {
+        uint32_t h, l;
+        pair_parts(v[r][q], h, l);
+        high[q] = h;
+        rest[q] = l;
+        most = umax(most, v[r][q]);
+      }
+      if (__ballot(most >= kPairEnds)) {
+#pragma unroll
+        for (int q = 0; q < kWords; ++q) rest[q] = v[r][q] >= kPairEnds ? 0u : rest[q];
+      }
+      reinterpret_cast<words_t*>(st + kRowsAt + kRowBytes * r)[lane] = high;
+      // row r's rests as row r + 8 of the columns: spread(r) ^ spread(r + 8) is piece 8
+      *reinterpret_cast<words_t*>(rests + kRowBytes * r + ((4 * kWords * lane) ^ (kBoth ? 128 : 0))) = rest;
+    }
+  };
 
   int stage = 0;
   f32x4_t* red = reinterpret_cast<f32x4_t*>(lds + kLayerRed);
@@ -372,6 +435,7 @@ __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds
       const int from = t.from(outputs), many = size(t);
       f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
       const int n_steps = DOWN ? many : steps;
+      const int rows_of_group = DOWN && PAIRS ? __builtin_amdgcn_readfirstlane(T.first[t.j + 1] - T.first[t.j]) : 0;
       for (int h = 0; h < n_steps; ++h) {
         if (in_turns && wave < kLayerWaves / 2) {
           if (h & 1) __builtin_amdgcn_s_setprio(1);
@@ -379,20 +443,25 @@ __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds
         }
         if (more) wait_copies<(D - 1) * kOps>();
         else wait_copies<0>();
-        const unsigned char* st = ring + stage * kStage;
+        unsigned char* st = ring + stage * kStage;
         u32x4_t w[kParts], b[kParts][4][kReads];
         uint32_t e8[kParts];
 #pragma unroll
         for (int i = 0; i < kParts; ++i) {
           w[i] = *reinterpret_cast<const u32x4_t*>(st + 64 * kParts * c + 16 * ((4 * i + g) ^ (c >> 1 & (kRowPieces - 1))));
           e8[i] = st[kMetaAt + 4 * kParts * c + 4 * i + g];
+        }
+        if constexpr (kRests > 0) part_pairs(st, rows_of_group);
+        // the parts' rows of column c
+        const unsigned char* const upper = st + kRowsAt + kRowBytes * row;
+        const unsigned char* const lower = (kRests ? rests : st + kRowsAt + 1024 * kOfPlane) + kRowBytes * row;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
+        for (int i = 0; i < kParts; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
 #pragma unroll
             for (int p = 0; p < kReads; ++p)
-              b[i][j][p] = *reinterpret_cast<const u32x4_t*>(st + a_at + 1024 * kOfPlane * p + 16 * ((16 * i + 4 * g + j) ^ x0));
-          }
-        }
+              b[i][j][p] = *reinterpret_cast<const u32x4_t*>((p || low ? lower : upper) + 16 * ((16 * i + 4 * g + j) ^ x0));
         wait_reads();                             // ... and is in registers: its stage is free
         if (more) copies(stage);
         stage = stage + 1 == D ? 0 : stage + 1;
@@ -423,18 +492,28 @@ __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds
       } else {
         // gate rows in the lanes with g < 2, the same outputs' up rows 32 lanes on
         const int at = T.first[t.j], rows = T.first[t.j + 1] - at;
+        float v[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float v = silu(acc[e]) * __shfl_xor(acc[e], 32);
-          if (c < rows && g < 2 && 4 * g + e < many) {
-            const uint32_t hi = pack_bf16x2(v, v) & 0xffffu;
-            const int64_t o = int64_t(at + c) * a.inter + from + 4 * g + e;
-            a.h[o] = uint16_t(hi);
-            if (a.parts == 2) {
-              // what the nearest bf16 leaves: 16 bits of v, so that out has its own rounding alone
-              const float rest = __builtin_isfinite(bf16_lo(hi)) ? v - bf16_lo(hi) : 0.f;
-              a.h[o + int64_t(a.t) * a.k * a.inter] = uint16_t(pack_bf16x2(rest, rest));
-            }
+        for (int e = 0; e < 4; ++e) v[e] = silu(acc[e]) * __shfl_xor(acc[e], 32);
+#pragma unroll
+        for (int e = 0; e < 4; e += 2) {
+          if (c >= rows || g >= 2 || 4 * g + e >= many) continue;
+          uint16_t* const h = a.h + int64_t(at + c) * a.inter + from + 4 * g + e;
+          if (a.pairs) {                          // `from` and `many` are even
+            *reinterpret_cast<uint32_t*>(h) = pack_pair(v[e], v[e + 1]);
+            continue;
+          }
+          // the nearest bf16 and what it leaves: 16 bits of v, so that out has its own rounding alone
+          const uint32_t hi = pack_bf16x2(v[e], v[e + 1]);
+          const float r0 = __builtin_isfinite(bf16_lo(hi)) ? v[e] - bf16_lo(hi) : 0.f;
+          const float r1 = __builtin_isfinite(bf16_hi(hi)) ? v[e + 1] - bf16_hi(hi) : 0.f;
+          const uint32_t rest = pack_bf16x2(r0, r1);
+          uint16_t* const low = h + int64_t(a.t) * a.k * a.inter;
+          h[0] = uint16_t(hi);
+          low[0] = uint16_t(rest);
+          if (4 * g + e + 1 < many) {
+            h[1] = uint16_t(hi >> 16);
+            low[1] = uint16_t(rest >> 16);
           }
         }
       }
@@ -463,14 +542,14 @@ __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds
   wait_copies<0>();
 }
 
-template <bool DOWN, int PARTS>
+template <bool DOWN, bool PAIRS>
 __device__ __forceinline__ void stream_any(const MoeLayerArgs& a, unsigned char* lds, LayerTables& T) {
   // with 8 and 16 rows steps of 128 codes: of 256 the ring would hold one or two
   const int kind = __builtin_amdgcn_readfirstlane(T.kind);
-  if (kind == 0) stream<DOWN, PARTS, 2, 256>(a, lds, T);
-  else if (kind == 1) stream<DOWN, PARTS, 4, 256>(a, lds, T);
-  else if (kind == 2) stream<DOWN, PARTS, 8, 128>(a, lds, T);
-  else stream<DOWN, PARTS, 16, 128>(a, lds, T);
+  if (kind == 0) stream<DOWN, PAIRS, 2, 256>(a, lds, T);
+  else if (kind == 1) stream<DOWN, PAIRS, 4, 256>(a, lds, T);
+  else if (kind == 2) stream<DOWN, PAIRS, 8, 128>(a, lds, T);
+  else stream<DOWN, PAIRS, 16, 128>(a, lds, T);
 }
 
 __global__ __launch_bounds__(64 * kLayerWaves) void layer_gate_up_kernel(MoeLayerArgs a) {
@@ -506,10 +585,10 @@ __global__ __launch_bounds__(64 * kLayerWaves) void layer_gate_up_kernel(MoeLaye
     a.weights[tid] = C.weights[tid];
   }
   make_tables(T, C, tokens, pairs, a.k, a.n_experts);
-  stream_any<false, 1>(a, lds, T);
+  stream_any<false, false>(a, lds, T);
 }
 
-template <int PARTS>
+template <bool PAIRS>
 __global__ __launch_bounds__(64 * kLayerWaves) void layer_down_kernel(MoeLayerArgs a) {
   extern __shared__ __attribute__((aligned(1024))) unsigned char lds[];
   LayerTables& T = *reinterpret_cast<LayerTables*>(lds + kLayerTables);
@@ -527,7 +606,7 @@ __global__ __launch_bounds__(64 * kLayerWaves) void layer_down_kernel(MoeLayerAr
   if (e >= 0) atomicOr(&tokens[e], 1u << tid / a.k);
   __syncthreads();
   make_tables(T, C, tokens, pairs, a.k, a.n_experts);
-  stream_any<true, PARTS>(a, lds, T);
+  stream_any<true, PAIRS>(a, lds, T);
 }
 
 }  // namespace
@@ -548,7 +627,7 @@ int launch_moe_layer(const MoeLayerArgs& args, void* stream) {
                         0, a);
   const int err = int(hipGetLastError());
   if (err) return err;
-  hipExtLaunchKernelGGL(a.parts == 2 ? layer_down_kernel<2> : layer_down_kernel<1>, dim3(unsigned(std::min(cus, blocks))),
+  hipExtLaunchKernelGGL(a.pairs ? layer_down_kernel<true> : layer_down_kernel<false>, dim3(unsigned(std::min(cus, blocks))),
                         block, kLayerLds, s, nullptr, static_cast<hipEvent_t>(pe.stop), 0, a);
   return int(hipGetLastError());
 }

@@ -188,17 +188,17 @@ qmm_status qmm_moe_layer(qmm_format f, const void* gate_up, int64_t gate_up_stri
   if (!aligned(logits, dtype == QMM_BF16 ? 2 : 4)) return api_fail(QMM_E_ALIGN, "logits must be aligned to their type");
   if (!aligned(bias, 4) || !aligned(topk, 4) || !aligned(weights, 4))
     return api_fail(QMM_E_ALIGN, "bias, topk and weights must be 4-byte aligned");
-  // half the size, as the call took it first, in whole 16 bytes: h in one part
+  // half the size, as the call took it first, in whole 16 bytes: h in pairs
   const size_t full = qmm_moe_layer_workspace_bytes(t, k, inter);
-  const int parts = ws_bytes >= full ? 2 : 1;
-  if (!ws || ws_bytes < full / 2 || (parts == 1 && ws_bytes % 16))
+  const bool pairs = ws_bytes < full;
+  if (!ws || ws_bytes < full / 2 || (pairs && ws_bytes % 16))
     return api_fail(QMM_E_WORKSPACE, "workspace NULL, or not of qmm_moe_layer_workspace_bytes() or half of it");
   if (!aligned(ws, 16)) return api_fail(QMM_E_ALIGN, "ws must be 16-byte aligned");
   const qmm::MoeLayerArgs a{static_cast<const uint8_t*>(gate_up), gate_up_stride_bytes,
                             static_cast<const uint8_t*>(down), down_stride_bytes, n_experts, int(d), int(inter), x,
                             int(t), logits, dtype == QMM_BF16, ld, score == QMM_SCORE_SIGMOID, bias, n_groups,
                             keep_groups, group_score == QMM_GROUP_TOP2, k, renorm != 0, scale, shared, topk, weights,
-                            out, static_cast<uint16_t*>(ws), parts};
+                            out, static_cast<uint16_t*>(ws), pairs};
   const int err = qmm::launch_moe_layer(a, stream);
   return err ? api_hip_fail(err, "qmm_moe_layer") : QMM_OK;
 }

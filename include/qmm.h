@@ -553,7 +553,7 @@ size_t qmm_moe_layer_workspace_bytes(int64_t t, int32_t k, int64_t inter);
  *   topk, weights   chosen and weighted as qmm_route_topk does: dtype, ld, score, bias,
  *                   n_groups, keep_groups, group_score, k, renorm and scale as there
  *   h[i][j]   = silu(G_e·x_i)·(U_e·x_i), e = topk[i][j], of fp32 sums, kept to 16 bits (in half
- *               the workspace rounded once to bf16)
+ *               the workspace to 2^-11 of the larger of two neighbours, the even one first)
  *   out[i]    = sum_j weights[i][j]·(D_e·h[i][j]) + shared[i], in fp32, rounded once to bf16;
  *               slots of -1 add nothing
  *   gate_up   [n_experts] packed matrices [2·inter, d] (rows [0, inter) the gate G, then the
@@ -562,8 +562,7 @@ size_t qmm_moe_layer_workspace_bytes(int64_t t, int32_t k, int64_t inter);
  *   x bf16[t][d], 16-byte aligned; shared bf16[t][d] or NULL (may be out) and out 8-byte
  *   topk int32[t][k], weights fp32[t][k]: outputs, which the second launch reads
  *   ws        qmm_moe_layer_workspace_bytes(t, k, inter) bytes or more, 16-byte aligned; or fewer, from
- *             half of it (2·t·k·inter) on, in whole 16 bytes: with h in bf16 out's error is up to 1.55
- *             times that of its own rounding, which is all that it has in the full workspace
+ *             half of it (2·t·k·inter) on, in whole 16 bytes
  * Calls that may run at the same time need ws, topk and weights of their own.
  * Limits: t <= 16 and t·k <= 256; d and inter multiples of 32, <= 65536; one matrix's codes
  * below 2 GiB; n_experts, k, n_groups as for qmm_route_topk.  t = 0 is a no-op.

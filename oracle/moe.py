@@ -21,8 +21,11 @@ def two_parts(h):
     return 2.0 ** -16 * h + 2.0 ** -132
 
 
-def one_part(h):
-    return 2.0 ** -8 * h + 2.0 ** -133
+def pairs(h):
+    """Two neighbours as multiples of one unit: 2^-10 of the larger one's binade, or of the next
+    where it rounds there (from 2 - 2^-11 on), at least 2^-126."""
+    most = np.repeat(h.reshape(*h.shape[:-1], -1, 2).max(-1), 2, -1)
+    return 2.0 ** -11 * (1 + 2.0 ** -11) * most + 2.0 ** -127
 
 
 def layer(x, gate_up, down, ids, weights, shared, kept=two_parts):
