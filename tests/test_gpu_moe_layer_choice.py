@@ -50,8 +50,9 @@ def test_choice(ne, groups, t):
                                                     ("softmax", False, True, F32)]):
         k = min([8, 1, 6, 16, 5][n], keep * (ne // groups))
         l = layer(t, ne, groups, score, bias, top2, k, n % 2 == 0, dtype, rng)
-        # sums of a probability and a bias may meet by chance
-        l.check(l.run(), 0.5 if bias else 0.9)
+        # a probability with its bias, or two probabilities of a group, may come near another sum by
+        # chance: such tokens are not compared (one of 8 with 1024 experts in 64 groups)
+        l.check(l.run(), 0.5 if bias or top2 else 0.9)
 
 
 @pytest.mark.parametrize("t", [3, 13])
