@@ -18,10 +18,10 @@
 // copy takes a CU 25 to 30 clocks whatever its size, which counts where a wave has few steps,
 // so a step has as few as possible: with groups of two rows four for 256 codes (steps of 128
 // codes had six: 38.3 and 32.8 us at one token, 174 and 147 at 16, as below), and none past
-// the work.  A lane's 16-byte piece of weights is a block of 32 codes, converted exactly to bf16 for
-// four v_mfma_f32_16x16x32_bf16 with 16 weight rows (A operand) and the group's rows (B
-// operand).  The second kernel's waves' weighted sums meet in LDS in the waves' order: nothing
-// depends on timing.
+// the work.  A lane's 16-byte piece of weights is a block of 32 codes, converted to bf16
+// (exactly up to E8M0 252; values of 2^128 and more are infinite) for four
+// v_mfma_f32_16x16x32_bf16 with 16 weight rows (A operand) and the group's rows (B operand).  The
+// second kernel's waves' weighted sums meet in LDS in the waves' order: nothing depends on timing.
 //
 // h is kept in two bf16 parts: rounded to one, the output's error against 64 bits was up to 1.55
 // times that of its own rounding, now 1.0 (second kernel 48 -> 54 us at 16 tokens, 11.7 -> 11.4

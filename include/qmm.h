@@ -566,6 +566,9 @@ size_t qmm_moe_layer_workspace_bytes(int64_t t, int32_t k, int64_t inter);
  * Calls that may run at the same time need ws, topk and weights of their own.
  * Limits: t <= 16 and t·k <= 256; d and inter multiples of 32, <= 65536; one matrix's codes
  * below 2 GiB; n_experts, k, n_groups as for qmm_route_topk.  t = 0 is a no-op.
+ * The weights are bf16 operands, exact for E8M0 up to 252.  At 253 the codes of magnitude 4 and
+ * 6, at 254 those from 2 on, are infinite: outputs that they take part in are infinite or NaN
+ * (the qmm_mxfp4_* products apply the exponents in the matrix instruction and have no such limit).
  * QMM_AFFINE4_G64 returns QMM_E_UNSUPPORTED.  The order of every sum depends on the shape and
  * on which tokens choose which experts alone. */
 qmm_status qmm_moe_layer(qmm_format f, const void* gate_up, int64_t gate_up_stride_bytes, const void* down,
