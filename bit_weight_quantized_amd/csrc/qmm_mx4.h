@@ -102,6 +102,18 @@ inline Mx4GroupedShape mx4_grouped_shape(const Mx4GemmArgs& a) {
 int launch_mx4_rows(const Mx4GemmArgs& a, void* stream);
 // many rows: LDS tiles of 256 x 256 (large) or 64 x 128
 int launch_mx4_tile(const Mx4GemmArgs& a, bool large, void* stream);
+// Tiles of either kind along the rows and the columns of Y; a grid may have fewer than 2^32 threads
+// along x.  Grouped: no more row tiles than whole tiles of rows and one part tile a segment.
+struct Mx4Tiles {
+  int64_t t, n;
+  bool fit;
+};
+inline Mx4Tiles mx4_tiles(const Mx4GemmArgs& a, bool large) {
+  const int rows = large ? 256 : 64, cols = (large ? 256 : 128) / (a.glu ? 2 : 1), threads = large ? 512 : 256;
+  const int64_t t = a.n_seg ? int64_t(a.m_total) / rows + std::min(a.n_seg, a.m_total) : (a.t + rows - 1) / rows;
+  const int64_t n = (int64_t(a.glu ? a.n / 2 : a.n) + cols - 1) / cols;
+  return {t, n, t * n * threads < (int64_t(1) << 32)};
+}
 // the choice between them, and its launch
 enum class MxKernel { kRows, kTile64, kTile256 };
 inline MxKernel mx4_kernel(const Mx4GemmArgs& a) {
@@ -122,7 +134,7 @@ inline MxKernel mx4_kernel(const Mx4GemmArgs& a) {
     const double t256 = tiles(256, 256), whole = double(int64_t(t256) / 256), rest = t256 - 256 * whole;
     const double large = 3.5 + whole * (7.5 + 0.88 * steps) +
                          (rest > 0 ? 4 + (0.62 + 0.26 * std::max(0.0, rest / 128 - 1)) * steps : 0.0);
-    if (few <= small && few <= large) return MxKernel::kRows;
+    if ((few <= small && few <= large) || !mx4_tiles(a, large < small).fit) return MxKernel::kRows;
     return large < small ? MxKernel::kTile256 : MxKernel::kTile64;
   }
   // The few-row kernel up to 8 rows a segment on average, if none can be long: 64 experts of
@@ -132,7 +144,10 @@ inline MxKernel mx4_kernel(const Mx4GemmArgs& a) {
   // 161; 16 experts of 2048 x 1408, 64 rows each, 128 large tiles, 10.7 and 14.7.
   if (a.max_seg_rows <= kMxRowsMax && a.m_total <= 8 * int64_t(a.n_seg)) return MxKernel::kRows;
   const int64_t tiles = std::max<int64_t>(a.n_seg, a.m_total / 256) * ((int64_t(a.n) + 255) / 256);
-  return a.m_total >= 48 * int64_t(a.n_seg) && tiles >= 160 ? MxKernel::kTile256 : MxKernel::kTile64;
+  const bool large = a.m_total >= 48 * int64_t(a.n_seg) && tiles >= 160;
+  // more tiles than a grid has: the few-row kernel, whose workgroups take turns
+  if (!mx4_tiles(a, large).fit) return MxKernel::kRows;
+  return large ? MxKernel::kTile256 : MxKernel::kTile64;
 }
 int launch_mx4_product(const Mx4GemmArgs& a, void* stream);
 

@@ -412,18 +412,15 @@ int go(const Mx4GemmArgs& a, hipStream_t s) {
   using T = Mx4Tile<TS, WS, WT, WN, GROUPED, GLU>;
   Layout l;
   if (!layout_of(QMM_MXFP4_G32, a.n, a.d, &l)) return int(hipErrorInvalidValue);
-  const int nout = GLU ? a.n / 2 : a.n;
-  const int64_t tiles_n = (int64_t(nout) + T::kOut - 1) / T::kOut;
-  // grouped: no more row tiles than whole tiles of rows and one part tile a segment
-  const int64_t tiles_t = GROUPED ? int64_t(a.m_total) / T::kT + std::min(a.n_seg, a.m_total)
-                                  : (a.t + T::kT - 1) / T::kT;
-  if (tiles_t == 0) return 0;
-  if (tiles_n * tiles_t * 64 * T::kWaves >= (int64_t(1) << 32)) return int(hipErrorInvalidValue);   // the grid's limit
+  static_assert(T::kWaves * 64 == (T::kT == 256 ? 512 : 256) && T::kOut == (T::kT == 256 ? 256 : 128) / (GLU ? 2 : 1), "mx4_tiles");
+  const Mx4Tiles tiles = mx4_tiles(a, T::kT == 256);
+  if (tiles.t == 0) return 0;
+  if (!tiles.fit) return int(hipErrorInvalidValue);
   Mx4TileArgs k{};
   k.place.n = a.n;
   k.place.d = a.d;
   k.place.t = a.t;
-  k.place.tiles_n = int(tiles_n);
+  k.place.tiles_n = int(tiles.n);
   k.place.row_index = a.row_index;
   k.place.seg_expert = a.seg_expert;
   k.place.seg_offsets = a.seg_offsets;
@@ -443,7 +440,7 @@ int go(const Mx4GemmArgs& a, hipStream_t s) {
   k.fit = a.fit;
   k.hq = a.hq;
   k.hs = a.hs;
-  launch_kernel_lds((mx4_tile_kernel<TS, WS, WT, WN, GROUPED, GLU>), dim3(unsigned(tiles_n * tiles_t)),
+  launch_kernel_lds((mx4_tile_kernel<TS, WS, WT, WN, GROUPED, GLU>), dim3(unsigned(tiles.n * tiles.t)),
                     dim3(64 * T::kWaves), size_t(T::kLds), s, k);
   return int(hipGetLastError());
 }
