@@ -30,11 +30,13 @@
 // reads operands (one token, 8 of 256 experts: 31.6 us, 16 of 8 of 64: 153).  One bf16 part takes 29.8
 // and 129 there, at 1.35 to 1.55 times the error.
 //
-// Measured, back to back (the two kernels by themselves): one token, 8 of 256 experts of 3584 x
-// 2048: 30.3 us (18.7 and 11.2; 93.6 MB, 3.1 TB/s: 3 us choice and 1 tables, then 62 MB at 5 TB/s;
-// 3 us before the second one's first copy), 2 tokens, 2 of 8, 1024 x 512: 14.0, 4 tokens, 8 of
-// 128, 2048 x 768: 30.5, 7 tokens, 4 of 60, 2080 x 1056: 32.4, 16 tokens, 8 of 64, 3584 x 2048:
-// 146 (93 and 53; 666 MB, 4.6 TB/s), 8 of 256: 224 (5.3 TB/s).
+// Measured, back to back, logits that favour no expert, the whole workspace (the two kernels by
+// themselves), half of it, and the four calls that the layer joins: one token, 8 of 256 experts of
+// 3584 x 2048: 30.2 us (18.8 and 11.2; 93.6 MB, 3.1 TB/s: 3 us choice and 1 tables, then 62 MB at 5
+// TB/s; 3 us before the second one's first copy), 31.5, 61.2; 2 tokens, 2 of 8, 1024 x 512: 14.0, 14.3,
+// 19.2; 4 tokens, 8 of 128, 2048 x 768: 30.2, 32.4, 37.9; 7 tokens, 4 of 60, 2080 x 1056: 32.2, 35.4,
+// 36.7; 16 tokens, 8 of 64 (57 have a row), 3584 x 2048: 146 (93 and 54; 666 MB, 4.6 TB/s), 154, 143; 8
+// of 256 (102 have one): 227 (5.2 TB/s), 240, 237.
 #include <hip/hip_runtime.h>
 
 #include "qmm_device.h"

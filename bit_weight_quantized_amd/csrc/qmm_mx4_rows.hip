@@ -1,5 +1,5 @@
-// Microscaled 4-bit product for a few activation rows (a decode batch, routed segments):
-// every weight is read once from memory for up to 64 rows.
+// Microscaled 4-bit product for a few activation rows (a decode batch, routed segments): passes of
+// up to 64 rows, 8 or 16 of a segment, each of which reads the weights once.
 //
 //   y[t,n] = Σ_b 2^(Ex[t,b] + Ew[n,b] - 254) · Σ_{k in b} x[t,k]·w[n,k]
 //
@@ -13,9 +13,10 @@
 // a slab (two steps, 16 bytes a row) at a time into slots of their own.  The waves' sums are
 // added in wave order through LDS: nothing depends on timing.
 //
-// Measured: 1 x 13824 x 5120 8.4 us (4.5 TB/s, a part of the weights from the Infinity Cache), 16
-// rows of it 8.9, 47 x 5120 x 13824 11.9, 64 x 4096 x 7168 6.8; SwiGLU 4096 x 3584 of 67 of 128
-// experts with a row or two 94 us (5.5 TB/s).
+// Measured, weights of three matrices in turn, which the Infinity Cache holds, and of over 1.2 GB, from
+// memory: 1 x 13824 x 5120 8.4 and 9.6 us (3.9 TB/s), 16 rows of it 8.8 and 10.3, 47 x 5120 x 13824
+// 11.9 and 17.3, 64 x 4096 x 7168 6.7 and 8.8; SwiGLU 4096 x 3584 of 67 of 128 experts with a row or
+// two 94 us (5.5 TB/s).
 #include <hip/hip_runtime.h>
 
 #include "qmm_fp8_tile.h"

@@ -510,7 +510,7 @@ qmm_status qmm_mxfp4_quant(const qmm_bf16* x, int64_t t, int64_t d, int64_t ldx,
 /* Y = X·Wᵀ with both sides in MXFP4:
  *   y[t][n] = Σ_b 2^(xs[t][b]-127)·2^(E[n][b]-127)·Σ_{k in b} x[t][k]·w[n][k]
  * block sums exact, the sum over the blocks in fp32 in the matrix cores, rounded once to
- * bf16.  A block with the exponent 255 makes its row NaN.  packed: a QMM_MXFP4_G32 blob of
+ * bf16.  A block of x with the exponent 255 makes its row NaN.  packed: a QMM_MXFP4_G32 blob of
  * [n, d]; y: bf16 rows of n at stride ldy (elements, >= n); the bytes between them are left
  * alone.  No workspace; the order of every sum depends on the sizes of the call alone. */
 qmm_status qmm_mxfp4_gemm(const void* packed, int64_t t, int64_t n, int64_t d, const uint8_t* x, const uint8_t* x_scales,
@@ -536,7 +536,10 @@ qmm_status qmm_mxfp4_grouped_gemm(const void* packed_stack, int64_t expert_strid
  *   hq, h_scales   v quantised as qmm_mxfp4_quant does by `rule`, but from fp32, ready to be
  *                  the x of the down projection (n/2 a multiple of 32); NaN rows get
  *                  exponents of 255
- * The other form's pointers are NULL (rule then does not matter without hq). */
+ * The other form's pointers are NULL (rule then does not matter without hq).  silu is within 2^-18 of
+ * its value (of gates from -40 on); which of two forms of its exponential a call takes, as the order of
+ * the sums, depends on n, d, n_seg, m_total and max_seg_rows, so that a row's last bits, and the code of
+ * a value at a midpoint, may differ between calls with other rows beside it. */
 qmm_status qmm_mxfp4_grouped_gemm_swiglu(const void* packed_stack, int64_t expert_stride_bytes, int32_t n_experts,
                                          int64_t n, int64_t d, const uint8_t* x, const uint8_t* x_scales, int64_t t_x,
                                          const int32_t* row_index, const int32_t* seg_expert,
