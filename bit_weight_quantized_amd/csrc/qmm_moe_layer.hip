@@ -210,19 +210,19 @@ __device__ __forceinline__ int spread(int row) { return (row & 7) | ((row >> 3 ^
 
 // Two neighbours of h in 32 bits: whole numbers of 12 bits, the even one's lowest, and the exponent
 // byte, as fp32 has it, of their unit, 2^-10 of the larger one's binade.  0 stands for zeros.
-constexpr uint32_t kPairEnds = 0xFE000000u;       // from here on: pairs with an infinity, NaN
+constexpr uint32_t kPairEnds = 0xF5000000u;       // from here on: pairs with an infinity (what rounds to 2^128 too), NaN
 __device__ __forceinline__ uint32_t pack_pair(float a, float b) {
   const uint32_t most = umax(__float_as_uint(a) & 0x7FFFFFFFu, __float_as_uint(b) & 0x7FFFFFFFu);
   if (most > 0x7F800000u) return 0xFF000000u;     // 0·inf, NaN
-  // the larger one to the next binade where it rounds there; no unit below fp32's smallest normal
-  const uint32_t unit = umax((most + 0x1000u) >> 23, 11u) - 10u;
-  const float per = __uint_as_float((254u - unit) << 23);
-  uint32_t qa = uint32_t(int(__builtin_rintf(a * per))), qb = uint32_t(int(__builtin_rintf(b * per)));
   if (most == 0x7F800000u) {
     // 2^11 - 1 times 2^127 is infinite; a number beside an infinity does not matter
     auto end = [](float v) { return __builtin_isinf(v) ? v > 0.f ? 0x7FFu : 0x801u : 0u; };
-    return kPairEnds | end(b) << 12 | end(a);
+    return 0xFE000000u | end(b) << 12 | end(a);
   }
+  // the larger one to the next binade where it rounds there; no unit below fp32's smallest normal
+  const uint32_t unit = umax((most + 0x1000u) >> 23, 11u) - 10u;
+  const float per = __uint_as_float((254u - unit) << 23);
+  const uint32_t qa = uint32_t(int(__builtin_rintf(a * per))), qb = uint32_t(int(__builtin_rintf(b * per)));
   return unit << 24 | (qb & 0xFFFu) << 12 | (qa & 0xFFFu);
 }
 // The pair as two bf16 parts each, exact: cut to 8 bits, and the rest (0 beside an infinity).
@@ -427,6 +427,7 @@ __device__ __forceinline__ void stream(const MoeLayerArgs& a, unsigned char* lds
       // row r's rests as row r + 8 of the columns: spread(r) ^ spread(r + 8) is piece 8
       *reinterpret_cast<words_t*>(rests + kRowBytes * r + ((4 * kWords * lane) ^ (kBoth ? 128 : 0))) = rest;
     }
+    asm volatile("" : : : "memory");              // before the operands' reads, in the wave's own order
   };
 
   int stage = 0;

@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")
-pytestmark = pytest.mark.gpu
+pytestmark = [pytest.mark.gpu, pytest.mark.filterwarnings("ignore:overflow encountered in exp")]   # silu of -2^40
 
 import bit_weight_quantized_amd as qmm  # noqa: E402
 from oracle import mxfp4  # noqa: E402

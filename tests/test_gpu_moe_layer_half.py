@@ -98,6 +98,25 @@ def test_the_largest_activations():
         assert bool((out[2:] == np.inf).all())                               # 2^128
 
 
+@pytest.mark.parametrize("kind", [Half, Layer])
+def test_numbers_that_round_to_infinity(kind):
+    """h = 2^128 - 2^114, a finite fp32 past bf16's largest: infinite, not NaN, of either sign."""
+    l = kind((2, 2, 1, 64, 32, "softmax", False, 1, 1, False, True, F32, 0, False), 9810)
+    for e, minus in ((0, 0), (1, 8)):
+        c = np.zeros((64, 64), np.int64)
+        c[:32, :2] = 2                                         # gate: x0 + x1
+        c[32:, 2] = 2 + minus                                  # up: x2 or -x2
+        qmm.qmm_pack(M, 64, 64, dev(mxfp4.pack_codes(c)), dev(np.full((64, 2), 127, np.uint8)), None, l.gate_up[e])
+        ones = dev(np.full((64, 16), 0x22, np.uint8))
+        qmm.qmm_pack(M, 64, 32, ones, dev(np.full((64, 1), 27, np.uint8)), None, l.down[e])
+    x = np.zeros((2, 64), np.float32)
+    x[:, 0], x[:, 1], x[:, 2] = 2.0 ** 63 * (2 - 2.0 ** -7), 2.0 ** 63 * (2.0 ** -7 - 2.0 ** -13), 2.0 ** 64
+    l.x = bf16_bits(x)
+    l.logits = np.array([[1.0, -1.0], [-1.0, 1.0]])
+    out = l.run()["out"].float()
+    assert bool((out[0] == np.inf).all()) and bool((out[1] == -np.inf).all())
+
+
 def far_pairs(kind, seed, tokens):
     """A layer whose h is silu(g)·c·2^e with c and e of each output's own, far apart, and whose down
     matrix takes single outputs and sums; shared takes out what bf16 leaves of them."""
